@@ -55,7 +55,7 @@ enum {
 };
 
 /* Element types. */
-enum { IDX_F32 = 0, IDX_BF16 = 1, IDX_FP8_E4M3 = 2 };
+enum { IDX_F32 = 0, IDX_BF16 = 1, IDX_FP8_E4M3 = 2, IDX_F16 = 3 /* attn_shared only */ };
 
 enum { IDX_MAX_SEGMENTS = 64, IDX_MAX_K = 4096 };
 
@@ -414,6 +414,130 @@ idx_status block_positions(const int32_t* blocks, const int32_t* counts, int64_t
 idx_status block_select_static(const float* index_q, const float* index_k, const int32_t* query_pos, int64_t Q,
                                int32_t n_kv, int32_t D, int64_t L, const block_sparse_config* cfg, int32_t* out,
                                int32_t out_width, int32_t* out_count, void* stream);
+
+/* -------------------------------------------------------------- attn_shared
+ * Attention of a decode step over the tokens that the indexer left visible:
+ * B requests with T tokens each attend to a prefix that the whole batch
+ * shares (its keys and values are stored, and read, once) and to their own
+ * private cache behind it, either to every slot or to the slots that a
+ * selection lists (the ids of idx_topk, witness_merge or block_positions).
+ *
+ * With h the KV head of query head hq (Hq / Hkv consecutive query heads share
+ * one), row (b, t, hq) attends to
+ *   prefix positions j < prefix_len[b], and
+ *   private slots s < n(b, t) = len[b, h] - T + t + 1 (token t of the step sits
+ *   in slot len - T + t), all of them or those of its id list;
+ * x = scale q.k, lse = log sum exp(x), out = sum exp(x - lse) v.  A row with no
+ * visible key gets out 0 and lse -inf.  Sums, maxima and scores are fp32; the
+ * weights are rounded to the element type for the product with v.
+ *
+ * mass (optional): running attention weight of every private slot;
+ *   mass[b, m, s] += sum over the tokens and the query heads of mass head m of
+ *   exp(x - lse); mass_heads is n_kv (one sum per KV head) or 1 (over all).
+ *   Each slot's terms are added in a fixed order, so repeated calls agree bit
+ *   for bit.  Slots that no row sees are left alone.
+ *
+ *   q           device [B, T, Hq, D], dtype IDX_BF16 or IDX_F16, D 64 or 128
+ *               contiguous; strides (in elements) for b, t and head.
+ *   k, v        device private caches, strides for b, slot and KV head, S slots
+ *               per request; NULL with S == 0.
+ *   len         device int32, [B] or [B, n_kv] (len_per_head): filled slots,
+ *               this step's T tokens included; 0..S.
+ *   pk, pv      device shared prefix, strides for position and KV head, P
+ *               positions; NULL with P == 0.
+ *   prefix_len  device [B] int32 (0..P), or NULL: all P.
+ *   ids         device [B, T, W] int32, or [B, T, n_kv, W] (ids_per_head), or
+ *               NULL (every slot).  Entries outside 0..n(b, t)-1 (-1 is the
+ *               padding) are ignored; the others of one list are distinct.
+ *   out         device [B, T, Hq, D] of the same type; lse device [B, T, Hq]
+ *               float32 or NULL (natural logarithm); mass device
+ *               [B, mass_heads, S] float32 or NULL.
+ * Base addresses and strides of q, k, v, pk, pv are multiples of 16 bytes.
+ * Lengths out of range count as 0 and set IDX_DEVERR_BAD_ROW.  Memory of
+ * slots that no row of the call sees may hold anything, NaN included; what
+ * some row sees is finite.  Workspace: partial results, and with mass the
+ * private scores (4 bytes per token, query head and slot or id). */
+typedef struct attn_problem {
+  const void* q;
+  int32_t dtype;
+  float scale;
+  int32_t B, T, Hq, n_kv, D;
+  int64_t q_stride_b, q_stride_t, q_stride_h;
+  const void* k;
+  const void* v;
+  int64_t S;
+  int64_t k_stride_b, k_stride_s, k_stride_h;
+  int64_t v_stride_b, v_stride_s, v_stride_h;
+  const int32_t* len;
+  int32_t len_per_head;
+  int32_t ids_per_head;
+  const void* pk;
+  const void* pv;
+  int64_t P;
+  int64_t pk_stride_s, pk_stride_h;
+  int64_t pv_stride_s, pv_stride_h;
+  const int32_t* prefix_len;
+  const int32_t* ids;
+  int64_t W;
+} attn_problem;
+
+size_t attn_shared_workspace_size(const attn_problem* p, int32_t with_mass);
+idx_status attn_shared(const attn_problem* p, void* out, float* lse, float* mass, int32_t mass_heads, void* ws,
+                       size_t ws_bytes, void* stream);
+
+/* -------------------------------------------------------------- cache_evict
+ * Eviction from private caches by accumulated attention weight.  Row (b, m),
+ * m < mass_heads, has len[b, m] filled slots; slot s holds the token at
+ * position pos[b, m, s] (pos NULL: s) with mass mass[b, m, s].  Slots at
+ * positions < n_first or >= cur[b] - n_last rank first (cur NULL: len[b, m]),
+ * the others by mass; the n_keep best by (rank desc, slot asc) stay.  NaN ranks
+ * last, -0 equals +0, and a mass of +inf ranks with the protected slots.
+ *
+ * The rows that stay keep their slot if it is below n_new = min(len, n_keep);
+ * those at or behind it move, in ascending order, to the freed slots below
+ * n_new, in ascending order.  No row is both read and overwritten, so the
+ * planes are compacted in place, and a call that is repeated with the same
+ * len, pos and mass leaves the same result.
+ *
+ *   out_src  device [B, mass_heads, n_keep] int32: the slot that each new slot
+ *            came from, -1 at and behind n_new;
+ *   out_len  device [B, mass_heads] int32 or NULL: n_new (may be len);
+ *   out_pos, out_mass  device [B, mass_heads, out_stride >= n_keep] int32 /
+ *            float32 or NULL: position (-1 behind n_new) and mass (0 behind
+ *            n_new) of each new slot.  They may be pos and mass themselves
+ *            (then out_stride equals stride); in that case the slots from n_new
+ *            to len get -1 and 0 as well.
+ *   planes   host array of n_planes (<= IDX_MAX_PLANES) caches whose rows move
+ *            along: row_bytes bytes per slot and head, byte strides for b, slot
+ *            and head; heads is 1 or any count with mass_heads == 1 (all move
+ *            alike), else mass_heads.  Rows of one plane do not overlap.
+ * mass and pos: device [B, mass_heads, S], row stride `stride` >= S elements.
+ * n_first + n_last <= n_keep, n_keep >= 1, S and n_keep <= 393216.  Lengths out
+ * of range count as 0 and set IDX_DEVERR_BAD_ROW.  No workspace. */
+enum { IDX_MAX_PLANES = 8 };
+typedef struct evict_plane {
+  void* base;
+  int64_t row_bytes;
+  int32_t heads;
+  int32_t reserved;
+  int64_t stride_b, stride_s, stride_h; /* bytes */
+} evict_plane;
+
+typedef struct evict_problem {
+  const float* mass;
+  const int32_t* pos;
+  const int32_t* len;
+  const int32_t* cur;
+  int32_t B, mass_heads;
+  int64_t S, stride;
+  int64_t n_keep;
+  int32_t n_first, n_last;
+  const evict_plane* planes;
+  int32_t n_planes;
+} evict_problem;
+
+idx_status cache_evict(const evict_problem* p, int32_t* out_src, int32_t* out_len, int32_t* out_pos,
+                       float* out_mass, int64_t out_stride, void* stream);
 
 #ifdef __cplusplus
 }

@@ -22,7 +22,8 @@ LIB_PATH = os.path.join(_PKG, "libidx.so")
 IDX_OK = 0
 STATUS_NAMES = {1: "ROWS_MISMATCH", 2: "SEGMENTS_OUT_OF_RANGE", 3: "KEEP_OUT_OF_RANGE", 4: "INVALID_ARG",
                 5: "UNSUPPORTED", 6: "WORKSPACE_TOO_SMALL", 7: "CUDA"}
-IDX_F32, IDX_BF16, IDX_FP8_E4M3 = 0, 1, 2
+IDX_F32, IDX_BF16, IDX_FP8_E4M3, IDX_F16 = 0, 1, 2, 3
+IDX_MAX_PLANES = 8
 IDX_MAX_SEGMENTS, IDX_MAX_K = 64, 4096
 DEVERR_WAIT_TIMEOUT, DEVERR_BAD_ROW, DEVERR_CAPACITY = 1, 2, 4
 
@@ -94,6 +95,34 @@ class block_sparse_config(ctypes.Structure):
                 ("local_blocks", ctypes.c_int32)]
 
 
+class attn_problem(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("scale", ctypes.c_float), ("B", ctypes.c_int32),
+                ("T", ctypes.c_int32), ("Hq", ctypes.c_int32), ("n_kv", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("q_stride_b", ctypes.c_int64), ("q_stride_t", ctypes.c_int64), ("q_stride_h", ctypes.c_int64),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("S", ctypes.c_int64),
+                ("k_stride_b", ctypes.c_int64), ("k_stride_s", ctypes.c_int64), ("k_stride_h", ctypes.c_int64),
+                ("v_stride_b", ctypes.c_int64), ("v_stride_s", ctypes.c_int64), ("v_stride_h", ctypes.c_int64),
+                ("len", ctypes.c_void_p), ("len_per_head", ctypes.c_int32), ("ids_per_head", ctypes.c_int32),
+                ("pk", ctypes.c_void_p), ("pv", ctypes.c_void_p), ("P", ctypes.c_int64),
+                ("pk_stride_s", ctypes.c_int64), ("pk_stride_h", ctypes.c_int64), ("pv_stride_s", ctypes.c_int64),
+                ("pv_stride_h", ctypes.c_int64), ("prefix_len", ctypes.c_void_p), ("ids", ctypes.c_void_p),
+                ("W", ctypes.c_int64)]
+
+
+class evict_plane(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("row_bytes", ctypes.c_int64), ("heads", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("stride_b", ctypes.c_int64), ("stride_s", ctypes.c_int64),
+                ("stride_h", ctypes.c_int64)]
+
+
+class evict_problem(ctypes.Structure):
+    _fields_ = [("mass", ctypes.c_void_p), ("pos", ctypes.c_void_p), ("len", ctypes.c_void_p),
+                ("cur", ctypes.c_void_p), ("B", ctypes.c_int32), ("mass_heads", ctypes.c_int32),
+                ("S", ctypes.c_int64), ("stride", ctypes.c_int64), ("n_keep", ctypes.c_int64),
+                ("n_first", ctypes.c_int32), ("n_last", ctypes.c_int32), ("planes", ctypes.POINTER(evict_plane)),
+                ("n_planes", ctypes.c_int32)]
+
+
 EXPORTS = {
     "idx_last_error_string": (ctypes.c_char_p, []),
     "idx_device_error": (ctypes.c_uint32, []),
@@ -148,6 +177,11 @@ EXPORTS = {
                                              ctypes.c_int32, ctypes.c_int32, ctypes.c_int64,
                                              ctypes.POINTER(block_sparse_config), ctypes.c_void_p, ctypes.c_int32,
                                              ctypes.c_void_p, ctypes.c_void_p]),
+    "attn_shared_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(attn_problem), ctypes.c_int32]),
+    "attn_shared": (ctypes.c_int32, [ctypes.POINTER(attn_problem), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                     ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "cache_evict": (ctypes.c_int32, [ctypes.POINTER(evict_problem), ctypes.c_void_p, ctypes.c_void_p,
+                                     ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]),
 }
 
 _lib = None
@@ -440,3 +474,166 @@ def block_select_static(index_q: torch.Tensor, index_k: torch.Tensor, query_pos:
     _check(lib().block_select_static(_ptr(index_q), _ptr(index_k), _ptr(query_pos), Q, n_kv, D, L,
                                      ctypes.byref(cfg), _ptr(out), out.shape[-1], _ptr(out_count), _stream(stream)))
     return out, out_count
+
+
+_ATTN_DT = {torch.bfloat16: IDX_BF16, torch.float16: IDX_F16}
+
+
+def _need(ok: bool, msg: str) -> None:
+    if not ok:
+        raise ValueError(msg)
+
+
+def _strided(t: torch.Tensor, name: str, shape, dtype):
+    """A strided device tensor whose last dimension is contiguous: its address
+    and the strides of the others (0 where a dimension has one element)."""
+    _need(t.is_cuda, f"{name}: expected a CUDA tensor")
+    _need(t.dtype == dtype, f"{name}: expected {dtype}, got {t.dtype}")
+    _need(tuple(t.shape) == tuple(shape), f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    _need(t.shape[-1] <= 1 or t.stride(-1) == 1, f"{name}: the last dimension must be contiguous")
+    return t.data_ptr(), [0 if n <= 1 else st for n, st in zip(t.shape[:-1], t.stride()[:-1])]
+
+
+def _dense(t: torch.Tensor, name: str, shapes, dtype):
+    """A contiguous device tensor of one of `shapes`."""
+    _need(t.is_cuda, f"{name}: expected a CUDA tensor")
+    _need(t.dtype == dtype, f"{name}: expected {dtype}, got {t.dtype}")
+    _need(tuple(t.shape) in shapes, f"{name}: shape {tuple(t.shape)} is none of {shapes}")
+    _need(t.is_contiguous(), f"{name}: expected a contiguous tensor")
+    return t.data_ptr()
+
+
+@dataclass
+class AttnProblem:
+    """Device tensors of one attn_shared call (see attn_problem in include/idx.h).
+    Caches are indexed [request, slot, KV head, D]; a head-major cache is passed
+    as its transposed view."""
+    q: torch.Tensor                              # [B, T, Hq, D] bfloat16 or float16
+    scale: float
+    k: Optional[torch.Tensor] = None             # [B, S, n_kv, D] private caches
+    v: Optional[torch.Tensor] = None
+    lens: Optional[torch.Tensor] = None          # [B], [B, 1] or [B, n_kv] int32 filled slots
+    pk: Optional[torch.Tensor] = None            # [P, n_kv, D] shared prefix
+    pv: Optional[torch.Tensor] = None
+    prefix_len: Optional[torch.Tensor] = None    # [B] int32
+    ids: Optional[torch.Tensor] = None           # [B, T, W] or [B, T, n_kv, W] int32
+
+    def c(self) -> attn_problem:
+        q = self.q
+        _need(q.dim() == 4, "q: expected [B, T, Hq, D]")
+        _need(q.dtype in _ATTN_DT, f"q: expected bfloat16 or float16, got {q.dtype}")
+        B, T, Hq, D = q.shape
+        some = self.k if self.k is not None else self.pk
+        _need(some is not None, "neither a private cache nor a prefix")
+        _need(some.dim() >= 2, "caches: expected [..., n_kv, D]")
+        n_kv = some.shape[-2]
+        a = attn_problem(dtype=_ATTN_DT[q.dtype], scale=float(self.scale), B=B, T=T, Hq=Hq, n_kv=n_kv, D=D)
+        a.q, (a.q_stride_b, a.q_stride_t, a.q_stride_h) = _strided(q, "q", q.shape, q.dtype)
+        if self.k is not None:
+            _need(self.v is not None and self.lens is not None, "k needs v and lens")
+            _need(self.k.dim() == 4, "k: expected [B, S, n_kv, D]")
+            S = self.k.shape[1]
+            a.S = S
+            a.k, (a.k_stride_b, a.k_stride_s, a.k_stride_h) = _strided(self.k, "k", (B, S, n_kv, D), q.dtype)
+            a.v, (a.v_stride_b, a.v_stride_s, a.v_stride_h) = _strided(self.v, "v", (B, S, n_kv, D), q.dtype)
+            a.len = _dense(self.lens, "lens", ((B,), (B, 1), (B, n_kv)), torch.int32)
+            a.len_per_head = int(self.lens.dim() == 2 and self.lens.shape[1] == n_kv)
+        if self.pk is not None:
+            _need(self.pv is not None and self.pk.dim() == 3, "pk: expected [P, n_kv, D] with pv")
+            P = self.pk.shape[0]
+            a.P = P
+            a.pk, (a.pk_stride_s, a.pk_stride_h) = _strided(self.pk, "pk", (P, n_kv, D), q.dtype)
+            a.pv, (a.pv_stride_s, a.pv_stride_h) = _strided(self.pv, "pv", (P, n_kv, D), q.dtype)
+            if self.prefix_len is not None:
+                a.prefix_len = _dense(self.prefix_len, "prefix_len", ((B,),), torch.int32)
+        if self.ids is not None:
+            W = self.ids.shape[-1]
+            a.W = W
+            a.ids = _dense(self.ids, "ids", ((B, T, W), (B, T, n_kv, W)), torch.int32)
+            a.ids_per_head = int(self.ids.dim() == 4)
+        return a
+
+
+def attn_shared_workspace_size(p: AttnProblem, mass: bool = True) -> int:
+    cp = p.c()
+    return int(lib().attn_shared_workspace_size(ctypes.byref(cp), int(mass)))
+
+
+def attn_shared(p: AttnProblem, out: torch.Tensor, lse: Optional[torch.Tensor], mass: Optional[torch.Tensor],
+                ws: torch.Tensor, stream=None):
+    """out [B, T, Hq, D]; lse [B, T, Hq] float32 or None; mass [B, n_kv or 1, S]
+    float32 (added to) or None."""
+    cp = p.c()
+    B, T, Hq, D = p.q.shape
+    rows = (B, T, Hq)
+    po = _dense(out, "out", (rows + (D,),), p.q.dtype)
+    pl = None if lse is None else _dense(lse, "lse", (rows,), torch.float32)
+    pm, heads = None, 1
+    if mass is not None:
+        _need(p.k is not None, "mass: there is no private cache")
+        pm = _dense(mass, "mass", ((B, 1, cp.S), (B, cp.n_kv, cp.S)), torch.float32)
+        heads = mass.shape[1]
+    _check(lib().attn_shared(ctypes.byref(cp), po, pl, pm, heads, _ptr(ws), ws.numel() * ws.element_size(),
+                             _stream(stream)))
+    return out, lse, mass
+
+
+@dataclass
+class EvictProblem:
+    """Device tensors of one cache_evict call (see evict_problem in include/idx.h).
+    planes are indexed [B, S, heads, row] or [B, S, row]; they are compacted in
+    place."""
+    mass: torch.Tensor                           # [B, mass_heads, S] float32, rows may be strided
+    lens: torch.Tensor                           # [B, mass_heads] int32
+    n_keep: int
+    n_first: int = 0
+    n_last: int = 0
+    pos: Optional[torch.Tensor] = None           # [B, mass_heads, S] int32
+    cur: Optional[torch.Tensor] = None           # [B] int32
+    planes: tuple = ()
+
+    def c(self) -> evict_problem:
+        _need(self.mass.dim() == 3, "mass: expected [B, mass_heads, S]")
+        B, Hm, S = self.mass.shape
+        e = evict_problem(B=B, mass_heads=Hm, S=S, stride=S, n_keep=int(self.n_keep), n_first=int(self.n_first),
+                          n_last=int(self.n_last))
+        e.mass = _dense(self.mass, "mass", ((B, Hm, S),), torch.float32)
+        e.len = _dense(self.lens, "lens", ((B, Hm),), torch.int32)
+        if self.pos is not None:
+            e.pos = _dense(self.pos, "pos", ((B, Hm, S),), torch.int32)
+        if self.cur is not None:
+            e.cur = _dense(self.cur, "cur", ((B,),), torch.int32)
+        n = len(self.planes)
+        _need(n <= IDX_MAX_PLANES, f"planes: at most {IDX_MAX_PLANES}")
+        arr = (evict_plane * max(n, 1))()
+        for i, t in enumerate(self.planes):
+            _need(t.dim() in (3, 4) and t.shape[0] == B and t.shape[1] == S,
+                  f"planes[{i}]: expected [B, S, heads, row] or [B, S, row], got {tuple(t.shape)}")
+            heads = t.shape[2] if t.dim() == 4 else 1
+            _need(Hm == 1 or heads == Hm, f"planes[{i}]: {heads} heads for {Hm} mass heads")
+            size = t.element_size()
+            ptr, st = _strided(t, f"planes[{i}]", t.shape, t.dtype)
+            arr[i] = evict_plane(ptr, t.shape[-1] * size, heads, 0, st[0] * size, st[1] * size,
+                                 st[2] * size if t.dim() == 4 else 0)
+        e.planes, e.n_planes = arr, n
+        return e
+
+
+def cache_evict(p: EvictProblem, out_src: torch.Tensor, out_len: Optional[torch.Tensor] = None,
+                out_pos: Optional[torch.Tensor] = None, out_mass: Optional[torch.Tensor] = None, stream=None):
+    """out_src [B, mass_heads, n_keep] int32; out_len [B, mass_heads] int32;
+    out_pos / out_mass [B, mass_heads, n_keep], or the problem's pos / mass
+    themselves."""
+    ce = p.c()
+    B, Hm, S = p.mass.shape
+    K = int(p.n_keep)
+    ps = _dense(out_src, "out_src", ((B, Hm, K),), torch.int32)
+    pl = None if out_len is None else _dense(out_len, "out_len", ((B, Hm),), torch.int32)
+    widths = {t.shape[-1] for t in (out_pos, out_mass) if t is not None}
+    _need(len(widths) <= 1, "out_pos and out_mass: row strides differ")
+    ld = widths.pop() if widths else K
+    _need(ld >= K, "out_pos and out_mass: rows shorter than n_keep")
+    pp = None if out_pos is None else _dense(out_pos, "out_pos", ((B, Hm, ld),), torch.int32)
+    pm = None if out_mass is None else _dense(out_mass, "out_mass", ((B, Hm, ld),), torch.float32)
+    _check(lib().cache_evict(ctypes.byref(ce), ps, pl, pp, pm, ld, _stream(stream)))
+    return out_src, out_len, out_pos, out_mass

@@ -3,6 +3,7 @@
 #include <atomic>
 #include <cstdarg>
 #include <cstdio>
+#include <initializer_list>
 #include <mutex>
 #include <vector>
 #include <cstring>
@@ -98,6 +99,43 @@ static idx_status check_problem(const idx_problem* p) {
   if (!p->key_off && p->max_key_len > p->n_keys)
     return fail(IDX_ERR_INVALID_ARG, "shared keys: max_key_len %d exceeds n_keys %lld", p->max_key_len,
                 (long long)p->n_keys);
+  return IDX_OK;
+}
+
+static bool aligned16(const void* base, std::initializer_list<int64_t> strides) {
+  if ((uintptr_t)base & 15) return false;
+  for (int64_t s : strides)
+    if (s & 7) return false;  // 2-byte elements
+  return true;
+}
+
+static idx_status check_attn(const attn_problem* p) {
+  if (!p) return fail(IDX_ERR_INVALID_ARG, "problem is NULL");
+  if (p->B < 0 || p->T < 1 || p->Hq < 1 || p->n_kv < 1 || p->S < 0 || p->P < 0 || p->W < 0)
+    return fail(IDX_ERR_INVALID_ARG, "negative or zero size (B=%d T=%d Hq=%d n_kv=%d S=%lld P=%lld W=%lld)", p->B,
+                p->T, p->Hq, p->n_kv, (long long)p->S, (long long)p->P, (long long)p->W);
+  if (p->Hq % p->n_kv) return fail(IDX_ERR_INVALID_ARG, "Hq=%d is no multiple of n_kv=%d", p->Hq, p->n_kv);
+  if (p->dtype != IDX_BF16 && p->dtype != IDX_F16)
+    return fail(IDX_ERR_UNSUPPORTED, "dtype %d (IDX_BF16 or IDX_F16)", p->dtype);
+  if (p->D != 64 && p->D != 128) return fail(IDX_ERR_UNSUPPORTED, "D=%d (64 or 128)", p->D);
+  // bounds that keep grids, row counts and key indices inside 32 bits
+  if (p->S > (1 << 30) || p->P > (1 << 30) || p->W > (1 << 30) ||
+      (int64_t)p->B * p->T > ((int64_t)1 << 30) / p->Hq || (int64_t)p->T * p->Hq > (1 << 20))
+    return fail(IDX_ERR_UNSUPPORTED, "problem too large (B=%d T=%d Hq=%d S=%lld P=%lld W=%lld)", p->B, p->T, p->Hq,
+                (long long)p->S, (long long)p->P, (long long)p->W);
+  if (!(p->scale == p->scale) || p->scale - p->scale != 0.f) return fail(IDX_ERR_INVALID_ARG, "scale is not finite");
+  if (p->B == 0) return IDX_OK;
+  if (!p->q) return fail(IDX_ERR_INVALID_ARG, "q is NULL");
+  if (p->S > 0 && (!p->k || !p->v || !p->len)) return fail(IDX_ERR_INVALID_ARG, "S > 0 needs k, v and len");
+  if (p->P > 0 && (!p->pk || !p->pv)) return fail(IDX_ERR_INVALID_ARG, "P > 0 needs pk and pv");
+  if (!p->ids && (p->W || p->ids_per_head)) return fail(IDX_ERR_INVALID_ARG, "W or ids_per_head without ids");
+  if (p->ids && p->S == 0) return fail(IDX_ERR_INVALID_ARG, "ids without a private cache");
+  if (!aligned16(p->q, {p->q_stride_b, p->q_stride_t, p->q_stride_h}) ||
+      (p->S > 0 && (!aligned16(p->k, {p->k_stride_b, p->k_stride_s, p->k_stride_h}) ||
+                    !aligned16(p->v, {p->v_stride_b, p->v_stride_s, p->v_stride_h}))) ||
+      (p->P > 0 && (!aligned16(p->pk, {p->pk_stride_s, p->pk_stride_h}) ||
+                    !aligned16(p->pv, {p->pv_stride_s, p->pv_stride_h}))))
+    return fail(IDX_ERR_INVALID_ARG, "q, k, v, pk and pv need 16-byte aligned bases and strides");
   return IDX_OK;
 }
 
@@ -363,6 +401,66 @@ idx_status block_positions(const int32_t* blocks, const int32_t* counts, int64_t
   return cuda_status(launch_block_positions(blocks, counts, Q * n_kv, W, query_pos, n_kv, L, block_size, out,
                                             out_width, out_count, (cudaStream_t)stream),
                      "block_positions");
+}
+
+size_t attn_shared_workspace_size(const attn_problem* p, int32_t with_mass) {
+  if (!p || p->B <= 0 || check_attn(p) != IDX_OK) return 0;
+  return attn_shared_ws(*p, with_mass != 0 && p->S > 0);
+}
+
+idx_status attn_shared(const attn_problem* p, void* out, float* lse, float* mass, int32_t mass_heads, void* ws,
+                       size_t ws_bytes, void* stream) {
+  idx_status st = check_attn(p);
+  if (st) return st;
+  if (mass && mass_heads != 1 && mass_heads != p->n_kv)
+    return fail(IDX_ERR_INVALID_ARG, "mass_heads=%d is neither 1 nor n_kv=%d", mass_heads, p->n_kv);
+  if (p->B == 0) return IDX_OK;
+  if (!out) return fail(IDX_ERR_INVALID_ARG, "out is NULL");
+  if (p->S == 0) mass = nullptr;
+  if (ws_bytes < attn_shared_ws(*p, mass != nullptr)) return fail(IDX_ERR_WORKSPACE_TOO_SMALL, "workspace too small");
+  if (!ws) return fail(IDX_ERR_INVALID_ARG, "workspace is NULL");
+  return cuda_status(launch_attn_shared(*p, out, lse, mass, mass ? mass_heads : 1, ws, (cudaStream_t)stream),
+                     "attn_shared");
+}
+
+idx_status cache_evict(const evict_problem* p, int32_t* out_src, int32_t* out_len, int32_t* out_pos, float* out_mass,
+                       int64_t out_stride, void* stream) {
+  if (!p) return fail(IDX_ERR_INVALID_ARG, "problem is NULL");
+  if (p->B < 0 || p->mass_heads < 1 || p->S < 0 || p->stride < p->S || p->n_keep < 1 || p->n_first < 0 ||
+      p->n_last < 0 || p->n_planes < 0)
+    return fail(IDX_ERR_INVALID_ARG, "bad size (B=%d mass_heads=%d S=%lld stride=%lld n_keep=%lld n_first=%d n_last=%d)",
+                p->B, p->mass_heads, (long long)p->S, (long long)p->stride, (long long)p->n_keep, p->n_first,
+                p->n_last);
+  if ((int64_t)p->n_first + p->n_last > p->n_keep)
+    return fail(IDX_ERR_INVALID_ARG, "n_first + n_last = %lld exceeds n_keep = %lld",
+                (long long)p->n_first + p->n_last, (long long)p->n_keep);
+  if (p->S > evict_max_slots() || p->n_keep > evict_max_slots())
+    return fail(IDX_ERR_UNSUPPORTED, "S=%lld, n_keep=%lld: at most %lld slots", (long long)p->S, (long long)p->n_keep,
+                (long long)evict_max_slots());
+  if ((int64_t)p->B * p->mass_heads > (1 << 20))
+    return fail(IDX_ERR_UNSUPPORTED, "B * mass_heads above 2^20");
+  if (p->n_planes > IDX_MAX_PLANES)
+    return fail(IDX_ERR_INVALID_ARG, "n_planes=%d above %d", p->n_planes, IDX_MAX_PLANES);
+  if (p->n_planes > 0 && !p->planes) return fail(IDX_ERR_INVALID_ARG, "planes is NULL");
+  int64_t heads = 0;
+  for (int i = 0; i < p->n_planes; i++) {
+    const evict_plane& q = p->planes[i];
+    if (q.heads < 1 || q.row_bytes < 0 || (p->mass_heads > 1 && q.heads != p->mass_heads))
+      return fail(IDX_ERR_INVALID_ARG, "plane %d: heads=%d for mass_heads=%d, row_bytes=%lld", i, q.heads,
+                  p->mass_heads, (long long)q.row_bytes);
+    if (q.row_bytes > (1 << 24)) return fail(IDX_ERR_UNSUPPORTED, "plane %d: rows above 2^24 bytes", i);
+    if (!q.base && p->B > 0 && p->S > 0 && q.row_bytes > 0) return fail(IDX_ERR_INVALID_ARG, "plane %d is NULL", i);
+    heads += p->mass_heads == 1 ? q.heads : 1;
+  }
+  if (heads > 65535) return fail(IDX_ERR_UNSUPPORTED, "planes: %lld heads in all, above 65535", (long long)heads);
+  if ((out_pos || out_mass) && out_stride < p->n_keep)
+    return fail(IDX_ERR_INVALID_ARG, "out_stride=%lld below n_keep=%lld", (long long)out_stride, (long long)p->n_keep);
+  if (((out_mass && out_mass == p->mass) || (out_pos && out_pos == p->pos)) && out_stride != p->stride)
+    return fail(IDX_ERR_INVALID_ARG, "outputs in place need out_stride == stride");
+  if (p->B == 0) return IDX_OK;
+  if (!p->len || !out_src || (p->S > 0 && !p->mass)) return fail(IDX_ERR_INVALID_ARG, "NULL pointer");
+  return cuda_status(launch_evict(*p, out_src, out_len, out_pos, out_mass, out_stride, (cudaStream_t)stream),
+                     "cache_evict");
 }
 
 }  // extern "C"

@@ -1,0 +1,64 @@
+// Attention of a decode step over a shared prefix and private caches: what its
+// kernels have in common (arguments, partial results, row limits).
+//
+// A row is (request b, token t, query head hq).  Its softmax is computed in
+// pieces: each (part of the prefix or of the private cache) leaves the
+// unnormalised sum  o = sum 2^(y - m) v  with y = log2(e) scale q.k, its
+// maximum m and its sum l = sum 2^(y - m), all fp32; the finish kernel joins a
+// row's pieces:  M = max m_i,  out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "internal.h"
+
+namespace idx {
+
+struct AttnArgs {
+  attn_problem p;
+  float scale_log2;    // scale * log2(e)
+  int G;               // query heads of one KV head
+  int parts_prefix;    // pieces of a row from the prefix, then from the private cache
+  int parts_private;
+  int64_t chunk_prefix, chunk_private;  // keys of a piece (private: of S or W; shorter rows have shorter pieces)
+  float* po;           // [rows, parts, D] unnormalised sums, rows = B*T*Hq
+  float2* pml;         // [rows, parts] (m, l); l == 0: the piece is empty and po is not written
+  float* sc;           // [rows, sc_ld] private scores y, or NULL
+  int64_t sc_ld;
+  void* out;
+  float* lse;
+  float* mass;
+  int mass_heads;
+};
+
+// Private slots that token t of request b sees under KV head h.
+__device__ __forceinline__ int attn_len(const attn_problem& p, int b, int h) {
+  if (!p.len) return 0;
+  int n = p.len[p.len_per_head ? (int64_t)b * p.n_kv + h : b];
+  if (n < 0 || n > p.S) {
+    atomicOr(&g_device_error, DEVERR_BAD_ROW);
+    n = 0;
+  }
+  return n;
+}
+__device__ __forceinline__ int64_t attn_prefix_len(const attn_problem& p, int b) {
+  if (!p.prefix_len) return p.P;
+  int n = p.prefix_len[b];
+  if (n < 0 || n > p.P) {
+    atomicOr(&g_device_error, DEVERR_BAD_ROW);
+    n = 0;
+  }
+  return n;
+}
+
+__device__ __forceinline__ float attn_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+cudaError_t launch_attn_stream(const AttnArgs& a, bool prefix, cudaStream_t st);
+cudaError_t launch_attn_finish(const AttnArgs& a, cudaStream_t st);
+
+}  // namespace idx

@@ -1,0 +1,97 @@
+"""The operators of one sparse-attention decode step, used together.
+
+`DecodeCache` holds the private caches of a batch of requests that share a
+prefix: keys, values and index keys by slot, each slot's position and running
+attention mass.  A step appends the new tokens, lets the indexer choose slots
+(idx_topk, covered by segment witnesses), attends to the prefix and the chosen
+slots (attn_shared, which adds the weights to the masses), and trims the caches
+to their budget by mass (cache_evict, which moves keys, values and index keys
+alike).  Everything is allocated once and enqueued on the current stream.
+"""
+from __future__ import annotations
+
+from typing import Optional
+
+import torch
+
+from . import binding as B
+
+
+class DecodeCache:
+    def __init__(self, requests: int, slots: int, q_heads: int, kv_heads: int, dim: int, index_dim: int, top_k: int,
+                 prefix_k: Optional[torch.Tensor] = None, prefix_v: Optional[torch.Tensor] = None,
+                 dtype=torch.bfloat16, device="cuda"):
+        z = lambda *s, dt=dtype: torch.zeros(s, dtype=dt, device=device)  # noqa: E731
+        self.k, self.v = z(requests, slots, kv_heads, dim), z(requests, slots, kv_heads, dim)
+        self.index_k = z(requests, slots, index_dim)
+        self.lens = z(requests, 1, dt=torch.int32)
+        self.pos = torch.full((requests, 1, slots), -1, dtype=torch.int32, device=device)
+        self.mass = z(requests, 1, slots, dt=torch.float32)
+        self.cur = z(requests, dt=torch.int32)            # positions seen so far
+        self.prefix_k, self.prefix_v = prefix_k, prefix_v
+        self.top_k = top_k
+        self.ids = z(requests, top_k, dt=torch.int32)
+        self.out = z(requests, 1, q_heads, dim)
+        self.key_off = torch.arange(requests, dtype=torch.int64, device=device) * slots
+        self.rows = torch.arange(requests, device=device)
+        self.ws: Optional[torch.Tensor] = None
+
+    def append(self, k: torch.Tensor, v: torch.Tensor, index_k: torch.Tensor) -> None:
+        """One token of every request: k, v [B, kv_heads, dim], index_k [B, index_dim]."""
+        at = self.lens[:, 0].long()
+        self.k[self.rows, at], self.v[self.rows, at], self.index_k[self.rows, at] = k, v, index_k
+        self.pos[self.rows, 0, at] = self.cur
+        self.lens += 1
+        self.cur += 1
+
+    def step(self, q: torch.Tensor, index_q: torch.Tensor, index_w: torch.Tensor, segments: int = 16) -> torch.Tensor:
+        """q [B, 1, q_heads, dim]; index_q [B, H, index_dim], index_w [B, H] of the
+        indexer.  Returns the attention output; its buffer is reused."""
+        requests, slots = self.index_k.shape[:2]
+        lens = self.lens.view(-1)
+        p = B.Problem(index_q, index_w, self.index_k.view(requests * slots, -1), lens, slots, self.key_off)
+        a = B.AttnProblem(q, q.shape[-1] ** -0.5, self.k, self.v, self.lens, self.prefix_k, self.prefix_v,
+                          ids=self.ids.view(requests, 1, -1))
+        need = max(B.idx_topk_workspace_size(p, self.top_k), B.attn_shared_workspace_size(a, True))
+        if self.ws is None or self.ws.numel() < need:
+            self.ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+        B.idx_topk(p, self.top_k, self.ids, None, self.ws)
+        B.witness_merge(self.ids, lens, max(self.top_k - segments, 0), segments, segments)
+        B.attn_shared(a, self.out, None, self.mass, self.ws)
+        return self.out
+
+    def trim(self, n_keep: int, n_first: int, n_last: int) -> None:
+        """Evicts every request down to n_keep slots."""
+        p = B.EvictProblem(self.mass, self.lens, n_keep, n_first, n_last, self.pos, self.cur,
+                           (self.k, self.v, self.index_k))
+        src = torch.empty((self.lens.shape[0], 1, n_keep), dtype=torch.int32, device=self.mass.device)
+        B.cache_evict(p, src, self.lens, self.pos, self.mass)
+
+
+def decode_step_example(seed: int = 0, requests: int = 8, prefix: int = 1000, slots: int = 2100, K: int = 256,
+                        n_keep: int = 2000, q_heads: int = 32, kv_heads: int = 4, dim: int = 128,
+                        index_heads: int = 16) -> dict:
+    """Fills the caches, runs a few decode steps with random tokens and trims."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rn = lambda *s: torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    c = DecodeCache(requests, slots, q_heads, kv_heads, dim, 128, K, rn(prefix, kv_heads, dim),
+                    rn(prefix, kv_heads, dim))
+    fill = slots - 4
+    c.k[:, :fill], c.v[:, :fill] = rn(requests, fill, kv_heads, dim), rn(requests, fill, kv_heads, dim)
+    c.index_k[:, :fill] = rn(requests, fill, 128)
+    c.lens += fill
+    c.cur += fill
+    c.pos[:, 0, :fill] = torch.arange(fill, device="cuda", dtype=torch.int32)
+    finite = True
+    for _ in range(4):
+        c.append(rn(requests, kv_heads, dim), rn(requests, kv_heads, dim), rn(requests, 128))
+        out = c.step(rn(requests, 1, q_heads, dim), rn(requests, index_heads, 128),
+                     torch.rand((requests, index_heads), generator=g, device="cuda"))
+        finite &= bool(torch.isfinite(out).all())
+    c.trim(n_keep, 4, n_keep // 8)
+    return {"len_after": c.lens.view(-1).tolist(), "finite": finite, "mass": c.mass[..., :n_keep], "pos": c.pos}
+
+
+if __name__ == "__main__":
+    got = decode_step_example()
+    print("slots kept per request:", got["len_after"], "finite outputs:", got["finite"])
