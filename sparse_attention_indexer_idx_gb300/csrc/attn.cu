@@ -1,6 +1,6 @@
 // Attention of a decode step: the plan of a call (which kernel takes which
 // part, how many pieces) and its workspace.  Host only.
-#include "attn.cuh"
+#include "attn_tc.cuh"
 
 #include <algorithm>
 
@@ -13,19 +13,53 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // Keys of the private part that a row can see at most.
 int64_t private_keys(const attn_problem& p) { return p.S == 0 ? 0 : p.ids ? p.W : p.S; }
 
-// How many pieces each part is cut into: pieces of one length everywhere, short
-// enough to give every SM two blocks, not below kMinChunk keys (a block's start
-// and the join of its warps cost about as much as 128 keys do).
+// Rows of a KV head that the streaming kernel takes in one pass over the keys.
+constexpr int64_t kStreamRows = 32;
+
+// Whether the shared prefix goes to the tensor-core kernel.  TMA reads it
+// there, so its strides have to be ones that a tensor map can hold.
+bool prefix_on_tc(const attn_problem& p) {
+  auto legal = [](int64_t n, int64_t stride) { return n <= 1 || (stride > 0 && stride < ((int64_t)1 << 38)); };
+  return p.P > 0 && (int64_t)p.B * p.T * (p.Hq / p.n_kv) > kStreamRows && legal(p.P, p.pk_stride_s) &&
+         legal(p.P, p.pv_stride_s) && legal(p.n_kv, p.pk_stride_h) && legal(p.n_kv, p.pv_stride_h);
+}
+
+// The tensor-core kernel's grid.  A whole number of pieces per (KV head, row
+// tile pair) is taken if it leaves at most a tenth of the SMs idle; otherwise
+// the key tiles are cut evenly, and a piece can end up on two blocks.
+AttnTcArgs plan_tc(const AttnArgs& a) {
+  const attn_problem& p = a.p;
+  AttnTcArgs t{};
+  t.a = a;
+  const int64_t tiles = ceil_div(p.P, 128), n = sm_count();
+  t.row_tiles = (int)ceil_div((int64_t)p.B * p.T * a.G, 256);
+  const int64_t items = (int64_t)p.n_kv * t.row_tiles;
+  const int64_t whole = std::min(tiles, n / items);
+  t.whole_cells = whole > 0 && (whole == tiles || items * whole * 10 >= n * 9);
+  t.cells_k = (int)(t.whole_cells ? whole : std::min(tiles, ceil_div(n, items)));
+  t.blocks = (int)(t.whole_cells ? items * whole : std::min(n, items * tiles));
+  return t;
+}
+
+// How many pieces each part is cut into.  The streaming kernel's pieces have
+// one length everywhere, short enough to give every SM two blocks, not below
+// kMinChunk keys (a block's start and the join of its warps cost about as much
+// as 128 keys do).
 void plan_parts(AttnArgs& a) {
   const attn_problem& p = a.p;
   constexpr int64_t kMinChunk = 128;
   auto tiles = [](int64_t rows) { return ceil_div(rows, rows <= 16 ? 16 : 32); };
-  const int64_t pre = (int64_t)p.n_kv * tiles((int64_t)p.B * p.T * a.G);
+  const bool tc = prefix_on_tc(p);
+  const int64_t pre = tc ? 0 : (int64_t)p.n_kv * tiles((int64_t)p.B * p.T * a.G);
   const int64_t prv = (int64_t)p.B * p.n_kv * (p.ids ? p.T * tiles(a.G) : tiles((int64_t)p.T * a.G));
   const int64_t keys = private_keys(p);
   const int64_t blocks = 2 * (int64_t)sm_count();
   const int64_t chunk = std::max(kMinChunk, ceil_div(pre * p.P + prv * keys, blocks));
   a.parts_prefix = (int)ceil_div(p.P, chunk);
+  if (tc) {
+    const AttnTcArgs t = plan_tc(a);
+    a.parts_prefix = t.cells_k * (t.whole_cells ? 1 : 2);
+  }
   a.parts_private = (int)ceil_div(keys, chunk);
 }
 
@@ -76,7 +110,10 @@ cudaError_t launch_attn_shared(const attn_problem& p, void* out, float* lse, flo
   a.mass = mass;
   a.mass_heads = mass_heads;
   cudaError_t e = cudaSuccess;
-  if (a.parts_prefix) e = launch_attn_stream(a, true, st);
+  if (prefix_on_tc(p))
+    e = launch_attn_tc(plan_tc(a), st);
+  else if (a.parts_prefix)
+    e = launch_attn_stream(a, true, st);
   if (e == cudaSuccess && a.parts_private) e = launch_attn_stream(a, false, st);
   if (e == cudaSuccess) e = launch_attn_finish(a, st);
   return e;

@@ -21,7 +21,6 @@ struct AttnArgs {
   int G;               // query heads of one KV head
   int parts_prefix;    // pieces of a row from the prefix, then from the private cache
   int parts_private;
-  int64_t chunk_prefix, chunk_private;  // keys of a piece (private: of S or W; shorter rows have shorter pieces)
   float* po;           // [rows, parts, D] unnormalised sums, rows = B*T*Hq
   float2* pml;         // [rows, parts] (m, l); l == 0: the piece is empty and po is not written
   float* sc;           // [rows, sc_ld] private scores y, or NULL

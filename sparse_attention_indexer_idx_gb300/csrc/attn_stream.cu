@@ -428,7 +428,8 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
   const attn_problem& p = a.p;
   const int smem = C::RING + (GATHER ? C::SLOTS : 0) + 16 * MT * D * 2;
   auto kern = attn_stream_kernel<D, MT, BF16, GATHER, PREFIX>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static KernelReady ready;
+  cudaError_t e = ready.once([&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
   if (e != cudaSuccess) return e;
   const int64_t rows = PREFIX ? (int64_t)p.B * p.T * a.G : GATHER ? a.G : (int64_t)p.T * a.G;
   const int tiles = (int)((rows + 16 * MT - 1) / (16 * MT));

@@ -1,0 +1,495 @@
+// Attention of many rows over the shared prefix on the 5th-generation tensor
+// cores: every request's query heads read the same keys and values, so the
+// rows of a KV head form the M axis of one long matrix problem.
+//
+// A block holds two tiles of 128 rows (TMEM lane = row) and walks tiles of 128
+// keys.  Per key tile and row tile:  S = Q K^T (fp32 in TMEM, both operands in
+// shared memory);  one warpgroup, a thread per row, takes the row's 128 scores
+// into registers, forms the weights 2^(y - m) and writes them back over S as
+// 16-bit operands;  O += P V with P read from TMEM.  The two row tiles
+// alternate: while one's weights are formed, the other's products run.
+//
+// The reference m of a row moves only when a score passes it by more than 2^8
+// (weights up to 2^8 lose nothing in fp32 sums or in the 16-bit operands), so
+// the accumulator in TMEM is almost never rescaled.
+//
+// Work is (KV head, piece of the keys, pair of row tiles, key tile), row tiles
+// inside pieces: blocks that run together read the same keys, which then come
+// from L2.  The line of key tiles is cut evenly over the SMs, or piece by piece
+// where the pieces fill them; a block leaves one partial result per piece it
+// touched and the finish kernel joins them.
+//
+// Warp roles: warp 0 TMA producer, warp 1 MMA issuer, warp 2 TMEM allocation,
+// warps 4..7 and 8..11 the two row tiles.  Waits are bounded as everywhere in
+// the library; on a timeout the roles stop and drain what they issued.
+#include "attn_tc.cuh"
+
+namespace idx {
+
+namespace {
+
+constexpr int kThreadsTc = 384;
+// After setmaxnreg: warps 0..3, and the softmax warps, which hold a row's 128
+// scores.  4 * 72 + 8 * 216 = 12 * 168, the launch's registers.
+constexpr int kRegsIssue = 72, kRegsSoftmax = 216;
+
+template <int D>
+struct TcCfg {
+  static constexpr int TILE = 128 * D * 2;            // 128 rows or keys
+  static constexpr int NS = D == 128 ? 5 : 8;         // ring of key and value tiles
+  static constexpr int SMEM = 2 * TILE + NS * TILE + 1024;
+};
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, uint64_t* bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+          dst),
+      "l"(tmap), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem], kind::f16.
+__device__ __forceinline__ void tc_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Values as the second operand: rows of the tile are keys (the K axis), 64
+// dims to a 128-byte row, so the operand is MN-major with the 128-byte swizzle:
+// 8-key groups follow at 1024 bytes, the next 64 dims at 128 keys * 128 bytes.
+__device__ __forceinline__ uint64_t desc_values(uint32_t addr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((addr & 0x3ffffu) >> 4);
+  d |= (uint64_t)(16384u >> 4) << 16;  // leading byte offset: between 64-dim chunks
+  d |= (uint64_t)(1024u >> 4) << 32;   // stride byte offset: between 8-key groups
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  if (BF16)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// A run of key tiles [j0, j1) of one (KV head, pair of row tiles).
+struct Run {
+  int h, rt, j0, j1, part;
+};
+
+// The line of units and this block's share of it.
+struct Line {
+  int tiles, cells_k, rts, heads;  // key tiles, pieces of the keys, row tile pairs, KV heads
+  int64_t u, u1, total;
+  int n, c;
+  bool whole;
+  __device__ __forceinline__ int cell_start(int kc) const { return (int)((int64_t)tiles * kc / cells_k); }
+  __device__ __forceinline__ void init(int tiles_, const AttnTcArgs& a) {
+    tiles = tiles_;
+    cells_k = min(a.cells_k, tiles);
+    rts = a.row_tiles;
+    heads = a.a.p.n_kv;
+    n = (int)gridDim.x;
+    c = (int)blockIdx.x;
+    whole = a.whole_cells;
+    total = (int64_t)heads * rts * tiles;
+    if (tiles == 0) {
+      u = u1 = 0;
+    } else if (whole) {
+      u = c;  // one cell: block index (h, kc, rt)
+      u1 = c < heads * cells_k * rts ? c + 1 : c;
+    } else {
+      u = total * c / n;
+      u1 = total * (c + 1) / n;
+    }
+  }
+  // The next run of this block; false at its end.
+  __device__ __forceinline__ bool next(Run* r) {
+    if (u >= u1) return false;
+    if (whole) {
+      r->rt = (int)(u % rts);
+      const int kc = (int)(u / rts % cells_k);
+      r->h = (int)(u / rts / cells_k);
+      r->j0 = cell_start(kc);
+      r->j1 = cell_start(kc + 1);
+      r->part = kc;
+      u++;
+      return true;
+    }
+    // unit u lies in head h; in it, cells of (piece, row tile pair)
+    const int64_t per = (int64_t)rts * tiles;
+    r->h = (int)(u / per);
+    const int64_t in = u % per;
+    int kc = (int)(in / rts * cells_k / tiles);
+    while (kc > 0 && (int64_t)cell_start(kc) * rts > in) kc--;
+    while ((int64_t)cell_start(kc + 1) * rts <= in) kc++;
+    const int s = cell_start(kc), len = cell_start(kc + 1) - s;
+    const int64_t off = in - (int64_t)s * rts;
+    r->rt = (int)(off / len);
+    r->j0 = s + (int)(off % len);
+    r->j1 = (int)min((int64_t)(s + len), r->j0 + (u1 - u));
+    // the cell's first unit lies in the same block's share, or in the one before
+    const int64_t first = (int64_t)r->h * per + (int64_t)s * rts + (int64_t)r->rt * len;
+    r->part = 2 * kc + (first < total * c / n ? 1 : 0);
+    u += r->j1 - r->j0;
+    return true;
+  }
+};
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kThreadsTc, 1)
+    attn_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                   const __grid_constant__ AttnTcArgs args) {
+  using C = TcCfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  uint8_t* sq = smem;
+  uint8_t* skv = smem + 2 * C::TILE;
+  __shared__ uint64_t kv_full[C::NS], kv_empty[C::NS], q_full[2], s_full[2], p_ready[2], o_full[2], drain;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort, s_vis;
+
+  const AttnArgs& a = args.a;
+  const attn_problem& p = a.p;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int parts_all = a.parts_prefix + a.parts_private;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::NS; i++) {
+      mbar_init(&kv_full[i], 1);
+      mbar_init(&kv_empty[i], 1);
+    }
+    for (int i = 0; i < 2; i++) {
+      mbar_init(&q_full[i], 128);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_ready[i], 128);
+      mbar_init(&o_full[i], 1);
+    }
+    mbar_init(&drain, 1);
+    s_abort = 0;
+    s_vis = p.prefix_len ? 0 : (int)p.P;
+    fence_mbar_init();
+  }
+  if (warp == 2) tmem_alloc(&s_tmem, 512);
+  __syncthreads();
+  if (p.prefix_len) {
+    int v = 0;
+    for (int b = threadIdx.x; b < p.B; b += kThreadsTc) v = max(v, (int)attn_prefix_len(p, b));
+    v = __reduce_max_sync(0xffffffffu, v);
+    if (lane == 0 && v) atomicMax(&s_vis, v);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  const int vis = s_vis;  // no row sees a position at or behind it
+  volatile int* abort_flag = &s_abort;
+  const int rows = p.B * p.T * a.G;
+  Line line;
+  line.init((vis + 127) / 128, args);
+
+  if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue) : "memory");
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t cnt = 0;  // tiles loaded
+      bool ok = true;
+      Run r;
+      while (ok && line.next(&r)) {
+        for (int j = r.j0; ok && j < r.j1; j++)
+          for (int kv = 0; kv < 2; kv++) {
+            const int st = cnt % C::NS;
+            if (cnt >= C::NS && !mbar_wait(&kv_empty[st], ((cnt / C::NS) & 1) ^ 1, abort_flag)) {
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(&kv_full[st], C::TILE);
+#pragma unroll
+            for (int x = 0; x < D / 64; x++)
+              tma_load_3d(smem_u32(skv) + st * C::TILE + x * 16384, kv ? &tv : &tk, &kv_full[st], x * 64, j * 128,
+                          r.h);
+            cnt++;
+          }
+      }
+      // the copies in flight land before the block ends
+      for (uint32_t i = cnt > C::NS ? cnt - C::NS : 0; i < cnt; i++)
+        mbar_wait_drain(&kv_full[i % C::NS], (i / C::NS) & 1);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t ab = BF16 ? 1 : 0;
+      constexpr uint32_t id_s = idesc_f16(128, 128, ab);
+      constexpr uint32_t id_o = idesc_f16(128, D, ab) | (1u << 16);  // B is MN-major
+      uint32_t cnt = 0;
+      uint32_t np[2] = {0, 0}, nq[2] = {0, 0};
+      bool ok = true;
+      Run r;
+      auto stage_wait = [&](uint32_t i) { return mbar_wait(&kv_full[i % C::NS], (i / C::NS) & 1, abort_flag); };
+      auto scores = [&](int i, uint32_t tile) {
+        const uint32_t k0 = smem_u32(skv) + (tile % C::NS) * C::TILE, q0 = smem_u32(sq) + i * C::TILE;
+#pragma unroll
+        for (int s = 0; s < D / 16; s++) {
+          const uint32_t off = (s / 4) * 16384 + (s % 4) * 32;
+          tc_mma_f16(tmem + 128 * i, smem_desc_sw128(q0 + off), smem_desc_sw128(k0 + off), id_s, s > 0);
+        }
+        tc_commit(&s_full[i]);
+      };
+      while (ok && line.next(&r)) {
+        const int na = rows - r.rt * 256 > 128 ? 2 : 1;  // row tiles with rows
+        const int n = r.j1 - r.j0;
+        for (int i = 0; ok && i < na; i++) ok = mbar_wait(&q_full[i], nq[i]++ & 1, abort_flag);
+        ok = ok && stage_wait(cnt);
+        if (!ok) break;
+        tc_fence_after();
+        for (int i = 0; i < na; i++) scores(i, cnt);
+        tc_commit(&kv_empty[cnt % C::NS]);
+        for (int j = 0; ok && j < n; j++) {
+          const uint32_t tv_ = cnt + 1, tk_ = cnt + 2;
+          ok = stage_wait(tv_) && (j + 1 >= n || stage_wait(tk_));
+          for (int i = 0; ok && i < na; i++) {
+            ok = mbar_wait(&p_ready[i], np[i]++ & 1, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t v0 = smem_u32(skv) + (tv_ % C::NS) * C::TILE;
+#pragma unroll
+            for (int s = 0; s < 8; s++)
+              tc_mma_f16_ts(tmem + 256 + 128 * i, tmem + 128 * i + 8 * s, desc_values(v0 + s * 2048), id_o,
+                            j > 0 || s > 0);
+            if (j + 1 < n)
+              scores(i, tk_);
+            else
+              tc_commit(&o_full[i]);
+          }
+          if (!ok) break;
+          tc_commit(&kv_empty[tv_ % C::NS]);
+          if (j + 1 < n) tc_commit(&kv_empty[tk_ % C::NS]);
+          cnt += 2;
+        }
+      }
+      // every product issued is done before the block's memory goes
+      tc_commit(&drain);
+      mbar_wait_drain(&drain, 0);
+    }
+  } else if (warp >= 4) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax) : "memory");
+    const int i = (warp - 4) >> 2;              // row tile
+    const int row = threadIdx.x - 128 - 128 * i;  // its row, = TMEM lane
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lane_off + 128 * i, to = tmem + lane_off + 256 + 128 * i;
+    // 2^(c s - m): a negative scale goes into the queries' sign, and a scale of
+    // zero becomes one that takes every score to zero but leaves -inf alone
+    const float c = fmaxf(fabsf(a.scale_log2), 1e-37f);
+    const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
+    uint32_t ns = 0, no = 0, cnt = 0;
+    bool ok = true;
+    Run r;
+    while (ok && line.next(&r)) {
+      const int n = r.j1 - r.j0;
+      const int rr = r.rt * 256 + i * 128 + row;
+      if (r.rt * 256 + i * 128 >= rows) {  // an empty row tile
+        cnt += 2 * n;
+        continue;
+      }
+      const bool live = rr < rows;
+      int64_t rid = -1;
+      int lim = 0;
+      const uint4* src = nullptr;
+      if (live) {
+        const int bt = rr / a.G, g = rr % a.G;
+        const int b = bt / p.T, t = bt % p.T;
+        const int hq = r.h * a.G + g;
+        rid = (int64_t)bt * p.Hq + hq;
+        lim = (int)attn_prefix_len(p, b);
+        src = reinterpret_cast<const uint4*>((const char*)p.q +
+                                             2 * (b * p.q_stride_b + t * p.q_stride_t + hq * p.q_stride_h));
+      }
+      // this row of the queries, in the swizzled layout of the keys
+#pragma unroll
+      for (int x = 0; x < D / 8; x++) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (live) v = __ldg(src + x);
+        v.x ^= flip;
+        v.y ^= flip;
+        v.z ^= flip;
+        v.w ^= flip;
+        *reinterpret_cast<uint4*>(sq + i * C::TILE + (x / 8) * 16384 + row * 128 + (((x & 7) ^ (row & 7)) << 4)) = v;
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&q_full[i]);
+
+      float m = -INFINITY;
+      uint64_t l2 = f2_pack(0.f, 0.f);
+      for (int j = r.j0; j < r.j1; j++) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[i], ns++ & 1, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int x = 0; x < 4; x++) tmem_ld_32x32b_x32(ts + 32 * x, s[x]);
+        tmem_ld_wait();
+        const int left = lim - j * 128;  // keys of the tile that the row sees
+        if (__any_sync(0xffffffffu, left < 128)) {
+#pragma unroll
+          for (int x = 0; x < 4; x++)
+#pragma unroll
+            for (int e = 0; e < 32; e++)
+              if (32 * x + e >= left) s[x][e] = 0xff800000u;  // -inf
+        }
+        float top = __uint_as_float(s[0][0]);
+#pragma unroll
+        for (int x = 0; x < 4; x++)
+#pragma unroll
+          for (int e = 0; e < 32; e += 2)
+            top = max3(top, __uint_as_float(s[x][e]), __uint_as_float(s[x][e + 1]));
+        top *= c;
+        const bool move = top > m + 8.f;  // also from -inf to the first score
+        if (__any_sync(0xffffffffu, move)) {
+          const float to_m = move ? top : m;
+          const float f = move ? attn_ex2(m - top) : 1.f;
+          m = to_m;
+          float a0, a1;
+          f2_unpack(l2, &a0, &a1);
+          l2 = f2_pack(a0 * f, a1 * f);
+          if (j > r.j0) {
+#pragma unroll
+            for (int x = 0; x < D / 32; x++) {
+              uint32_t o[32];
+              tmem_ld_32x32b_x32(to + 32 * x, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st_32x32b_x32(to + 32 * x, o);
+            }
+          }
+        }
+        const float base = m == -INFINITY ? 0.f : m;
+        const uint64_t c2 = f2_pack(c, c), b2 = f2_pack(-base, -base), one = f2_pack(1.f, 1.f);
+#pragma unroll
+        for (int x = 0; x < 4; x += 2) {
+          uint32_t w[32];
+#pragma unroll
+          for (int e = 0; e < 32; e++) {
+            const int y = x + e / 16, z = 2 * (e & 15);
+            float p0, p1;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(s[y][z]), __uint_as_float(s[y][z + 1])), c2, b2), &p0, &p1);
+            p0 = attn_ex2(p0);
+            p1 = attn_ex2(p1);
+            l2 = f2_fma(f2_pack(p0, p1), one, l2);
+            w[e] = pack2<BF16>(p0, p1);
+          }
+          tmem_st_32x32b_x32(ts + 16 * x, w);
+        }
+        if (i == 0 && vis < p.P && j * 128 + 128 > vis) {
+          // positions behind every row's limit are not data: their values
+          // must not reach the product, where 0 * NaN would
+          const uint32_t v = cnt + 1;
+          ok = mbar_wait(&kv_full[v % C::NS], (v / C::NS) & 1, abort_flag);
+          if (ok && row >= vis - j * 128) {
+            uint4* z = reinterpret_cast<uint4*>(skv + (v % C::NS) * C::TILE + row * 128);
+#pragma unroll
+            for (int x = 0; x < D / 64; x++)
+#pragma unroll
+              for (int e = 0; e < 8; e++) z[x * 1024 + e] = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&p_ready[i]);
+        cnt += 2;
+      }
+      ok = ok && mbar_wait(&o_full[i], no++ & 1, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      float l0, l1;
+      f2_unpack(l2, &l0, &l1);
+      const float l = l0 + l1;
+      if (live) a.pml[rid * parts_all + r.part] = make_float2(l > 0.f ? m : -INFINITY, l);
+      // a cell that one block did alone has no second part
+      if (live && !line.whole && (r.part & 1) == 0 && r.j1 == line.cell_start(r.part / 2 + 1))
+        a.pml[rid * parts_all + r.part + 1] = make_float2(-INFINITY, 0.f);
+      float* po = a.po + (rid * parts_all + r.part) * D;
+#pragma unroll
+      for (int x = 0; x < D / 32; x++) {
+        uint32_t o[32];
+        tmem_ld_32x32b_x32(to + 32 * x, o);
+        tmem_ld_wait();
+        if (live && l > 0.f)
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<uint4*>(po + 32 * x + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+      }
+      tc_fence_before();
+    }
+    // pieces that the visible prefix does not reach
+    const int used = line.cells_k * (line.whole ? 1 : 2);
+    if (used < a.parts_prefix) {
+      const int64_t all = (int64_t)p.B * p.T * p.Hq;
+      for (int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x - 128; x < all; x += (int64_t)gridDim.x * 256)
+        for (int y = used; y < a.parts_prefix; y++) a.pml[x * parts_all + y] = make_float2(-INFINITY, 0.f);
+    }
+  }
+  __syncthreads();
+  if (warp == 2) tmem_dealloc(tmem, 512);
+}
+
+template <int D, bool BF16>
+cudaError_t launch(const AttnTcArgs& t, cudaStream_t st) {
+  using C = TcCfg<D>;
+  const attn_problem& p = t.a.p;
+  CUtensorMap tk, tv;
+  const CUtensorMapDataType dt = BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  // one head: its stride is never used, but has to be a legal one
+  const int64_t kh = p.n_kv > 1 ? p.pk_stride_h : p.D, vh = p.n_kv > 1 ? p.pv_stride_h : p.D;
+  const int64_t ks = p.P > 1 ? p.pk_stride_s : p.D, vs = p.P > 1 ? p.pv_stride_s : p.D;
+  if (!make_tmap_3d(&tk, dt, p.pk, D, (uint64_t)p.P, (uint64_t)p.n_kv, 2 * ks, 2 * kh, 64, 128) ||
+      !make_tmap_3d(&tv, dt, p.pv, D, (uint64_t)p.P, (uint64_t)p.n_kv, 2 * vs, 2 * vh, 64, 128))
+    return cudaErrorInvalidValue;
+  auto kern = attn_tc_kernel<D, BF16>;
+  static KernelReady ready;
+  cudaError_t e = ready.once([&]() -> cudaError_t {
+    // setmaxnreg moves registers within the block: what the softmax warps take
+    // must not exceed what the others give back from the launch count
+    cudaFuncAttributes fa;
+    cudaError_t x = cudaFuncGetAttributes(&fa, kern);
+    if (x != cudaSuccess) return x;
+    if (4 * kRegsIssue + 8 * kRegsSoftmax > 12 * fa.numRegs || fa.numRegs > kRegsSoftmax) return cudaErrorInvalidConfiguration;
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  });
+  if (e != cudaSuccess) return e;
+  kern<<<t.blocks, kThreadsTc, C::SMEM, st>>>(tk, tv, t);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attn_tc(const AttnTcArgs& t, cudaStream_t st) {
+  const bool bf = t.a.p.dtype == IDX_BF16;
+  if (t.a.p.D == 128) return bf ? launch<128, true>(t, st) : launch<128, false>(t, st);
+  return bf ? launch<64, true>(t, st) : launch<64, false>(t, st);
+}
+
+}  // namespace idx

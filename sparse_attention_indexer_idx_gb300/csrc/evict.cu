@@ -345,7 +345,10 @@ cudaError_t launch_evict(const evict_problem& p, int32_t* src, int32_t* out_len,
   while (C < kMaxCluster && (p.S > (int64_t)C * kMaxSlice || (rows * C < sm_count() && p.S > (int64_t)C * 4096))) C *= 2;
   a.slice_max = (int)(((p.S + C - 1) / C + 31) & ~int64_t(31));
   const size_t smem = (size_t)std::max(a.slice_max, 32) * 4;
-  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static KernelReady ready;
+  cudaError_t e = ready.once([] {
+    return cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSlice * 4);
+  });
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(rows * C));

@@ -1,6 +1,7 @@
 // Library-internal declarations shared by the .cu files of libidx.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -117,6 +118,24 @@ cudaError_t launch_attn_shared(const attn_problem& p, void* out, float* lse, flo
 int64_t evict_max_slots();  // longest row that cache_evict takes
 cudaError_t launch_evict(const evict_problem& p, int32_t* src, int32_t* out_len, int32_t* out_pos, float* out_mass,
                          int64_t out_stride, cudaStream_t st);
+
+// Runs a kernel's one-time setup (its attributes) once per device.
+class KernelReady {
+ public:
+  template <class F>
+  cudaError_t once(F setup) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return setup();
+    const uint64_t bit = uint64_t(1) << dev;
+    if (done_.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    const cudaError_t e = setup();
+    if (e == cudaSuccess) done_.fetch_or(bit, std::memory_order_release);
+    return e;
+  }
+
+ private:
+  std::atomic<uint64_t> done_{0};
+};
 
 // ---- workspace carving -------------------------------------------------------
 struct WsCarver {
