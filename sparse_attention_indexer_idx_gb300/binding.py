@@ -235,6 +235,17 @@ def _stream(stream: Optional[torch.cuda.Stream]):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+# torch.cuda.current_stream() builds a Stream object; a decode step of a few
+# microseconds asks for the handle alone
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _raw_stream(stream: Optional[torch.cuda.Stream]):
+    if stream is not None or _current_raw_stream is None:
+        return _stream(stream)
+    return _current_raw_stream(torch.cuda.current_device())
+
+
 _DT = {torch.float32: IDX_F32, torch.bfloat16: IDX_BF16, torch.uint8: IDX_FP8_E4M3,
        torch.float8_e4m3fn: IDX_FP8_E4M3}
 
@@ -503,8 +514,40 @@ def _dense(t: torch.Tensor, name: str, shapes, dtype):
     return t.data_ptr()
 
 
+class _Described:
+    """A problem whose C struct is built, with all its checks, when it is first
+    used and again after a field was assigned or one of its tensors got other
+    memory; a decode loop that only changes the tensors' contents builds it
+    once."""
+
+    def __setattr__(self, name, value):
+        self.__dict__[name] = value
+        self.__dict__.pop("_desc", None)
+
+    def _tensors(self):
+        for v in list(self.__dict__.values()):
+            if isinstance(v, torch.Tensor):
+                yield v
+            elif isinstance(v, (tuple, list)):
+                yield from (t for t in v if isinstance(t, torch.Tensor))
+
+    def desc(self):
+        d = self.__dict__.get("_desc")
+        if d is not None:
+            for t, at in d[1]:
+                if t.data_ptr() != at:
+                    break
+            else:
+                return d
+        self.__dict__.pop("_desc", None)
+        c = self.c()
+        d = (ctypes.byref(c), [(t, t.data_ptr()) for t in self._tensors()], c)
+        self.__dict__["_desc"] = d
+        return d
+
+
 @dataclass
-class AttnProblem:
+class AttnProblem(_Described):
     """Device tensors of one attn_shared call (see attn_problem in include/idx.h).
     Caches are indexed [request, slot, KV head, D]; a head-major cache is passed
     as its transposed view."""
@@ -555,31 +598,36 @@ class AttnProblem:
 
 
 def attn_shared_workspace_size(p: AttnProblem, mass: bool = True) -> int:
-    cp = p.c()
-    return int(lib().attn_shared_workspace_size(ctypes.byref(cp), int(mass)))
+    return int(lib().attn_shared_workspace_size(p.desc()[0], int(mass)))
+
+
+def _out(t: torch.Tensor, name: str, shape, dtype):
+    """_dense for one shape, quick where the tensor is right."""
+    if t.shape == shape and t.dtype == dtype and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    return _dense(t, name, (tuple(shape),), dtype)
 
 
 def attn_shared(p: AttnProblem, out: torch.Tensor, lse: Optional[torch.Tensor], mass: Optional[torch.Tensor],
                 ws: torch.Tensor, stream=None):
     """out [B, T, Hq, D]; lse [B, T, Hq] float32 or None; mass [B, n_kv or 1, S]
     float32 (added to) or None."""
-    cp = p.c()
-    B, T, Hq, D = p.q.shape
-    rows = (B, T, Hq)
-    po = _dense(out, "out", (rows + (D,),), p.q.dtype)
-    pl = None if lse is None else _dense(lse, "lse", (rows,), torch.float32)
+    ref, _, cp = p.desc()
+    shape = p.q.shape
+    po = _out(out, "out", shape, p.q.dtype)
+    pl = None if lse is None else _out(lse, "lse", shape[:3], torch.float32)
     pm, heads = None, 1
     if mass is not None:
         _need(p.k is not None, "mass: there is no private cache")
-        pm = _dense(mass, "mass", ((B, 1, cp.S), (B, cp.n_kv, cp.S)), torch.float32)
-        heads = mass.shape[1]
-    _check(lib().attn_shared(ctypes.byref(cp), po, pl, pm, heads, _ptr(ws), ws.numel() * ws.element_size(),
-                             _stream(stream)))
+        heads = mass.shape[1] if mass.dim() == 3 and mass.shape[1] == cp.n_kv else 1
+        pm = _out(mass, "mass", (cp.B, heads, cp.S), torch.float32)
+    _check((_lib or lib()).attn_shared(ref, po, pl, pm, heads, _ptr(ws), ws.numel() * ws.element_size(),
+                                       _raw_stream(stream)))
     return out, lse, mass
 
 
 @dataclass
-class EvictProblem:
+class EvictProblem(_Described):
     """Device tensors of one cache_evict call (see evict_problem in include/idx.h).
     planes are indexed [B, S, heads, row] or [B, S, row]; they are compacted in
     place."""
@@ -624,16 +672,18 @@ def cache_evict(p: EvictProblem, out_src: torch.Tensor, out_len: Optional[torch.
     """out_src [B, mass_heads, n_keep] int32; out_len [B, mass_heads] int32;
     out_pos / out_mass [B, mass_heads, n_keep], or the problem's pos / mass
     themselves."""
-    ce = p.c()
-    B, Hm, S = p.mass.shape
-    K = int(p.n_keep)
-    ps = _dense(out_src, "out_src", ((B, Hm, K),), torch.int32)
-    pl = None if out_len is None else _dense(out_len, "out_len", ((B, Hm),), torch.int32)
-    widths = {t.shape[-1] for t in (out_pos, out_mass) if t is not None}
-    _need(len(widths) <= 1, "out_pos and out_mass: row strides differ")
-    ld = widths.pop() if widths else K
+    ref, _, ce = p.desc()
+    B, Hm, K = ce.B, ce.mass_heads, ce.n_keep
+    ps = _out(out_src, "out_src", (B, Hm, K), torch.int32)
+    pl = None if out_len is None else _out(out_len, "out_len", (B, Hm), torch.int32)
+    ld, pp, pm = K, None, None
+    if out_pos is not None:
+        ld = out_pos.shape[-1]
+        pp = _out(out_pos, "out_pos", (B, Hm, ld), torch.int32)
+    if out_mass is not None:
+        _need(out_pos is None or out_mass.shape[-1] == ld, "out_pos and out_mass: row strides differ")
+        ld = out_mass.shape[-1]
+        pm = _out(out_mass, "out_mass", (B, Hm, ld), torch.float32)
     _need(ld >= K, "out_pos and out_mass: rows shorter than n_keep")
-    pp = None if out_pos is None else _dense(out_pos, "out_pos", ((B, Hm, ld),), torch.int32)
-    pm = None if out_mass is None else _dense(out_mass, "out_mass", ((B, Hm, ld),), torch.float32)
-    _check(lib().cache_evict(ctypes.byref(ce), ps, pl, pp, pm, ld, _stream(stream)))
+    _check((_lib or lib()).cache_evict(ref, ps, pl, pp, pm, ld, _raw_stream(stream)))
     return out_src, out_len, out_pos, out_mass

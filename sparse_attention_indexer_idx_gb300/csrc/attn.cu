@@ -42,19 +42,24 @@ AttnTcArgs plan_tc(const AttnArgs& a) {
 }
 
 // How many pieces each part is cut into.  The streaming kernel's pieces have
-// one length everywhere, short enough to give every SM two blocks, not below
+// one length everywhere: short enough to give every SM two blocks, not below
 // kMinChunk keys (a block's start and the join of its warps cost about as much
-// as 128 keys do).
+// as 128 keys do), and long ones are cut further, to eight blocks for each of
+// those places, so that the last blocks leave few SMs idle.
 void plan_parts(AttnArgs& a) {
   const attn_problem& p = a.p;
-  constexpr int64_t kMinChunk = 128;
-  auto tiles = [](int64_t rows) { return ceil_div(rows, rows <= 16 ? 16 : 32); };
+  constexpr int64_t kMinChunk = 128, kLongChunk = 1024;
   const bool tc = prefix_on_tc(p);
+  const int64_t rows_pre = tc ? 0 : p.P > 0 ? (int64_t)p.B * p.T * a.G : 0;
+  const int64_t rows_prv = p.S == 0 ? 0 : p.ids ? a.G : (int64_t)p.T * a.G;
+  a.stream_rows = (int)std::min(kStreamRows, std::max(rows_pre, rows_prv));
+  const int64_t tile = a.stream_rows <= 16 ? 16 : 32;
+  auto tiles = [&](int64_t rows) { return ceil_div(rows, tile); };
   const int64_t pre = tc ? 0 : (int64_t)p.n_kv * tiles((int64_t)p.B * p.T * a.G);
   const int64_t prv = (int64_t)p.B * p.n_kv * (p.ids ? p.T * tiles(a.G) : tiles((int64_t)p.T * a.G));
   const int64_t keys = private_keys(p);
-  const int64_t blocks = 2 * (int64_t)sm_count();
-  const int64_t chunk = std::max(kMinChunk, ceil_div(pre * p.P + prv * keys, blocks));
+  const int64_t work = pre * p.P + prv * keys, sms = sm_count();
+  const int64_t chunk = std::max(std::max(kMinChunk, std::min(kLongChunk, ceil_div(work, 2 * sms))), ceil_div(work, 16 * sms));
   a.parts_prefix = (int)ceil_div(p.P, chunk);
   if (tc) {
     const AttnTcArgs t = plan_tc(a);
@@ -88,7 +93,7 @@ AttnArgs make_args(const attn_problem& p) {
   a.p = p;
   a.G = p.Hq / p.n_kv;
   a.scale_log2 = (float)((double)p.scale * 1.4426950408889634);
-  a.sc_ld = (private_keys(p) + 2) & ~int64_t(1);
+  a.sc_ld = (private_keys(p) + 4) & ~int64_t(3);  // rows of 16-byte groups, with room behind an odd last slot
   plan_parts(a);
   return a;
 }
@@ -110,11 +115,10 @@ cudaError_t launch_attn_shared(const attn_problem& p, void* out, float* lse, flo
   a.mass = mass;
   a.mass_heads = mass_heads;
   cudaError_t e = cudaSuccess;
-  if (prefix_on_tc(p))
-    e = launch_attn_tc(plan_tc(a), st);
-  else if (a.parts_prefix)
-    e = launch_attn_stream(a, true, st);
-  if (e == cudaSuccess && a.parts_private) e = launch_attn_stream(a, false, st);
+  const bool tc = prefix_on_tc(p);
+  if (tc) e = launch_attn_tc(plan_tc(a), st);
+  const bool stream_prefix = !tc && a.parts_prefix > 0;
+  if (e == cudaSuccess && (stream_prefix || a.parts_private)) e = launch_attn_stream(a, stream_prefix, tc, st);
   if (e == cudaSuccess) e = launch_attn_finish(a, st);
   return e;
 }

@@ -21,6 +21,7 @@ struct AttnArgs {
   int G;               // query heads of one KV head
   int parts_prefix;    // pieces of a row from the prefix, then from the private cache
   int parts_private;
+  int stream_rows;     // rows of one sequence and KV head in the streaming kernel, at most
   float* po;           // [rows, parts, D] unnormalised sums, rows = B*T*Hq
   float2* pml;         // [rows, parts] (m, l); l == 0: the piece is empty and po is not written
   float* sc;           // [rows, sc_ld] private scores y, or NULL
@@ -57,7 +58,9 @@ __device__ __forceinline__ float attn_ex2(float x) {
   return y;
 }
 
-cudaError_t launch_attn_stream(const AttnArgs& a, bool prefix, cudaStream_t st);
+// prefix: the shared prefix is streamed too.  after: a kernel of the same call
+// comes before this one, and does not write what this one reads.
+cudaError_t launch_attn_stream(const AttnArgs& a, bool prefix, bool after, cudaStream_t st);
 cudaError_t launch_attn_finish(const AttnArgs& a, cudaStream_t st);
 
 }  // namespace idx

@@ -2,97 +2,87 @@
 // of every private slot added to its mass.
 //
 // Both parts are bound by reading what the pieces left (po, and the private
-// scores).  One launch holds both: blocks 0 .. join_blocks - 1 join rows, a warp
-// each; the others add masses.  A mass block takes its rows' normalisers from
-// the pieces' (m, l) itself, so it need not wait for the join.
+// scores: 4 bytes a row and slot).  One launch holds both: blocks 0 ..
+// join_blocks - 1 join rows, a warp each; the others add masses.  A mass block
+// takes its rows' normalisers from the pieces' (m, l) itself, so it need not
+// wait for the join.
 #include "attn.cuh"
 
 namespace idx {
 
 namespace {
 
-constexpr int kJoinWarps = 4;
-constexpr int kThreads = 32 * kJoinWarps;
-
-// log2 of sum_i 2^(m_i) l_i over a row's pieces; -inf for a row without keys.
-__device__ __forceinline__ float row_lse2(const float2* ml, int parts) {
-  float top = -INFINITY;
-  for (int i = 0; i < parts; i++) {
-    const float2 x = ml[i];
-    if (x.y > 0.f) top = fmaxf(top, x.x);
-  }
-  if (top == -INFINITY) return top;
-  float l = 0.f;
-  for (int i = 0; i < parts; i++) {
-    const float2 x = ml[i];
-    if (x.y > 0.f) l += x.y * attn_ex2(x.x - top);
-  }
-  return top + log2f(l);
-}
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kSlots = 4;    // consecutive slots of a thread: one 16-byte load per row
+constexpr int kRowsAt = 128; // rows whose normalisers are held at a time
+constexpr int kBatch = 8;    // rows loaded before the first is used
 
 template <int D, bool BF16>
 __device__ void join_rows(const AttnArgs& a) {
   const int parts = a.parts_prefix + a.parts_private;
   const int64_t rows = (int64_t)a.p.B * a.p.T * a.p.Hq;
-  const int64_t r = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+  const int64_t r = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (r >= rows) return;
   const float2* ml = a.pml + r * parts;
-  // every lane takes pieces lane, lane + 32, ...
-  float top = -INFINITY, l = 0.f;
-  for (int i = lane; i < parts; i += 32) {
+  // lane i holds piece i (of the first 32; the others are read again)
+  const float2 none = make_float2(-INFINITY, 0.f);
+  const float2 first = lane < parts ? ml[lane] : none;
+  float top = first.y > 0.f ? first.x : -INFINITY;
+  for (int i = lane + 32; i < parts; i += 32) {
     const float2 x = ml[i];
     if (x.y > 0.f) top = fmaxf(top, x.x);
   }
 #pragma unroll
   for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
   const float base = top == -INFINITY ? 0.f : top;
-  for (int i = lane; i < parts; i += 32) {
-    const float2 x = ml[i];
-    if (x.y > 0.f) l += x.y * attn_ex2(x.x - base);
-  }
-#pragma unroll
-  for (int s = 16; s; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-
+  float l = 0.f;
   constexpr int E = D / 32;  // elements of a lane
   float acc[E];
 #pragma unroll
   for (int e = 0; e < E; e++) acc[e] = 0.f;
   for (int i0 = 0; i0 < parts; i0 += 32) {
-    float w = 0.f;
-    if (i0 + lane < parts) {
-      const float2 x = ml[i0 + lane];
-      if (x.y > 0.f) w = attn_ex2(x.x - base) * inv;
-    }
-    const unsigned some = __ballot_sync(0xffffffffu, w != 0.f);
-    const int n = min(32, parts - i0);
-#pragma unroll 4
-    for (int i = 0; i < n; i++) {
-      const float wi = __shfl_sync(0xffffffffu, w, i);
-      if (!((some >> i) & 1)) continue;  // empty pieces hold no data
-      const float* o = a.po + (r * parts + i0 + i) * D + lane * E;
-      if (E == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(o);
-        acc[0] += wi * x.x;
-        acc[1] += wi * x.y;
-        acc[E - 2] += wi * x.z;
-        acc[E - 1] += wi * x.w;
-      } else {
-        const float2 x = *reinterpret_cast<const float2*>(o);
-        acc[0] += wi * x.x;
-        acc[1] += wi * x.y;
+    const float2 x = i0 == 0 ? first : i0 + lane < parts ? ml[i0 + lane] : none;
+    const float w = x.y > 0.f ? attn_ex2(x.x - base) : 0.f;
+    l += w * x.y;
+    unsigned some = __ballot_sync(0xffffffffu, w != 0.f);  // empty pieces hold no data
+    while (some) {
+      constexpr int U = 8;
+      float v[U][E], wi[U];
+#pragma unroll
+      for (int u = 0; u < U; u++) {
+        const int i = some ? __ffs(some) - 1 : -1;
+        some &= some - 1;
+        wi[u] = __shfl_sync(0xffffffffu, w, i < 0 ? 0 : i);
+        if (i < 0) wi[u] = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; e++) v[u][e] = 0.f;
+        if (i >= 0) {
+          const float* o = a.po + (r * parts + i0 + i) * D + lane * E;
+          if constexpr (E == 4)
+            *reinterpret_cast<float4*>(v[u]) = *reinterpret_cast<const float4*>(o);
+          else
+            *reinterpret_cast<float2*>(v[u]) = *reinterpret_cast<const float2*>(o);
+        }
       }
+#pragma unroll
+      for (int u = 0; u < U; u++)
+#pragma unroll
+        for (int e = 0; e < E; e++) acc[e] += wi[u] * v[u][e];
     }
   }
+#pragma unroll
+  for (int s = 16; s; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
+  const float inv = l > 0.f ? 1.f / l : 0.f;
   uint32_t pk[E / 2];
 #pragma unroll
   for (int e = 0; e < E / 2; e++) {
     if (BF16) {
-      const __nv_bfloat162 x = __floats2bfloat162_rn(acc[2 * e], acc[2 * e + 1]);
+      const __nv_bfloat162 x = __floats2bfloat162_rn(acc[2 * e] * inv, acc[2 * e + 1] * inv);
       pk[e] = *reinterpret_cast<const uint32_t*>(&x);
     } else {
-      const __half2 x = __floats2half2_rn(acc[2 * e], acc[2 * e + 1]);
+      const __half2 x = __floats2half2_rn(acc[2 * e] * inv, acc[2 * e + 1] * inv);
       pk[e] = *reinterpret_cast<const uint32_t*>(&x);
     }
   }
@@ -102,61 +92,121 @@ __device__ void join_rows(const AttnArgs& a) {
   if (lane == 0 && a.lse) a.lse[r] = l > 0.f ? (top + log2f(l)) * 0.693147180559945309f : -INFINITY;
 }
 
-// Mass of every slot: a thread per slot sums its rows' weights in row order.
-__device__ void mass_dense(const AttnArgs& a, int64_t block) {
-  __shared__ float s_lse[kThreads];
+// What a mass block needs of a row: its log2 normaliser and how many private
+// slots it sees.
+struct MassRows {
+  float lse2[kRowsAt];
+  int lim[kRowsAt];
+  int longest;
+};
+
+// Rows (b, t, hq): i-th of the block's, t = t0 + i / heads, hq = hq0 + i %
+// heads.  A warp takes four rows at a time, eight lanes to a row's pieces.
+__device__ __forceinline__ void load_rows(const AttnArgs& a, MassRows& s, int b, int t0, int hq0, int heads, int i0,
+                                          int n) {
   const attn_problem& p = a.p;
   const int parts = a.parts_prefix + a.parts_private;
-  const int64_t per = (p.S + kThreads - 1) / kThreads;  // blocks of one (b, mass head)
+  const int lane = threadIdx.x & 31, sub = lane & 7;
+  if (threadIdx.x == 0) s.longest = 0;
+  __syncthreads();
+  for (int i = (threadIdx.x >> 5) * 4 + (lane >> 3); i < ((n + 3) & ~3); i += kWarps * 4) {
+    const bool live = i < n;
+    const int t = t0 + (i0 + (live ? i : 0)) / heads, hq = hq0 + (i0 + (live ? i : 0)) % heads;
+    const float2* ml = a.pml + (((int64_t)b * p.T + t) * p.Hq + hq) * parts;
+    float top = -INFINITY, l = 0.f;
+    for (int j0 = 0; j0 < parts; j0 += 32) {  // four pieces of a lane at a time
+      float2 x[4];
+#pragma unroll
+      for (int u = 0; u < 4; u++) {
+        const int j = j0 + u * 8 + sub;
+        x[u] = live && j < parts ? ml[j] : make_float2(-INFINITY, 0.f);
+      }
+      float m = top;
+#pragma unroll
+      for (int u = 0; u < 4; u++)
+        if (x[u].y > 0.f) m = fmaxf(m, x[u].x);
+      if (m == -INFINITY) continue;
+      l *= attn_ex2(top - m);
+      top = m;
+#pragma unroll
+      for (int u = 0; u < 4; u++)
+        if (x[u].y > 0.f) l += x[u].y * attn_ex2(x[u].x - top);
+    }
+    float m = top;
+#pragma unroll
+    for (int d = 1; d < 8; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    l = m == -INFINITY ? 0.f : l * attn_ex2(top - m);
+#pragma unroll
+    for (int d = 1; d < 8; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+    if (live && sub == 0) {
+      const int len = p.len[p.len_per_head ? (int64_t)b * p.n_kv + hq / a.G : b];
+      const int lim = len < 0 || len > p.S ? 0 : max(0, len - p.T + t + 1);
+      s.lse2[i] = m + log2f(l);
+      s.lim[i] = lim;
+      atomicMax(&s.longest, lim);
+    }
+  }
+  __syncthreads();
+}
+
+// Mass of every slot: a thread sums its slots' weights in row order.
+__device__ void mass_dense(const AttnArgs& a, int64_t block) {
+  __shared__ MassRows s;
+  const attn_problem& p = a.p;
+  const int64_t per = (p.S + kThreads * kSlots - 1) / (kThreads * kSlots);  // blocks of one (b, mass head)
   const int64_t bm = block / per;
-  const int64_t slot = (block % per) * kThreads + threadIdx.x;
+  const int64_t slot = (block % per * kThreads + threadIdx.x) * kSlots;
   const int b = (int)(bm / a.mass_heads), m = (int)(bm % a.mass_heads);
   const int heads = p.Hq / a.mass_heads;  // query heads of the mass head
   const int rows = heads * p.T;
-  float add = 0.f;
-  bool any = false;
-  for (int r0 = 0; r0 < rows; r0 += kThreads) {
+  float add[kSlots] = {};
+  int seen = 0;  // the thread's slots that some row sees
+  for (int r0 = 0; r0 < rows; r0 += kRowsAt) {
+    const int n = min(kRowsAt, rows - r0);
     __syncthreads();
-    if (r0 + (int)threadIdx.x < rows) {
-      const int r = r0 + threadIdx.x;
-      const int64_t row = ((int64_t)b * p.T + r / heads) * p.Hq + (int64_t)m * heads + r % heads;
-      s_lse[threadIdx.x] = row_lse2(a.pml + row * parts, parts);
-    }
-    __syncthreads();
-    const int n = min(kThreads, rows - r0);
-    int h_have = -1, len = 0;
-    for (int i = 0; i < n; i++) {
-      const int t = (r0 + i) / heads, hq = m * heads + (r0 + i) % heads;
-      const int h = hq / a.G;
-      if (h != h_have) {
-        h_have = h;
-        len = p.len[p.len_per_head ? (int64_t)b * p.n_kv + h : b];
-        if (len > p.S) len = 0;
+    load_rows(a, s, b, 0, m * heads, heads, r0, n);
+    if (slot >= s.longest) continue;
+    seen = max(seen, (int)min((int64_t)kSlots, s.longest - slot));
+    for (int i0 = 0; i0 < n; i0 += kBatch) {
+      float4 y[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; u++) {
+        const int i = i0 + u, r = r0 + i;
+        const bool in = i < n && slot < s.lim[i];
+        y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (in)
+          y[u] = *reinterpret_cast<const float4*>(
+              a.sc + (((int64_t)b * p.T + r / heads) * p.Hq + m * heads + r % heads) * a.sc_ld + slot);
       }
-      if (slot < (int64_t)len - p.T + t + 1) {
-        const float y = a.sc[(((int64_t)b * p.T + t) * p.Hq + hq) * a.sc_ld + slot];
-        add += attn_ex2(y - s_lse[i]);
-        any = true;
+#pragma unroll
+      for (int u = 0; u < kBatch; u++) {
+        const int i = i0 + u;
+        if (i >= n) break;
+        const float z = s.lse2[i];
+        const int64_t left = s.lim[i] - slot;
+        if (left > 0) add[0] += attn_ex2(y[u].x - z);
+        if (left > 1) add[1] += attn_ex2(y[u].y - z);
+        if (left > 2) add[2] += attn_ex2(y[u].z - z);
+        if (left > 3) add[3] += attn_ex2(y[u].w - z);
       }
     }
   }
-  if (any) a.mass[bm * p.S + slot] += add;
+  float* to = a.mass + bm * p.S + slot;
+#pragma unroll
+  for (int e = 0; e < kSlots; e++)
+    if (e < seen) to[e] += add[e];
 }
 
 // Mass of listed slots.  One list holds a slot at most once, so its threads add
 // to different slots; lists that can share a slot (another token's, or another
 // KV head's when all heads share the mass) follow one another in one block.
-__device__ void mass_listed(const AttnArgs& a, int64_t block) {
-  __shared__ float s_lse[kThreads];
+__device__ void mass_listed(const AttnArgs& a, int64_t block, int64_t per) {
+  __shared__ MassRows s;
   const attn_problem& p = a.p;
-  const int parts = a.parts_prefix + a.parts_private;
   const int lists_h = p.ids_per_head && a.mass_heads == 1 ? p.n_kv : 1;
   const int lists = p.T * lists_h;
-  const int64_t per = lists == 1 ? (p.W + kThreads - 1) / kThreads : 1;
   const int64_t bm = block / per;
   const int b = (int)(bm / a.mass_heads), m = (int)(bm % a.mass_heads);
-  const int64_t w0 = (block % per) * kThreads + threadIdx.x;
-  const int64_t step = per * kThreads;
   const int heads = p.Hq / a.mass_heads / lists_h;  // query heads that read one list into one mass head
   float* mass = a.mass + bm * p.S;
   for (int q = 0; q < lists; q++) {
@@ -165,73 +215,65 @@ __device__ void mass_listed(const AttnArgs& a, int64_t block) {
     const int32_t* list = p.ids + (p.ids_per_head ? (((int64_t)b * p.T + t) * p.n_kv + hq0 / a.G) * p.W
                                                   : ((int64_t)b * p.T + t) * p.W);
     const int64_t row0 = ((int64_t)b * p.T + t) * p.Hq + hq0;
-    for (int r0 = 0; r0 < heads; r0 += kThreads) {
-      __syncthreads();  // the previous list's additions are done, s_lse is free
-      if (r0 + (int)threadIdx.x < heads) s_lse[threadIdx.x] = row_lse2(a.pml + (row0 + r0 + threadIdx.x) * parts, parts);
-      __syncthreads();
-      const int n = min(kThreads, heads - r0);
-      for (int64_t w = w0; w < p.W; w += step) {
+    for (int r0 = 0; r0 < heads; r0 += kRowsAt) {
+      const int n = min(kRowsAt, heads - r0);
+      __syncthreads();  // the previous list's additions are done
+      load_rows(a, s, b, t, hq0, heads, r0, n);
+      for (int64_t w = block % per * kThreads + threadIdx.x; w < p.W; w += per * kThreads) {
         const int id = list[w];
+        if (id < 0 || id >= s.longest) continue;
         float add = 0.f;
-        int h_have = -1, lim = 0;
-        bool any = false;
-        for (int i = 0; i < n; i++) {
-          const int h = (hq0 + r0 + i) / a.G;
-          if (h != h_have) {
-            h_have = h;
-            const int len = p.len[p.len_per_head ? (int64_t)b * p.n_kv + h : b];
-            lim = len > p.S ? 0 : len - p.T + t + 1;
-          }
-          if (id >= 0 && id < lim) {
-            add += attn_ex2(a.sc[(row0 + r0 + i) * a.sc_ld + w] - s_lse[i]);
-            any = true;
-          }
+        for (int i0 = 0; i0 < n; i0 += kBatch) {
+          float y[kBatch];
+#pragma unroll
+          for (int u = 0; u < kBatch; u++) y[u] = i0 + u < n ? a.sc[(row0 + r0 + i0 + u) * a.sc_ld + w] : 0.f;
+#pragma unroll
+          for (int u = 0; u < kBatch; u++)
+            if (i0 + u < n && id < s.lim[i0 + u]) add += attn_ex2(y[u] - s.lse2[i0 + u]);
         }
-        if (any) atomicAdd(mass + id, add);
+        atomicAdd(mass + id, add);
       }
     }
   }
 }
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kThreads) attn_finish_kernel(const __grid_constant__ AttnArgs a, int64_t join_blocks) {
+__global__ void __launch_bounds__(kThreads, 2)
+    attn_finish_kernel(const __grid_constant__ AttnArgs a, int64_t join_blocks, int64_t per) {
+  grid_wait();
   if (blockIdx.x < join_blocks)
     join_rows<D, BF16>(a);
   else if (a.p.ids)
-    mass_listed(a, blockIdx.x - join_blocks);
+    mass_listed(a, blockIdx.x - join_blocks, per);
   else
     mass_dense(a, blockIdx.x - join_blocks);
+}
+
+template <int D, bool BF16>
+cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
+  const attn_problem& p = a.p;
+  const int64_t rows = (int64_t)p.B * p.T * p.Hq;
+  const int64_t join = (rows + kWarps - 1) / kWarps;
+  int64_t per = 0;  // mass blocks of one (b, mass head)
+  if (a.mass && a.parts_private) {
+    per = (p.S + kThreads * kSlots - 1) / (kThreads * kSlots);
+    if (p.ids) {
+      const bool one = p.T == 1 && !(p.ids_per_head && a.mass_heads == 1 && p.n_kv > 1);
+      per = one ? (p.W + kThreads - 1) / kThreads : 1;
+    }
+  }
+  const int64_t blocks = join + (int64_t)p.B * a.mass_heads * per;
+  if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+  return launch_after(attn_finish_kernel<D, BF16>, dim3((unsigned)blocks), kThreads, 0, st,
+                      a.parts_prefix + a.parts_private > 0, a, join, per);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_finish(const AttnArgs& a, cudaStream_t st) {
-  const attn_problem& p = a.p;
-  const int64_t rows = (int64_t)p.B * p.T * p.Hq;
-  const int64_t join = (rows + kJoinWarps - 1) / kJoinWarps;
-  int64_t mass = 0;
-  if (a.mass && a.parts_private) {
-    int64_t per = (p.S + kThreads - 1) / kThreads;
-    if (p.ids) {
-      const bool one = p.T == 1 && !(p.ids_per_head && a.mass_heads == 1 && p.n_kv > 1);
-      per = one ? (p.W + kThreads - 1) / kThreads : 1;
-    }
-    mass = (int64_t)p.B * a.mass_heads * per;
-  }
-  const dim3 grid((unsigned)(join + mass));
-  const bool bf = p.dtype == IDX_BF16;
-  if (p.D == 128) {
-    if (bf)
-      attn_finish_kernel<128, true><<<grid, kThreads, 0, st>>>(a, join);
-    else
-      attn_finish_kernel<128, false><<<grid, kThreads, 0, st>>>(a, join);
-  } else {
-    if (bf)
-      attn_finish_kernel<64, true><<<grid, kThreads, 0, st>>>(a, join);
-    else
-      attn_finish_kernel<64, false><<<grid, kThreads, 0, st>>>(a, join);
-  }
-  return cudaGetLastError();
+  const bool bf = a.p.dtype == IDX_BF16;
+  if (a.p.D == 128) return bf ? launch<128, true>(a, st) : launch<128, false>(a, st);
+  return bf ? launch<64, true>(a, st) : launch<64, false>(a, st);
 }
 
 }  // namespace idx

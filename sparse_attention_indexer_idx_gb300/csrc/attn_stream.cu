@@ -90,8 +90,10 @@ struct StreamItem {
   int row0, rows;   // rows row0 .. row0 + n - 1 of `rows`
 };
 
+// block: number of this item among those of its kind, row tiles of a piece next
+// to one another (they read the same keys), then the sequences, then the pieces.
 template <int D, int MT, bool BF16, bool GATHER, bool PREFIX>
-__global__ void __launch_bounds__(32 * kWarps) attn_stream_kernel(const __grid_constant__ AttnArgs a) {
+__device__ __forceinline__ void stream_item(const AttnArgs& a, int64_t block) {
   using C = StreamCfg<D>;
   constexpr int KT = C::KT, NT = KT / 8, KS = D / 16, CH = C::CH;
   constexpr int R = 16 * MT;
@@ -109,9 +111,13 @@ __global__ void __launch_bounds__(32 * kWarps) attn_stream_kernel(const __grid_c
 
   // ---- the item of this block
   StreamItem it;
-  it.part = blockIdx.y;
-  const int64_t seq = blockIdx.x;
-  const int tile = blockIdx.z;
+  const int64_t rows_all = PREFIX ? (int64_t)p.B * p.T * a.G : GATHER ? a.G : (int64_t)p.T * a.G;
+  const int64_t seqs = PREFIX ? p.n_kv : (int64_t)p.B * (GATHER ? p.T : 1) * p.n_kv;
+  const int64_t tiles = (rows_all + R - 1) / R;
+  const int tile = (int)(block % tiles);
+  const int64_t seq = block / tiles % seqs;
+  it.part = (int)(block / tiles / seqs);
+  it.rows = (int)rows_all;
   if (PREFIX) {
     it.h = (int)seq;
     it.b = it.t = 0;
@@ -119,7 +125,6 @@ __global__ void __launch_bounds__(32 * kWarps) attn_stream_kernel(const __grid_c
     it.v = (const char*)p.pv + 2 * it.h * p.pv_stride_h;
     it.ks = 2 * p.pk_stride_s;
     it.vs = 2 * p.pv_stride_s;
-    it.rows = p.B * p.T * a.G;
   } else {
     it.h = (int)(seq % p.n_kv);
     const int64_t bt = seq / p.n_kv;
@@ -129,7 +134,6 @@ __global__ void __launch_bounds__(32 * kWarps) attn_stream_kernel(const __grid_c
     it.v = (const char*)p.v + 2 * ((int64_t)it.b * p.v_stride_b + it.h * p.v_stride_h);
     it.ks = 2 * p.k_stride_s;
     it.vs = 2 * p.v_stride_s;
-    it.rows = GATHER ? a.G : p.T * a.G;
   }
   it.row0 = tile * R;
   const int nrow = min(R, it.rows - it.row0);
@@ -422,41 +426,54 @@ __global__ void __launch_bounds__(32 * kWarps) attn_stream_kernel(const __grid_c
   }
 }
 
-template <int D, int MT, bool BF16, bool GATHER, bool PREFIX>
-cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
+// Prefix items (if this kernel has them) come first: they are the longer ones.
+template <int D, int MT, bool BF16, bool GATHER>
+__global__ void __launch_bounds__(32 * kWarps)
+    attn_stream_kernel(const __grid_constant__ AttnArgs a, int64_t prefix_blocks) {
+  grid_let_next_start();
+  if (blockIdx.x < prefix_blocks)
+    stream_item<D, MT, BF16, false, true>(a, blockIdx.x);
+  else
+    stream_item<D, MT, BF16, GATHER, false>(a, blockIdx.x - prefix_blocks);
+  // the finish kernel waits for this grid alone: it ends behind the one before it
+  grid_wait();
+}
+
+int64_t tiles_of(int64_t rows, int mt) { return (rows + 16 * mt - 1) / (16 * mt); }
+
+template <int D, int MT, bool BF16, bool GATHER>
+cudaError_t launch(const AttnArgs& a, bool prefix, bool after, cudaStream_t st) {
   using C = StreamCfg<D>;
   const attn_problem& p = a.p;
   const int smem = C::RING + (GATHER ? C::SLOTS : 0) + 16 * MT * D * 2;
-  auto kern = attn_stream_kernel<D, MT, BF16, GATHER, PREFIX>;
+  auto kern = attn_stream_kernel<D, MT, BF16, GATHER>;
   static KernelReady ready;
   cudaError_t e = ready.once([&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
   if (e != cudaSuccess) return e;
-  const int64_t rows = PREFIX ? (int64_t)p.B * p.T * a.G : GATHER ? a.G : (int64_t)p.T * a.G;
-  const int tiles = (int)((rows + 16 * MT - 1) / (16 * MT));
-  const int64_t seqs = PREFIX ? p.n_kv : (int64_t)p.B * (GATHER ? p.T : 1) * p.n_kv;
-  const dim3 grid((unsigned)seqs, (unsigned)(PREFIX ? a.parts_prefix : a.parts_private), (unsigned)tiles);
-  kern<<<grid, 32 * kWarps, smem, st>>>(a);
-  return cudaGetLastError();
+  const int64_t np = prefix ? a.parts_prefix * p.n_kv * tiles_of((int64_t)p.B * p.T * a.G, MT) : 0;
+  const int64_t ns = a.parts_private * (int64_t)p.B * p.n_kv *
+                     (GATHER ? p.T * tiles_of(a.G, MT) : tiles_of((int64_t)p.T * a.G, MT));
+  if (np + ns > INT32_MAX) return cudaErrorInvalidConfiguration;
+  return launch_after(kern, dim3((unsigned)(np + ns)), 32 * kWarps, smem, st, after, a, np);
 }
 
-template <int D, bool BF16, bool GATHER, bool PREFIX>
-cudaError_t launch_rows(const AttnArgs& a, cudaStream_t st) {
-  const int64_t rows = PREFIX ? (int64_t)a.p.B * a.p.T * a.G : GATHER ? a.G : (int64_t)a.p.T * a.G;
-  return rows <= 16 ? launch<D, 1, BF16, GATHER, PREFIX>(a, st) : launch<D, 2, BF16, GATHER, PREFIX>(a, st);
+template <int D, bool BF16, bool GATHER>
+cudaError_t launch_rows(const AttnArgs& a, bool prefix, bool after, cudaStream_t st) {
+  return a.stream_rows <= 16 ? launch<D, 1, BF16, GATHER>(a, prefix, after, st)
+                             : launch<D, 2, BF16, GATHER>(a, prefix, after, st);
 }
 
 template <int D, bool BF16>
-cudaError_t launch_kind(const AttnArgs& a, bool prefix, cudaStream_t st) {
-  if (prefix) return launch_rows<D, BF16, false, true>(a, st);
-  return a.p.ids ? launch_rows<D, BF16, true, false>(a, st) : launch_rows<D, BF16, false, false>(a, st);
+cudaError_t launch_kind(const AttnArgs& a, bool prefix, bool after, cudaStream_t st) {
+  return a.p.ids ? launch_rows<D, BF16, true>(a, prefix, after, st) : launch_rows<D, BF16, false>(a, prefix, after, st);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_stream(const AttnArgs& a, bool prefix, cudaStream_t st) {
+cudaError_t launch_attn_stream(const AttnArgs& a, bool prefix, bool after, cudaStream_t st) {
   const bool bf = a.p.dtype == IDX_BF16;
-  if (a.p.D == 128) return bf ? launch_kind<128, true>(a, prefix, st) : launch_kind<128, false>(a, prefix, st);
-  return bf ? launch_kind<64, true>(a, prefix, st) : launch_kind<64, false>(a, prefix, st);
+  if (a.p.D == 128) return bf ? launch_kind<128, true>(a, prefix, after, st) : launch_kind<128, false>(a, prefix, after, st);
+  return bf ? launch_kind<64, true>(a, prefix, after, st) : launch_kind<64, false>(a, prefix, after, st);
 }
 
 }  // namespace idx

@@ -177,6 +177,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int parts_all = a.parts_prefix + a.parts_private;
 
+  grid_let_next_start();
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NS; i++) {
       mbar_init(&kv_full[i], 1);

@@ -71,6 +71,7 @@ __device__ __forceinline__ uint32_t warps_before(const uint32_t* count, int warp
 
 __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_constant__ EvictArgs a) {
   extern __shared__ __align__(16) uint32_t keys[];  // [slice_max]; later the late rows' slots
+  grid_let_next_start();
   __shared__ SelShared sh;
   cg::cluster_group cl = cg::this_cluster();
   const evict_problem& p = a.p;
@@ -309,6 +310,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
   const int64_t s = (blockIdx.x % chunks) * kMoveSlots + threadIdx.x;
   if (threadIdx.x == 0) count = 0;
   __syncthreads();
+  grid_wait();
   const int from = s < a.n_keep ? a.src[row * a.n_keep + s] : -1;
   const bool moves = from >= 0 && from != s;
   const unsigned m = __ballot_sync(0xffffffffu, moves);
@@ -381,8 +383,7 @@ cudaError_t launch_evict(const evict_problem& p, int32_t* src, int32_t* out_len,
   if (m.n_planes == 0) return cudaSuccess;
   const int64_t chunks = (p.n_keep + kMoveSlots - 1) / kMoveSlots;
   const dim3 grid((unsigned)(rows * chunks), (unsigned)m.first[m.n_planes]);
-  evict_move_kernel<<<grid, kMoveThreads, 0, st>>>(m);
-  return cudaGetLastError();
+  return launch_after(evict_move_kernel, grid, kMoveThreads, 0, st, true, m);
 }
 
 }  // namespace idx

@@ -137,6 +137,32 @@ class KernelReady {
   std::atomic<uint64_t> done_{0};
 };
 
+// Waits until the kernels before this one in the stream are complete and their
+// writes visible: needed in a kernel that launch_after() let start early.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Lets the next kernel of the call start as soon as every block of this one has
+// come this far and there is room for it (it still waits for this one's end).
+__device__ __forceinline__ void grid_let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Launches a kernel; with `early` its blocks may start while the last ones of
+// the kernel before it (of the same call) still run, and it calls grid_wait()
+// before it touches what that kernel reads or writes.
+template <class... P, class... A>
+cudaError_t launch_after(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, bool early, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = early ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, P(args)...);
+}
+
 // ---- workspace carving -------------------------------------------------------
 struct WsCarver {
   char* base;
