@@ -448,7 +448,7 @@ idx_status cache_evict(const evict_problem* p, int32_t* out_src, int32_t* out_le
     if (q.heads < 1 || q.row_bytes < 0 || (p->mass_heads > 1 && q.heads != p->mass_heads))
       return fail(IDX_ERR_INVALID_ARG, "plane %d: heads=%d for mass_heads=%d, row_bytes=%lld", i, q.heads,
                   p->mass_heads, (long long)q.row_bytes);
-    if (q.row_bytes > (1 << 24)) return fail(IDX_ERR_UNSUPPORTED, "plane %d: rows above 2^24 bytes", i);
+    if (q.row_bytes > (1 << 20)) return fail(IDX_ERR_UNSUPPORTED, "plane %d: rows above 2^20 bytes", i);
     if (!q.base && p->B > 0 && p->S > 0 && q.row_bytes > 0) return fail(IDX_ERR_INVALID_ARG, "plane %d is NULL", i);
     heads += p->mass_heads == 1 ? q.heads : 1;
   }

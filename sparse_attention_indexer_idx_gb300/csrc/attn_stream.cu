@@ -21,7 +21,6 @@ namespace idx {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kStages = 3;  // ring slots of a warp: two tiles in flight while one is used
 
 __device__ __forceinline__ void cp_async_16z(uint32_t dst, const void* src, bool live) {
   // live == false: no bytes are read, the 16 bytes become zero
@@ -62,8 +61,12 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return r;
 }
 
-template <int D>
+template <int D, int MT>
 struct StreamCfg {
+  // Ring slots of a warp.  With up to 16 rows two of them leave room for three
+  // blocks on an SM (registers allow no more), whose twelve tiles in flight
+  // cover the latency of HBM; with more rows two blocks fit, and a third slot.
+  static constexpr int kStages = MT == 1 ? 2 : 3;
   static constexpr int KT = D == 128 ? 16 : 32;  // keys of a warp's tile: 4 KB of keys, 4 KB of values
   static constexpr int ROWB = D * 2;
   static constexpr int CH = ROWB / 16;            // 16-byte chunks of a row
@@ -94,8 +97,8 @@ struct StreamItem {
 // to one another (they read the same keys), then the sequences, then the pieces.
 template <int D, int MT, bool BF16, bool GATHER, bool PREFIX>
 __device__ __forceinline__ void stream_item(const AttnArgs& a, int64_t block) {
-  using C = StreamCfg<D>;
-  constexpr int KT = C::KT, NT = KT / 8, KS = D / 16, CH = C::CH;
+  using C = StreamCfg<D, MT>;
+  constexpr int KT = C::KT, NT = KT / 8, KS = D / 16, CH = C::CH, kStages = C::kStages;
   constexpr int R = 16 * MT;
   extern __shared__ __align__(1024) char smem[];
   char* sring = smem;
@@ -428,7 +431,7 @@ __device__ __forceinline__ void stream_item(const AttnArgs& a, int64_t block) {
 
 // Prefix items (if this kernel has them) come first: they are the longer ones.
 template <int D, int MT, bool BF16, bool GATHER>
-__global__ void __launch_bounds__(32 * kWarps)
+__global__ void __launch_bounds__(32 * kWarps, MT == 1 ? 3 : 2)
     attn_stream_kernel(const __grid_constant__ AttnArgs a, int64_t prefix_blocks) {
   grid_let_next_start();
   if (blockIdx.x < prefix_blocks)
@@ -443,7 +446,7 @@ int64_t tiles_of(int64_t rows, int mt) { return (rows + 16 * mt - 1) / (16 * mt)
 
 template <int D, int MT, bool BF16, bool GATHER>
 cudaError_t launch(const AttnArgs& a, bool prefix, bool after, cudaStream_t st) {
-  using C = StreamCfg<D>;
+  using C = StreamCfg<D, MT>;
   const attn_problem& p = a.p;
   const int smem = C::RING + (GATHER ? C::SLOTS : 0) + 16 * MT * D * 2;
   auto kern = attn_stream_kernel<D, MT, BF16, GATHER>;

@@ -66,6 +66,15 @@ __device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+// Ties the registers of a tcgen05.ld to the wait before it, so that no use of
+// them can be scheduled ahead of that wait.
+__device__ __forceinline__ void tie(uint32_t (&r)[32]) {
+  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                    "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+  asm volatile("" : "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                    "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                    "+r"(r[30]), "+r"(r[31]));
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Values as the second operand: rows of the tile are keys (the K axis), 64
@@ -341,44 +350,67 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       mbar_arrive(&q_full[i]);
 
       float m = -INFINITY;
-      uint64_t l2 = f2_pack(0.f, 0.f);
+      uint64_t l2[4];
+#pragma unroll
+      for (int q = 0; q < 4; q++) l2[q] = f2_pack(0.f, 0.f);
       for (int j = r.j0; j < r.j1; j++) {
         ok = __all_sync(0xffffffffu, mbar_wait(&s_full[i], ns++ & 1, abort_flag));
         if (!ok) break;
         tc_fence_after();
+        // the row's scores, the second half on its way while the first is used;
+        // maxima and sums run in four chains each, the latency of one would be
+        // longer than the products
         uint32_t s[4][32];
-#pragma unroll
-        for (int x = 0; x < 4; x++) tmem_ld_32x32b_x32(ts + 32 * x, s[x]);
-        tmem_ld_wait();
+        float tops[4];
         const int left = lim - j * 128;  // keys of the tile that the row sees
-        if (__any_sync(0xffffffffu, left < 128)) {
-#pragma unroll
-          for (int x = 0; x < 4; x++)
+        const bool cut = __any_sync(0xffffffffu, left < 128);
+        tmem_ld_32x32b_x32(ts, s[0]);
+        tmem_ld_32x32b_x32(ts + 32, s[1]);
+        tmem_ld_wait();
+        tie(s[0]);
+        tie(s[1]);
+        tmem_ld_32x32b_x32(ts + 64, s[2]);
+        tmem_ld_32x32b_x32(ts + 96, s[3]);
+        auto look = [&](int x) {
+          if (cut) {
 #pragma unroll
             for (int e = 0; e < 32; e++)
               if (32 * x + e >= left) s[x][e] = 0xff800000u;  // -inf
-        }
-        float top = __uint_as_float(s[0][0]);
+          }
+          if (x == 0) {
 #pragma unroll
-        for (int x = 0; x < 4; x++)
+            for (int q = 0; q < 4; q++) tops[q] = __uint_as_float(s[0][q]);
+          }
 #pragma unroll
-          for (int e = 0; e < 32; e += 2)
-            top = max3(top, __uint_as_float(s[x][e]), __uint_as_float(s[x][e + 1]));
+          for (int e = 0; e < 32; e += 8)
+#pragma unroll
+            for (int q = 0; q < 4; q++)
+              tops[q] = max3(tops[q], __uint_as_float(s[x][e + 2 * q]), __uint_as_float(s[x][e + 2 * q + 1]));
+        };
+        look(0);
+        look(1);
+        tmem_ld_wait();
+        tie(s[2]);
+        tie(s[3]);
+        look(2);
+        look(3);
+        float top = max3(tops[0], tops[1], fmaxf(tops[2], tops[3]));
         top *= c;
         const bool move = top > m + 8.f;  // also from -inf to the first score
         if (__any_sync(0xffffffffu, move)) {
           const float to_m = move ? top : m;
           const float f = move ? attn_ex2(m - top) : 1.f;
           m = to_m;
-          float a0, a1;
-          f2_unpack(l2, &a0, &a1);
-          l2 = f2_pack(a0 * f, a1 * f);
+          const uint64_t f2 = f2_pack(f, f), zero = f2_pack(0.f, 0.f);
+#pragma unroll
+          for (int q = 0; q < 4; q++) l2[q] = f2_fma(l2[q], f2, zero);
           if (j > r.j0) {
 #pragma unroll
             for (int x = 0; x < D / 32; x++) {
               uint32_t o[32];
               tmem_ld_32x32b_x32(to + 32 * x, o);
               tmem_ld_wait();
+              tie(o);
 #pragma unroll
               for (int e = 0; e < 32; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
               tmem_st_32x32b_x32(to + 32 * x, o);
@@ -397,7 +429,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             f2_unpack(f2_fma(f2_pack(__uint_as_float(s[y][z]), __uint_as_float(s[y][z + 1])), c2, b2), &p0, &p1);
             p0 = attn_ex2(p0);
             p1 = attn_ex2(p1);
-            l2 = f2_fma(f2_pack(p0, p1), one, l2);
+            l2[e & 3] = f2_fma(f2_pack(p0, p1), one, l2[e & 3]);
             w[e] = pack2<BF16>(p0, p1);
           }
           tmem_st_32x32b_x32(ts + 16 * x, w);
@@ -425,9 +457,13 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
-      float l0, l1;
-      f2_unpack(l2, &l0, &l1);
-      const float l = l0 + l1;
+      float l = 0.f;
+#pragma unroll
+      for (int q = 0; q < 4; q++) {
+        float l0, l1;
+        f2_unpack(l2[q], &l0, &l1);
+        l += l0 + l1;
+      }
       if (live) a.pml[rid * parts_all + r.part] = make_float2(l > 0.f ? m : -INFINITY, l);
       // a cell that one block did alone has no second part
       if (live && !line.whole && (r.part & 1) == 0 && r.j1 == line.cell_start(r.part / 2 + 1))
@@ -438,6 +474,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         uint32_t o[32];
         tmem_ld_32x32b_x32(to + 32 * x, o);
         tmem_ld_wait();
+        tie(o);
         if (live && l > 0.f)
 #pragma unroll
           for (int e = 0; e < 32; e += 4)

@@ -25,8 +25,6 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512;
-constexpr int kSelWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxSlice = 49152;  // keys of one block: 192 KB of shared memory
@@ -38,15 +36,13 @@ struct EvictArgs {
   int32_t* out_pos;
   float* out_mass;
   int64_t out_stride;
-  int slice_max;  // keys that a block has room for
 };
 
 struct SelShared {
-  alignas(16) uint32_t hist[2][kBins];  // read four bins at a time
-  uint32_t bitmap[kMaxSlice / 32];
-  uint32_t wcount[kSelWarps];
-  uint32_t wcount2[kSelWarps];
-  uint32_t scan[kSelWarps];
+  alignas(16) uint32_t hist[2][kBins];  // read several bins at a time
+  uint32_t wcount[32];
+  uint32_t wcount2[32];
+  uint32_t scan[32];
   uint32_t found_bin, found_above;
   uint32_t ties, late, holes;  // this block's counts, read by the cluster
 };
@@ -57,25 +53,48 @@ __device__ __forceinline__ uint32_t rank_key(float m, bool guard) {
   return score_key(m);
 }
 
-// Exclusive sum of one value per warp (lane 0's), and their total.
-__device__ __forceinline__ uint32_t warps_before(const uint32_t* count, int warp, uint32_t* total) {
-  uint32_t before = 0, all = 0;
-  for (int w = 0; w < kSelWarps; w++) {
-    const uint32_t c = count[w];
-    if (w < warp) before += c;
-    all += c;
-  }
-  *total = all;
-  return before;
+// Sum of the values of the warps before this one, and of all (a value per
+// warp, at most 32).
+__device__ __forceinline__ uint32_t warps_before(const uint32_t* count, int warps, int warp, uint32_t* total) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t v = lane < warps ? count[lane] : 0;
+  *total = __reduce_add_sync(0xffffffffu, v);
+  return __reduce_add_sync(0xffffffffu, lane < warp ? v : 0);
 }
 
-__global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_constant__ EvictArgs a) {
-  extern __shared__ __align__(16) uint32_t keys[];  // [slice_max]; later the late rows' slots
-  grid_let_next_start();
+// The cluster of a row, or the one block that has it all: there the exchange
+// needs no cluster barriers and no distributed addresses.
+template <bool ONE>
+struct RowGroup {
+  __device__ __forceinline__ int blocks() const { return ONE ? 1 : (int)cg::this_cluster().num_blocks(); }
+  __device__ __forceinline__ int rank() const { return ONE ? 0 : (int)cg::this_cluster().block_rank(); }
+  __device__ __forceinline__ void sync() const {
+    if (ONE)
+      __syncthreads();
+    else
+      cg::this_cluster().sync();
+  }
+  template <class T>
+  __device__ __forceinline__ T* at(T* x, int r) const {
+    return ONE ? x : cg::this_cluster().map_shared_rank(x, r);
+  }
+};
+
+// NT threads; each takes U slots, or words of 32 slots, at a time, so that U
+// loads are in flight.
+template <int NT, bool ONE>
+__global__ void __launch_bounds__(NT, 1024 / NT) evict_select_kernel(const __grid_constant__ EvictArgs a, int slice_max) {
+  constexpr int W = NT / 32, U = 8;
+  // the slice's keys, later the late rows' slots; a bitmap of the slots that
+  // stay; and the slice's holes before each word of it
+  extern __shared__ __align__(16) uint32_t keys[];
+  uint32_t* bitmap = keys + slice_max;
+  uint16_t* rank = reinterpret_cast<uint16_t*>(bitmap + slice_max / 32);
   __shared__ SelShared sh;
-  cg::cluster_group cl = cg::this_cluster();
+  grid_let_next_start();
+  const RowGroup<ONE> cl;
   const evict_problem& p = a.p;
-  const int C = (int)cl.num_blocks(), c = (int)cl.block_rank();
+  const int C = cl.blocks(), c = cl.rank();
   const int64_t row = blockIdx.x / C;
   const int b = (int)(row / p.mass_heads);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -100,20 +119,32 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
   const int cnt = s1 - s0;
   const int words = (cnt + 31) >> 5;
   // a warp's words [w0, w1) for the ordered passes
-  const int wper = (words + kSelWarps - 1) / kSelWarps;
+  const int wper = (words + W - 1) / W;
   const int w0 = min(words, warp * wper), w1 = min(words, w0 + wper);
 
-  uint32_t before_late = 0, before_holes = 0;
   if (trim) {
-    for (int i = tid; i < kBins; i += kThreads) sh.hist[0][i] = sh.hist[1][i] = 0;
+    for (int i = tid; i < kBins; i += NT) sh.hist[0][i] = sh.hist[1][i] = 0;
+    // positions from here on are protected
+    const int recent = (int)max((int64_t)INT32_MIN, (p.cur ? p.cur[b] : n) - (int64_t)p.n_last);
     __syncthreads();
-    const int64_t cur = p.cur ? p.cur[b] : n;
-    for (int i = tid; i < cnt; i += kThreads) {
-      const int s = s0 + i;
-      const int64_t at = pos ? pos[s] : s;
-      const uint32_t k = rank_key(mass[s], at < p.n_first || at >= cur - p.n_last);
-      keys[i] = k;
-      atomicAdd(&sh.hist[0][k >> 21], 1u);
+    for (int i0 = tid; i0 < cnt; i0 += NT * U) {
+      float x[U];
+      int at[U];
+#pragma unroll
+      for (int u = 0; u < U; u++) {
+        const int i = i0 + u * NT;
+        x[u] = i < cnt ? mass[s0 + i] : 0.f;
+        at[u] = i < cnt && pos ? pos[s0 + i] : s0 + i;
+      }
+#pragma unroll
+      for (int u = 0; u < U; u++) {
+        const int i = i0 + u * NT;
+        if (i < cnt) {
+          const uint32_t k = rank_key(x[u], at[u] < p.n_first || at[u] >= recent);
+          keys[i] = k;
+          atomicAdd(&sh.hist[0][k >> 21], 1u);
+        }
+      }
     }
     // digits from the top: after each, `prefix` holds the found digits and
     // `need` how many keys of that prefix stay
@@ -125,25 +156,30 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
         const int shift = pass == 1 ? 10 : 0;
         const uint32_t mask = pass == 1 ? 2047u : 1023u;
         const int top = pass == 1 ? 21 : 10;
-        for (int i = tid; i < cnt; i += kThreads) {
+#pragma unroll 4
+        for (int i = tid; i < cnt; i += NT) {
           const uint32_t k = keys[i];
           if ((k >> top) == (prefix >> top)) atomicAdd(&hist[(k >> shift) & mask], 1u);
         }
       }
       cl.sync();
-      // the cluster's histogram, four bins a thread, largest bin first
-      uint32_t v[4], mine = 0;
-      const int b0 = kBins - 4 * (tid + 1);
+      // the cluster's histogram, a few bins a thread, largest bin first
+      constexpr int V = kBins / NT;  // 2 to 8
+      uint32_t v[V], mine = 0;
+      const int b0 = kBins - V * (tid + 1);
 #pragma unroll
-      for (int j = 0; j < 4; j++) v[j] = 0;
+      for (int j = 0; j < V; j++) v[j] = 0;
       for (int r = 0; r < C; r++) {
-        const uint4 x = *reinterpret_cast<const uint4*>(cl.map_shared_rank(hist, r) + b0);
-        v[0] += x.x;
-        v[1] += x.y;
-        v[2] += x.z;
-        v[3] += x.w;
+        const uint2* h = reinterpret_cast<const uint2*>(cl.at(hist, r) + b0);
+#pragma unroll
+        for (int j = 0; j < V / 2; j++) {
+          const uint2 x = h[j];
+          v[2 * j] += x.x;
+          v[2 * j + 1] += x.y;
+        }
       }
-      mine = v[0] + v[1] + v[2] + v[3];
+#pragma unroll
+      for (int j = 0; j < V; j++) mine += v[j];
       uint32_t incl = mine;
 #pragma unroll
       for (int s = 1; s < 32; s <<= 1) {
@@ -153,10 +189,10 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
       if (lane == 31) sh.scan[warp] = incl;
       __syncthreads();
       uint32_t all;
-      uint32_t above = warps_before(sh.scan, warp, &all) + incl - mine;
+      uint32_t above = warps_before(sh.scan, W, warp, &all) + incl - mine;
       if (above < need && need <= above + mine) {
 #pragma unroll
-        for (int j = 3; j >= 0; j--) {
+        for (int j = V - 1; j >= 0; j--) {
           if (above < need && need <= above + v[j]) {
             sh.found_bin = b0 + j;
             sh.found_above = above;
@@ -164,28 +200,30 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
           above += v[j];
         }
       }
-      // every block has read hist[(pass - 1) & 1] before this pass's cluster
-      // barrier: it can be cleared for the next pass
+      // every block has read hist[0] before the second pass's cluster barrier
       if (pass == 1)
-        for (int i = tid; i < kBins; i += kThreads) sh.hist[0][i] = 0;
+        for (int i = tid; i < kBins; i += NT) sh.hist[0][i] = 0;
       __syncthreads();
       need -= sh.found_above;
       prefix |= sh.found_bin << (pass == 0 ? 21 : pass == 1 ? 10 : 0);
     }
     // ties of the last kept key: the lowest slots stay
     uint32_t t = 0;
+#pragma unroll 4
     for (int w = w0; w < w1; w++) {
       const int i = w * 32 + lane;
-      t += __popc(__ballot_sync(0xffffffffu, i < cnt && keys[i] == prefix));
+      t += i < cnt && keys[i] == prefix;
     }
+    t = __reduce_add_sync(0xffffffffu, t);
     if (lane == 0) sh.wcount[warp] = t;
     __syncthreads();
     uint32_t total;
-    uint32_t tie = warps_before(sh.wcount, warp, &total);
+    uint32_t tie = warps_before(sh.wcount, W, warp, &total);
     if (tid == 0) sh.ties = total;
     cl.sync();
-    for (int r = 0; r < c; r++) tie += *cl.map_shared_rank(&sh.ties, r);
+    for (int r = 0; r < c; r++) tie += *cl.at(&sh.ties, r);
     uint32_t late = 0, holes = 0;
+#pragma unroll 2
     for (int w = w0; w < w1; w++) {
       const int i = w * 32 + lane;
       const uint32_t k = i < cnt ? keys[i] : 0;
@@ -195,8 +233,11 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
       tie += __popc(eqs);
       const unsigned word = __ballot_sync(0xffffffffu, stay);
       late += __popc(__ballot_sync(0xffffffffu, stay && s0 + i >= nk));
+      if (lane == 0) {
+        bitmap[w] = word;
+        rank[w] = (uint16_t)holes;  // within the warp's words, for now
+      }
       holes += __popc(__ballot_sync(0xffffffffu, i < cnt && !stay && s0 + i < nk));
-      if (lane == 0) sh.bitmap[w] = word;
     }
     if (lane == 0) {
       sh.wcount[warp] = late;
@@ -204,52 +245,85 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
     }
     __syncthreads();  // the keys are read, the bitmap is whole: the late rows' slots take the keys' place
     uint32_t all_late, all_holes;
-    before_late = warps_before(sh.wcount, warp, &all_late);
-    before_holes = warps_before(sh.wcount2, warp, &all_holes);
+    uint32_t at = warps_before(sh.wcount, W, warp, &all_late);
+    const uint32_t holes_before = warps_before(sh.wcount2, W, warp, &all_holes);
     if (tid == 0) {
       sh.late = all_late;
       sh.holes = all_holes;
     }
-    uint32_t at = before_late;
+    for (int w = w0 + lane; w < w1; w += 32) rank[w] += (uint16_t)holes_before;
     for (int w = w0; w < w1; w++) {
+      if (s0 + w * 32 + 31 < nk) continue;
       const int i = w * 32 + lane;
-      const bool is = i < cnt && s0 + i >= nk && ((sh.bitmap[w] >> lane) & 1);
+      const bool is = i < cnt && s0 + i >= nk && ((bitmap[w] >> lane) & 1);
       const unsigned m = __ballot_sync(0xffffffffu, is);
       if (is) keys[at + __popc(m & ((1u << lane) - 1))] = (uint32_t)(s0 + i);
       at += __popc(m);
     }
     cl.sync();
-    for (int r = 0; r < c; r++) before_holes += *cl.map_shared_rank(&sh.holes, r);
   }
 
-  // where each new slot comes from
-  for (int w = w0; w < w1; w++) {
-    const int i = w * 32 + lane;
-    const int s = s0 + i;
-    if (s0 + w * 32 >= nk) break;
-    const bool in = i < cnt && s < nk;
-    const bool hole = in && trim && !((sh.bitmap[w] >> lane) & 1);
-    const unsigned m = __ballot_sync(0xffffffffu, hole);
-    int from = s;
-    if (hole) {
-      uint32_t r = before_holes + __popc(m & ((1u << lane) - 1));
-      int q = 0;
-      while (q < C - 1) {
-        const uint32_t l = *cl.map_shared_rank(&sh.late, q);
-        if (r < l) break;
-        r -= l;
-        q++;
+  // where each new slot comes from: words of 32 new slots in turn over the
+  // warps of the whole cluster
+  uint32_t holes_of = 0, late_of = 0;  // lane r: holes and late rows of the blocks before block r
+  if (trim) {
+    uint32_t h = lane < C ? *cl.at(&sh.holes, lane) : 0;
+    uint32_t l = lane < C ? *cl.at(&sh.late, lane) : 0;
+    holes_of = h;
+    late_of = l;
+#pragma unroll
+    for (int s = 1; s < kMaxCluster; s <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, holes_of, s), y = __shfl_up_sync(0xffffffffu, late_of, s);
+      if (lane >= s) {
+        holes_of += x;
+        late_of += y;
       }
-      from = (int)*cl.map_shared_rank(keys + r, q);
     }
-    before_holes += __popc(m);
-    if (in) {
-      src[s] = from;
-      if (opos) opos[s] = pos ? pos[from] : from;
-      if (omass) omass[s] = mass[from];
-    }
+    holes_of -= h;
+    late_of -= l;
   }
-  for (int64_t s = nk + (int64_t)c * kThreads + tid; s < p.n_keep; s += (int64_t)C * kThreads) {
+  const int new_words = (nk + 31) >> 5, stride = C * W;
+  for (int v0 = c * W + warp; v0 < new_words; v0 += stride * 4) {
+    int from[4], slot[4];
+#pragma unroll
+    for (int u = 0; u < 4; u++) {
+      const int v = v0 + u * stride;
+      const int s = v * 32 + lane;
+      const bool in = v < new_words && s < nk;
+      slot[u] = in ? s : -1;
+      from[u] = s;
+      if (trim && v < new_words) {
+        const int q = v * 32 / slice, w = v - q * (slice >> 5);  // the block that has this word
+        const unsigned word = cl.at(bitmap, q)[w];
+        const bool hole = in && !((word >> lane) & 1);
+        const unsigned m = __ballot_sync(0xffffffffu, hole);
+        if (m) {
+          const uint32_t r = __shfl_sync(0xffffffffu, holes_of, q) + cl.at(rank, q)[w] +
+                             __popc(m & ((1u << lane) - 1));
+          int z = 0;  // the block that has late row r
+#pragma unroll
+          for (int x = 1; x < kMaxCluster; x++) z += x < C && r >= __shfl_sync(0xffffffffu, late_of, x);
+          const uint32_t first = __shfl_sync(0xffffffffu, late_of, z);
+          if (hole) from[u] = (int)*cl.at(keys + (r - first), z);
+        }
+      }
+    }
+    int ps[4];
+    float ms[4];
+#pragma unroll
+    for (int u = 0; u < 4; u++) {
+      ps[u] = slot[u] >= 0 && opos && pos ? pos[from[u]] : from[u];
+      ms[u] = slot[u] >= 0 && omass ? mass[from[u]] : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; u++)
+      if (slot[u] >= 0) {
+        src[slot[u]] = from[u];
+        if (opos) opos[slot[u]] = ps[u];
+        if (omass) omass[slot[u]] = ms[u];
+      }
+  }
+  for (int64_t s = nk + (int64_t)c * NT + tid; s < p.n_keep; s += (int64_t)C * NT) {
     src[s] = -1;
     if (opos) opos[s] = -1;
     if (omass) omass[s] = 0.f;
@@ -259,7 +333,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
     // outputs in place: the slots that the row no longer has start afresh
     const bool clear_pos = opos && opos == pos, clear_mass = omass && omass == mass;
     if (clear_pos || clear_mass)
-      for (int s = max(s0, nk) + tid; s < s1; s += kThreads) {
+      for (int s = max(s0, nk) + tid; s < s1; s += NT) {
         if (clear_pos) opos[s] = -1;
         if (clear_mass) omass[s] = 0.f;
       }
@@ -269,7 +343,6 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
 
 // ------------------------------------------------------------------- moves --
 constexpr int kMoveThreads = 256;
-constexpr int kMoveSlots = 256;  // new slots that a block looks at
 
 struct MoveArgs {
   const int32_t* src;  // [B, mass_heads, n_keep]
@@ -281,43 +354,58 @@ struct MoveArgs {
 
 template <class V>
 __device__ __forceinline__ void move_rows(const int2* list, int n, char* base, int64_t ss, int64_t row_bytes) {
-  const int per = (int)(row_bytes / (int64_t)sizeof(V));  // vectors of a row
-  const int64_t all = (int64_t)n * per;
-  constexpr int U = 4;
-  for (int64_t i0 = threadIdx.x; i0 < all; i0 += (int64_t)U * kMoveThreads) {
+  const uint32_t per = (uint32_t)(row_bytes / (int64_t)sizeof(V));  // vectors of a row
+  const uint32_t all = n * per;  // at most 1024 rows of 2^20 bytes
+  constexpr uint32_t U = 4;
+  for (uint32_t i0 = threadIdx.x; i0 < all; i0 += U * kMoveThreads) {
     V x[U];
+    V* to[U];
 #pragma unroll
-    for (int u = 0; u < U; u++) {
-      const int64_t i = i0 + (int64_t)u * kMoveThreads;
-      if (i < all) x[u] = reinterpret_cast<const V*>(base + list[i / per].y * ss)[i % per];
+    for (uint32_t u = 0; u < U; u++) {
+      const uint32_t i = i0 + u * kMoveThreads;
+      if (i < all) {
+        const uint32_t r = i / per, e = i - r * per;
+        const int2 mv = list[r];
+        x[u] = reinterpret_cast<const V*>(base + mv.y * ss)[e];
+        to[u] = reinterpret_cast<V*>(base + mv.x * ss) + e;
+      }
     }
 #pragma unroll
-    for (int u = 0; u < U; u++) {
-      const int64_t i = i0 + (int64_t)u * kMoveThreads;
-      if (i < all) reinterpret_cast<V*>(base + list[i / per].x * ss)[i % per] = x[u];
-    }
+    for (uint32_t u = 0; u < U; u++)
+      if (i0 + u * kMoveThreads < all) *to[u] = x[u];
   }
 }
 
+// SLOTS: new slots that a block looks at.
+template <int SLOTS>
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ MoveArgs a) {
-  __shared__ int2 list[kMoveSlots];  // (new slot, slot it comes from)
+  __shared__ int2 list[SLOTS];  // (new slot, slot it comes from)
   __shared__ int count;
   int pl = 0;
   while (pl + 1 < a.n_planes && (int)blockIdx.y >= a.first[pl + 1]) pl++;
   const evict_plane& q = a.plane[pl];
-  const int64_t chunks = (a.n_keep + kMoveSlots - 1) / kMoveSlots;
+  const int64_t chunks = (a.n_keep + SLOTS - 1) / SLOTS;
   const int64_t row = blockIdx.x / chunks;
-  const int64_t s = (blockIdx.x % chunks) * kMoveSlots + threadIdx.x;
+  const int64_t s0 = (blockIdx.x % chunks) * SLOTS + threadIdx.x;
   if (threadIdx.x == 0) count = 0;
   __syncthreads();
   grid_wait();
-  const int from = s < a.n_keep ? a.src[row * a.n_keep + s] : -1;
-  const bool moves = from >= 0 && from != s;
-  const unsigned m = __ballot_sync(0xffffffffu, moves);
-  int at = 0;
-  if ((threadIdx.x & 31) == 0 && m) at = atomicAdd(&count, __popc(m));
-  at = __shfl_sync(0xffffffffu, at, 0);
-  if (moves) list[at + __popc(m & ((1u << (threadIdx.x & 31)) - 1))] = make_int2((int)s, from);
+  int from[SLOTS / kMoveThreads];
+#pragma unroll
+  for (int u = 0; u < SLOTS / kMoveThreads; u++) {
+    const int64_t s = s0 + u * kMoveThreads;
+    from[u] = s < a.n_keep ? a.src[row * a.n_keep + s] : -1;
+  }
+#pragma unroll
+  for (int u = 0; u < SLOTS / kMoveThreads; u++) {
+    const int s = (int)s0 + u * kMoveThreads;
+    const bool moves = from[u] >= 0 && from[u] != s;
+    const unsigned m = __ballot_sync(0xffffffffu, moves);
+    int at = 0;
+    if ((threadIdx.x & 31) == 0 && m) at = atomicAdd(&count, __popc(m));
+    at = __shfl_sync(0xffffffffu, at, 0);
+    if (moves) list[at + __popc(m & ((1u << (threadIdx.x & 31)) - 1))] = make_int2(s, from[u]);
+  }
   __syncthreads();
   const int n = count;
   if (n == 0) return;
@@ -337,33 +425,44 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
 
 int64_t evict_max_slots() { return (int64_t)kMaxCluster * kMaxSlice; }
 
-cudaError_t launch_evict(const evict_problem& p, int32_t* src, int32_t* out_len, int32_t* out_pos, float* out_mass,
-                         int64_t out_stride, cudaStream_t st) {
-  const int64_t rows = (int64_t)p.B * p.mass_heads;
-  EvictArgs a{p, src, out_len, out_pos, out_mass, out_stride, 0};
-  // blocks of a row: as many as its keys need, more while the rows leave SMs
-  // idle and a block still has a few thousand keys
-  int C = 1;
-  while (C < kMaxCluster && (p.S > (int64_t)C * kMaxSlice || (rows * C < sm_count() && p.S > (int64_t)C * 4096))) C *= 2;
-  a.slice_max = (int)(((p.S + C - 1) / C + 31) & ~int64_t(31));
-  const size_t smem = (size_t)std::max(a.slice_max, 32) * 4;
+template <int NT, bool ONE>
+static cudaError_t launch_select(const EvictArgs& a, int64_t rows, int C, cudaStream_t st) {
+  auto bytes = [](int64_t slice) { return (size_t)(slice * 4 + slice / 32 * 6); };
+  const int64_t slice = std::max<int64_t>(((a.p.S + C - 1) / C + 31) & ~int64_t(31), 32);
+  auto kern = evict_select_kernel<NT, ONE>;
   static KernelReady ready;
-  cudaError_t e = ready.once([] {
-    return cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSlice * 4);
-  });
+  cudaError_t e =
+      ready.once([&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes(kMaxSlice)); });
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(rows * C));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.blockDim = dim3(NT);
+  cfg.dynamicSmemBytes = bytes(slice);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = (unsigned)C;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a);
+  cfg.numAttrs = ONE ? 0 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, a, (int)slice);
+}
+
+cudaError_t launch_evict(const evict_problem& p, int32_t* src, int32_t* out_len, int32_t* out_pos, float* out_mass,
+                         int64_t out_stride, cudaStream_t st) {
+  const int64_t rows = (int64_t)p.B * p.mass_heads;
+  const EvictArgs a{p, src, out_len, out_pos, out_mass, out_stride};
+  // blocks of a row: as many as its keys need, more while the rows leave SMs
+  // idle and a block still has a few thousand keys
+  int C = 1;
+  while (C < kMaxCluster && (p.S > (int64_t)C * kMaxSlice || (rows * C < sm_count() && p.S > (int64_t)C * 4096))) C *= 2;
+  cudaError_t e;
+  if (C > 1)
+    e = launch_select<1024, false>(a, rows, C, st);
+  else if (p.S > 8192)
+    e = launch_select<1024, true>(a, rows, C, st);
+  else
+    e = launch_select<256, true>(a, rows, C, st);
   if (e != cudaSuccess || p.n_planes == 0) return e;
 
   MoveArgs m{};
@@ -381,9 +480,14 @@ cudaError_t launch_evict(const evict_problem& p, int32_t* src, int32_t* out_len,
     m.n_planes++;
   }
   if (m.n_planes == 0) return cudaSuccess;
-  const int64_t chunks = (p.n_keep + kMoveSlots - 1) / kMoveSlots;
-  const dim3 grid((unsigned)(rows * chunks), (unsigned)m.first[m.n_planes]);
-  return launch_after(evict_move_kernel, grid, kMoveThreads, 0, st, true, m);
+  // a block looks at 1024 new slots, or at 256 where that leaves SMs idle
+  const int64_t wide = rows * ((p.n_keep + 1023) / 1024);
+  if (wide * m.first[m.n_planes] >= 4 * sm_count())
+    return launch_after(evict_move_kernel<1024>, dim3((unsigned)wide, (unsigned)m.first[m.n_planes]), kMoveThreads, 0, st,
+                        true, m);
+  const int64_t narrow = rows * ((p.n_keep + 255) / 256);
+  return launch_after(evict_move_kernel<256>, dim3((unsigned)narrow, (unsigned)m.first[m.n_planes]), kMoveThreads, 0, st,
+                      true, m);
 }
 
 }  // namespace idx
