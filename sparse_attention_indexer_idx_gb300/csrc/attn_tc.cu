@@ -19,7 +19,7 @@
 // where the pieces fill them; a block leaves one partial result per piece it
 // touched and the finish kernel joins them.
 //
-// Warp roles: warp 0 TMA producer, warp 1 MMA issuer, warp 2 TMEM allocation,
+// Warp roles: warp 0 TMA producer, warp 1 MMA issue, warp 2 TMEM allocation,
 // warps 4..7 and 8..11 the two row tiles.  Waits are bounded as everywhere in
 // the library; on a timeout the roles stop and drain what they issued.
 #include "attn_tc.cuh"
@@ -55,6 +55,12 @@ __device__ __forceinline__ void tc_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, 
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+// True in one lane, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
 }
 __device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t* r) {
   asm volatile(
@@ -183,7 +189,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
 
   const AttnArgs& a = args.a;
   const attn_problem& p = a.p;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // A warp index that is uniform for the compiler, and a warp that runs
+  // converged around the issue of its products: their descriptors then stay in
+  // uniform registers (24 cycles a product; from one lane's own it was 45, and
+  // twice that next to the softmax warps, more than a product takes).
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int parts_all = a.parts_prefix + a.parts_private;
 
   grid_let_next_start();
@@ -248,60 +258,99 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         mbar_wait_drain(&kv_full[i % C::NS], (i / C::NS) & 1);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t ab = BF16 ? 1 : 0;
-      constexpr uint32_t id_s = idesc_f16(128, 128, ab);
-      constexpr uint32_t id_o = idesc_f16(128, D, ab) | (1u << 16);  // B is MN-major
-      uint32_t cnt = 0;
-      uint32_t np[2] = {0, 0}, nq[2] = {0, 0};
-      bool ok = true;
-      Run r;
-      auto stage_wait = [&](uint32_t i) { return mbar_wait(&kv_full[i % C::NS], (i / C::NS) & 1, abort_flag); };
-      auto scores = [&](int i, uint32_t tile) {
-        const uint32_t k0 = smem_u32(skv) + (tile % C::NS) * C::TILE, q0 = smem_u32(sq) + i * C::TILE;
+    constexpr uint32_t ab = BF16 ? 1 : 0;
+    constexpr uint32_t id_s = idesc_f16(128, 128, ab);
+    constexpr uint32_t id_o = idesc_f16(128, D, ab) | (1u << 16);  // B is MN-major
+    // descriptors of the first query tile and the first ring slot; others follow
+    // at their distance (in 16 bytes)
+    const uint64_t dq = smem_desc_sw128(smem_u32(sq)), dk = smem_desc_sw128(smem_u32(skv)),
+                   dv = desc_values(smem_u32(skv));
+    uint32_t slot = 0, phase = 0;  // of the next ring slot
+    uint32_t np = 0, nq0 = 0, nq1 = 0, np1 = 0;
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+    };
+    auto advance = [&] {
+      if (++slot == C::NS) {
+        slot = 0;
+        phase ^= 1;
+      }
+    };
+    // S_i = Q_i K^T, then the barrier of its readers
+    auto scores = [&](int i, uint32_t k) {
+      const uint64_t q0 = dq + i * (C::TILE / 16), k0 = dk + k * (C::TILE / 16);
 #pragma unroll
-        for (int s = 0; s < D / 16; s++) {
-          const uint32_t off = (s / 4) * 16384 + (s % 4) * 32;
-          tc_mma_f16(tmem + 128 * i, smem_desc_sw128(q0 + off), smem_desc_sw128(k0 + off), id_s, s > 0);
+      for (int s = 0; s < D / 16; s++) {
+        const uint32_t off = ((s / 4) * 16384 + (s % 4) * 32) / 16;
+        tc_mma_f16(tmem + 128 * i, q0 + off, k0 + off, id_s, s > 0);
+      }
+      tc_commit(&s_full[i]);
+    };
+    // O_i += P_i V, then the next S_i, or the barrier of O's reader
+    auto values = [&](int i, uint32_t v, uint32_t k, bool add, bool more) {
+      const uint64_t v0 = dv + v * (C::TILE / 16);
+#pragma unroll
+      for (int s = 0; s < 8; s++)
+        tc_mma_f16_ts(tmem + 256 + 128 * i, tmem + 128 * i + 8 * s, v0 + s * (2048 / 16), id_o, add || s > 0);
+      if (more)
+        scores(i, k);
+      else
+        tc_commit(&o_full[i]);
+    };
+    Run r;
+    while (ok && line.next(&r)) {
+      const bool two = rows - r.rt * 256 > 128;  // both row tiles have rows
+      const int n = r.j1 - r.j0;
+      ok = wait(&q_full[0], nq0++ & 1);
+      if (two) ok = ok && wait(&q_full[1], nq1++ & 1);
+      ok = ok && wait(&kv_full[slot], phase);
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {
+        scores(0, slot);
+        if (two) scores(1, slot);
+        tc_commit(&kv_empty[slot]);
+      }
+      __syncwarp();
+      advance();
+      for (int j = 0; j < n; j++) {
+        const uint32_t v = slot;
+        ok = wait(&kv_full[slot], phase);
+        advance();
+        const uint32_t k = slot;
+        const bool more = j + 1 < n;
+        if (more) {
+          ok = ok && wait(&kv_full[slot], phase);
+          advance();
         }
-        tc_commit(&s_full[i]);
-      };
-      while (ok && line.next(&r)) {
-        const int na = rows - r.rt * 256 > 128 ? 2 : 1;  // row tiles with rows
-        const int n = r.j1 - r.j0;
-        for (int i = 0; ok && i < na; i++) ok = mbar_wait(&q_full[i], nq[i]++ & 1, abort_flag);
-        ok = ok && stage_wait(cnt);
+        ok = ok && wait(&p_ready[0], np++ & 1);
         if (!ok) break;
         tc_fence_after();
-        for (int i = 0; i < na; i++) scores(i, cnt);
-        tc_commit(&kv_empty[cnt % C::NS]);
-        for (int j = 0; ok && j < n; j++) {
-          const uint32_t tv_ = cnt + 1, tk_ = cnt + 2;
-          ok = stage_wait(tv_) && (j + 1 >= n || stage_wait(tk_));
-          for (int i = 0; ok && i < na; i++) {
-            ok = mbar_wait(&p_ready[i], np[i]++ & 1, abort_flag);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t v0 = smem_u32(skv) + (tv_ % C::NS) * C::TILE;
-#pragma unroll
-            for (int s = 0; s < 8; s++)
-              tc_mma_f16_ts(tmem + 256 + 128 * i, tmem + 128 * i + 8 * s, desc_values(v0 + s * 2048), id_o,
-                            j > 0 || s > 0);
-            if (j + 1 < n)
-              scores(i, tk_);
-            else
-              tc_commit(&o_full[i]);
+        if (elect_one()) {
+          values(0, v, k, j > 0, more);
+          if (!two) {
+            tc_commit(&kv_empty[v]);
+            if (more) tc_commit(&kv_empty[k]);
           }
-          if (!ok) break;
-          tc_commit(&kv_empty[tv_ % C::NS]);
-          if (j + 1 < n) tc_commit(&kv_empty[tk_ % C::NS]);
-          cnt += 2;
         }
+        __syncwarp();
+        if (!two) continue;
+        ok = wait(&p_ready[1], np1++ & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          values(1, v, k, j > 0, more);
+          tc_commit(&kv_empty[v]);
+          if (more) tc_commit(&kv_empty[k]);
+        }
+        __syncwarp();
       }
-      // every product issued is done before the block's memory goes
-      tc_commit(&drain);
-      mbar_wait_drain(&drain, 0);
     }
+    // every product issued is done before the block's memory goes
+    if (elect_one()) tc_commit(&drain);
+    __syncwarp();
+    mbar_wait_drain(&drain, 0);
   } else if (warp >= 4) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax) : "memory");
     const int i = (warp - 4) >> 2;              // row tile
