@@ -41,31 +41,40 @@ AttnTcArgs plan_tc(const AttnArgs& a) {
   return t;
 }
 
-// How many pieces each part is cut into.  The streaming kernel's pieces have
-// one length everywhere: short enough to give every SM two blocks, not below
-// kMinChunk keys (a block's start and the join of its warps cost about as much
-// as 128 keys do), and long ones are cut further, to eight blocks for each of
-// those places, so that the last blocks leave few SMs idle.
-void plan_parts(AttnArgs& a) {
+// The streaming kernel's groups and the parts of a sequence.  Every SM holds
+// three blocks of 16 rows or two of 32.  The share of a group depends on the
+// lengths, which only the device knows; the parts allow for lines down to a
+// quarter of the longest.
+StreamLine plan_stream(AttnArgs& a) {
   const attn_problem& p = a.p;
-  constexpr int64_t kMinChunk = 128, kLongChunk = 1024;
-  const bool tc = prefix_on_tc(p);
-  const int64_t rows_pre = tc ? 0 : p.P > 0 ? (int64_t)p.B * p.T * a.G : 0;
+  StreamLine l{};
+  const bool prefix = p.P > 0 && !prefix_on_tc(p);
+  const int64_t rows_pre = prefix ? (int64_t)p.B * p.T * a.G : 0;
   const int64_t rows_prv = p.S == 0 ? 0 : p.ids ? a.G : (int64_t)p.T * a.G;
-  a.stream_rows = (int)std::min(kStreamRows, std::max(rows_pre, rows_prv));
-  const int64_t tile = a.stream_rows <= 16 ? 16 : 32;
-  auto tiles = [&](int64_t rows) { return ceil_div(rows, tile); };
-  const int64_t pre = tc ? 0 : (int64_t)p.n_kv * tiles((int64_t)p.B * p.T * a.G);
-  const int64_t prv = (int64_t)p.B * p.n_kv * (p.ids ? p.T * tiles(a.G) : tiles((int64_t)p.T * a.G));
-  const int64_t keys = private_keys(p);
-  const int64_t work = pre * p.P + prv * keys, sms = sm_count();
-  const int64_t chunk = std::max(std::max(kMinChunk, std::min(kLongChunk, ceil_div(work, 2 * sms))), ceil_div(work, 16 * sms));
-  a.parts_prefix = (int)ceil_div(p.P, chunk);
-  if (tc) {
+  const int64_t rows = std::max<int64_t>(1, std::max(rows_pre, rows_prv));
+  l.row_tile = rows <= 16 ? 16 : 32;
+  l.members = (int)(p.n_kv * ceil_div(rows, l.row_tile));
+  l.groups = (int)std::max<int64_t>(1, (l.row_tile == 16 ? 3 : 2) * (int64_t)sm_count() / l.members);
+  const int64_t unit = stream_unit(p.D);
+  l.prefix_units = prefix ? (int)ceil_div(p.P, unit) : 0;
+  const int64_t longest = ceil_div(private_keys(p), unit);
+  l.seqs = longest == 0 ? 0 : p.ids ? p.B * p.T : p.B;
+  const int64_t total = l.prefix_units + l.seqs * longest;
+  // a unit more than a quarter of the even share, at least two: a block's start
+  // and the join of its warps cost about as much as two units do
+  l.least = (int)std::max<int64_t>(2, ceil_div(total, 4 * (int64_t)l.groups));
+  auto parts = [&](int64_t units) { return units == 0 ? 0 : (int)std::min(units, ceil_div(units - 1, l.least) + 1); };
+  if (prefix) a.parts_prefix = parts(l.prefix_units);
+  a.parts_private = l.seqs ? parts(longest) : 0;
+  return l;
+}
+
+void plan_parts(AttnArgs& a) {
+  if (prefix_on_tc(a.p)) {
     const AttnTcArgs t = plan_tc(a);
     a.parts_prefix = t.cells_k * (t.whole_cells ? 1 : 2);
   }
-  a.parts_private = (int)ceil_div(keys, chunk);
+  plan_stream(a);
 }
 
 struct AttnWs {
@@ -117,8 +126,8 @@ cudaError_t launch_attn_shared(const attn_problem& p, void* out, float* lse, flo
   cudaError_t e = cudaSuccess;
   const bool tc = prefix_on_tc(p);
   if (tc) e = launch_attn_tc(plan_tc(a), st);
-  const bool stream_prefix = !tc && a.parts_prefix > 0;
-  if (e == cudaSuccess && (stream_prefix || a.parts_private)) e = launch_attn_stream(a, stream_prefix, tc, st);
+  const StreamLine line = plan_stream(a);
+  if (e == cudaSuccess && line.prefix_units + line.seqs > 0) e = launch_attn_stream(a, line, tc, st);
   if (e == cudaSuccess) e = launch_attn_finish(a, st);
   return e;
 }

@@ -21,7 +21,6 @@ struct AttnArgs {
   int G;               // query heads of one KV head
   int parts_prefix;    // pieces of a row from the prefix, then from the private cache
   int parts_private;
-  int stream_rows;     // rows of one sequence and KV head in the streaming kernel, at most
   float* po;           // [rows, parts, D] unnormalised sums, rows = B*T*Hq
   float2* pml;         // [rows, parts] (m, l); l == 0: the piece is empty and po is not written
   float* sc;           // [rows, sc_ld] private scores y, or NULL
@@ -58,9 +57,19 @@ __device__ __forceinline__ float attn_ex2(float x) {
   return y;
 }
 
-// prefix: the shared prefix is streamed too.  after: a kernel of the same call
-// comes before this one, and does not write what this one reads.
-cudaError_t launch_attn_stream(const AttnArgs& a, bool prefix, bool after, cudaStream_t st);
+// The streaming kernel's line of key units and its cut (see attn_stream.cu).
+constexpr int stream_unit(int D) { return D == 128 ? 64 : 128; }  // keys
+struct StreamLine {
+  int row_tile;      // 16 or 32 rows of a block
+  int members;       // blocks of a group: KV heads times row tiles
+  int groups;
+  int prefix_units;  // 0: the prefix is not streamed
+  int seqs;          // private sequences: requests, or (request, token) lists
+  int least;         // smallest share of a group, so that no sequence has more parts than planned
+};
+// after: a kernel of the same call comes before this one, and does not write
+// what this one reads.
+cudaError_t launch_attn_stream(const AttnArgs& a, const StreamLine& line, bool after, cudaStream_t st);
 cudaError_t launch_attn_finish(const AttnArgs& a, cudaStream_t st);
 
 }  // namespace idx

@@ -6,6 +6,8 @@
 // join_blocks - 1 join rows, a warp each; the others add masses.  A mass block
 // takes its rows' normalisers from the pieces' (m, l) itself, so it need not
 // wait for the join.
+#include <algorithm>
+
 #include "attn.cuh"
 
 namespace idx {
@@ -149,39 +151,59 @@ __device__ __forceinline__ void load_rows(const AttnArgs& a, MassRows& s, int b,
   __syncthreads();
 }
 
-// Mass of every slot: a thread sums its slots' weights in row order.
-__device__ void mass_dense(const AttnArgs& a, int64_t block) {
+// Mass of every slot.  A slot's rows are split over `groups` threads in equal
+// runs; each sums its own in row order, then the runs are added in order.  The
+// scores and the old masses do not depend on the normalisers: the first of
+// them are under way while those are formed.
+__device__ void mass_dense(const AttnArgs& a, int64_t block, int groups) {
   __shared__ MassRows s;
+  __shared__ float4 s_add[kThreads];
   const attn_problem& p = a.p;
-  const int64_t per = (p.S + kThreads * kSlots - 1) / (kThreads * kSlots);  // blocks of one (b, mass head)
+  const int lanes = kThreads / groups;  // threads next to one another in the slots
+  const int64_t per = (p.S + lanes * kSlots - 1) / (lanes * kSlots);  // blocks of one (b, mass head)
   const int64_t bm = block / per;
-  const int64_t slot = (block % per * kThreads + threadIdx.x) * kSlots;
+  const int mine = threadIdx.x % lanes, run = threadIdx.x / lanes;
+  const int64_t slot = (block % per * lanes + mine) * kSlots;
   const int b = (int)(bm / a.mass_heads), m = (int)(bm % a.mass_heads);
   const int heads = p.Hq / a.mass_heads;  // query heads of the mass head
   const int rows = heads * p.T;
-  float add[kSlots] = {};
+  // slots that a row of the block can see (all, where the heads differ)
+  int64_t most = p.S;
+  if (!p.len_per_head || a.mass_heads > 1) most = min(most, (int64_t)p.len[p.len_per_head ? bm : b]);
+  const bool inside = slot < most;
+  float* to = a.mass + bm * p.S + slot;
+  float old[kSlots] = {}, add[kSlots] = {};
+  float4 y[kBatch];
+  const float* sc = a.sc + ((int64_t)b * p.T * p.Hq + m * heads) * a.sc_ld + slot;
+  auto batch = [&](int r0, int n) {
+#pragma unroll
+    for (int u = 0; u < kBatch; u++) {
+      const int r = r0 + u;
+      y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (u < n && inside)
+        y[u] = *reinterpret_cast<const float4*>(sc + ((int64_t)(r / heads) * p.Hq + r % heads) * a.sc_ld);
+    }
+  };
+  if (inside && run == 0) {
+#pragma unroll
+    for (int e = 0; e < kSlots; e++)
+      if (slot + e < p.S) old[e] = to[e];
+  }
   int seen = 0;  // the thread's slots that some row sees
   for (int r0 = 0; r0 < rows; r0 += kRowsAt) {
     const int n = min(kRowsAt, rows - r0);
+    const int step = (n + groups - 1) / groups;
+    const int i1 = min(n, run * step + step);  // this thread's rows of those held
+    batch(r0 + run * step, i1 - run * step);
     __syncthreads();
     load_rows(a, s, b, 0, m * heads, heads, r0, n);
     if (slot >= s.longest) continue;
     seen = max(seen, (int)min((int64_t)kSlots, s.longest - slot));
-    for (int i0 = 0; i0 < n; i0 += kBatch) {
-      float4 y[kBatch];
-#pragma unroll
-      for (int u = 0; u < kBatch; u++) {
-        const int i = i0 + u, r = r0 + i;
-        const bool in = i < n && slot < s.lim[i];
-        y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (in)
-          y[u] = *reinterpret_cast<const float4*>(
-              a.sc + (((int64_t)b * p.T + r / heads) * p.Hq + m * heads + r % heads) * a.sc_ld + slot);
-      }
+    for (int i0 = run * step; i0 < i1; i0 += kBatch) {
 #pragma unroll
       for (int u = 0; u < kBatch; u++) {
         const int i = i0 + u;
-        if (i >= n) break;
+        if (i >= i1) break;
         const float z = s.lse2[i];
         const int64_t left = s.lim[i] - slot;
         if (left > 0) add[0] += attn_ex2(y[u].x - z);
@@ -189,12 +211,24 @@ __device__ void mass_dense(const AttnArgs& a, int64_t block) {
         if (left > 2) add[2] += attn_ex2(y[u].z - z);
         if (left > 3) add[3] += attn_ex2(y[u].w - z);
       }
+      if (i0 + kBatch < i1) batch(r0 + i0 + kBatch, i1 - i0 - kBatch);
     }
   }
-  float* to = a.mass + bm * p.S + slot;
+  if (groups > 1) {
+    s_add[threadIdx.x] = make_float4(add[0], add[1], add[2], add[3]);
+    __syncthreads();
+    if (run > 0) return;
+    for (int g = 1; g < groups; g++) {
+      const float4 x = s_add[g * lanes + mine];
+      add[0] += x.x;
+      add[1] += x.y;
+      add[2] += x.z;
+      add[3] += x.w;
+    }
+  }
 #pragma unroll
   for (int e = 0; e < kSlots; e++)
-    if (e < seen) to[e] += add[e];
+    if (e < seen) to[e] = old[e] + add[e];
 }
 
 // Mass of listed slots.  One list holds a slot at most once, so its threads add
@@ -202,51 +236,74 @@ __device__ void mass_dense(const AttnArgs& a, int64_t block) {
 // KV head's when all heads share the mass) follow one another in one block.
 __device__ void mass_listed(const AttnArgs& a, int64_t block, int64_t per) {
   __shared__ MassRows s;
+  constexpr int E = 4;  // entries of a thread
   const attn_problem& p = a.p;
   const int lists_h = p.ids_per_head && a.mass_heads == 1 ? p.n_kv : 1;
   const int lists = p.T * lists_h;
   const int64_t bm = block / per;
   const int b = (int)(bm / a.mass_heads), m = (int)(bm % a.mass_heads);
-  const int heads = p.Hq / a.mass_heads / lists_h;  // query heads that read one list into one mass head
+  const int all = p.Hq / a.mass_heads;  // query heads of the mass head
+  const int heads = all / lists_h;      // of these, the ones that read one list
   float* mass = a.mass + bm * p.S;
+  // rows (t, query head) of the mass head: list q has rows q * heads ..
+  const bool once = lists * heads <= kRowsAt;
+  const int64_t first = block % per * kThreads + threadIdx.x, step = per * kThreads;
   for (int q = 0; q < lists; q++) {
-    const int t = q / lists_h;
-    const int hq0 = m * (p.Hq / a.mass_heads) + (q % lists_h) * heads;
+    const int t = q / lists_h, hq0 = m * all + (q % lists_h) * heads;
     const int32_t* list = p.ids + (p.ids_per_head ? (((int64_t)b * p.T + t) * p.n_kv + hq0 / a.G) * p.W
                                                   : ((int64_t)b * p.T + t) * p.W);
-    const int64_t row0 = ((int64_t)b * p.T + t) * p.Hq + hq0;
+    const float* sc = a.sc + (((int64_t)b * p.T + t) * p.Hq + hq0) * a.sc_ld;
     for (int r0 = 0; r0 < heads; r0 += kRowsAt) {
       const int n = min(kRowsAt, heads - r0);
-      __syncthreads();  // the previous list's additions are done
-      load_rows(a, s, b, t, hq0, heads, r0, n);
-      for (int64_t w = block % per * kThreads + threadIdx.x; w < p.W; w += per * kThreads) {
-        const int id = list[w];
-        if (id < 0 || id >= s.longest) continue;
-        float add = 0.f;
-        for (int i0 = 0; i0 < n; i0 += kBatch) {
-          float y[kBatch];
+      const int base = once ? q * heads : 0;  // of the list's rows in s
+      for (int64_t w0 = first; w0 - threadIdx.x < p.W; w0 += step * E) {
+        int id[E];
+        float add[E] = {};
 #pragma unroll
-          for (int u = 0; u < kBatch; u++) y[u] = i0 + u < n ? a.sc[(row0 + r0 + i0 + u) * a.sc_ld + w] : 0.f;
+        for (int e = 0; e < E; e++) id[e] = w0 + e * step < p.W ? list[w0 + e * step] : -1;
+        for (int i0 = 0; i0 < n; i0 += kBatch) {
+          float y[kBatch][E];
 #pragma unroll
           for (int u = 0; u < kBatch; u++)
-            if (i0 + u < n && id < s.lim[i0 + u]) add += attn_ex2(y[u] - s.lse2[i0 + u]);
+#pragma unroll
+            for (int e = 0; e < E; e++)
+              y[u][e] = i0 + u < n && w0 + e * step < p.W ? sc[(r0 + i0 + u) * a.sc_ld + w0 + e * step] : 0.f;
+          if (w0 == first && i0 == 0) {
+            // the previous list's additions are done; this one's rows
+            __syncthreads();
+            if (!once)
+              load_rows(a, s, b, t, hq0, heads, r0, n);
+            else if (q == 0)
+              load_rows(a, s, b, 0, m * all, all, 0, lists * heads);
+          }
+#pragma unroll
+          for (int u = 0; u < kBatch; u++)
+            if (i0 + u < n) {
+              const float z = s.lse2[base + i0 + u];
+              const int lim = s.lim[base + i0 + u];
+#pragma unroll
+              for (int e = 0; e < E; e++)
+                if (id[e] < lim) add[e] += attn_ex2(y[u][e] - z);
+            }
         }
-        atomicAdd(mass + id, add);
+#pragma unroll
+        for (int e = 0; e < E; e++)
+          if (id[e] >= 0 && id[e] < s.longest) atomicAdd(mass + id[e], add[e]);
       }
     }
   }
 }
 
-template <int D, bool BF16>
-__global__ void __launch_bounds__(kThreads, 2)
-    attn_finish_kernel(const __grid_constant__ AttnArgs a, int64_t join_blocks, int64_t per) {
+template <int D, bool BF16, bool LISTED>
+__global__ void __launch_bounds__(kThreads, LISTED ? 2 : 3)
+    attn_finish_kernel(const __grid_constant__ AttnArgs a, int64_t join_blocks, int64_t per, int row_groups) {
   grid_wait();
   if (blockIdx.x < join_blocks)
     join_rows<D, BF16>(a);
-  else if (a.p.ids)
+  else if (LISTED)
     mass_listed(a, blockIdx.x - join_blocks, per);
   else
-    mass_dense(a, blockIdx.x - join_blocks);
+    mass_dense(a, blockIdx.x - join_blocks, row_groups);
 }
 
 template <int D, bool BF16>
@@ -254,18 +311,21 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
   const attn_problem& p = a.p;
   const int64_t rows = (int64_t)p.B * p.T * p.Hq;
   const int64_t join = (rows + kWarps - 1) / kWarps;
+  // a slot's rows are spread over up to four threads where there are many
+  const int mass_rows = p.Hq / a.mass_heads * p.T, groups = mass_rows >= 32 ? 4 : mass_rows >= 16 ? 2 : 1;
   int64_t per = 0;  // mass blocks of one (b, mass head)
   if (a.mass && a.parts_private) {
-    per = (p.S + kThreads * kSlots - 1) / (kThreads * kSlots);
+    per = (p.S + kThreads / groups * kSlots - 1) / (kThreads / groups * kSlots);
     if (p.ids) {
       const bool one = p.T == 1 && !(p.ids_per_head && a.mass_heads == 1 && p.n_kv > 1);
-      per = one ? (p.W + kThreads - 1) / kThreads : 1;
+      per = one ? std::min<int64_t>((p.W + kThreads - 1) / kThreads, 2 * sm_count() / ((int64_t)p.B * a.mass_heads) + 1) : 1;
     }
   }
   const int64_t blocks = join + (int64_t)p.B * a.mass_heads * per;
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
-  return launch_after(attn_finish_kernel<D, BF16>, dim3((unsigned)blocks), kThreads, 0, st,
-                      a.parts_prefix + a.parts_private > 0, a, join, per);
+  auto kern = p.ids && per ? attn_finish_kernel<D, BF16, true> : attn_finish_kernel<D, BF16, false>;
+  return launch_after(kern, dim3((unsigned)blocks), kThreads, 0, st, a.parts_prefix + a.parts_private > 0, a, join, per,
+                      groups);
 }
 
 }  // namespace

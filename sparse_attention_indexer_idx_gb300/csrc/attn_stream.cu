@@ -1,13 +1,20 @@
 // Attention over few rows per key sequence, bound by reading keys and values:
 // the private caches of a decode step, and a shared prefix under a small batch.
 //
-// Mapping.  One block takes one (key sequence, KV head, tile of up to 32 rows,
-// piece of the keys).  Its four warps are independent streams: warp w takes
-// every fourth tile of KT keys, copies the keys and values with 16-byte
-// cp.async into a ring of its own (swizzled, so ldmatrix is free of bank
-// conflicts) and keeps the running maximum, sum and output of its keys in
-// registers; nothing but the warp itself waits for a copy.  The four
-// results are joined through shared memory at the end of the piece.
+// Mapping.  The key sequences (the prefix, then every request's cache or list)
+// form one line of key units; it is cut evenly over groups of blocks, with one
+// block of a group for each KV head (and tile of up to 32 rows).  The heads of a
+// group run side by side, so their rows of a cache, which lie next to one
+// another, are read together, and all groups end together however ragged the
+// lengths are.  A group that starts or ends inside a sequence leaves one of
+// several partial results of it.
+//
+// A block's four warps are independent streams: warp w takes every fourth tile
+// of KT keys, copies the keys and values with 16-byte cp.async into a ring of
+// its own (swizzled, so ldmatrix is free of bank conflicts) and keeps the
+// running maximum, sum and output of its keys in registers; nothing but the
+// warp itself waits for a copy.  The four results are joined through shared
+// memory at the end of a sequence or of the block's share.
 //
 // The products use mma.sync (16 x 8 x 16): a decode row group is 1 to 32 rows,
 // so the tensor work is a few percent of the time the bytes take, and the
@@ -71,6 +78,7 @@ struct StreamCfg {
   static constexpr int ROWB = D * 2;
   static constexpr int CH = ROWB / 16;            // 16-byte chunks of a row
   static constexpr int STAGE = 2 * KT * ROWB;
+  static constexpr int UNIT = kWarps * KT;        // keys of the four warps' tiles
   static constexpr int RING = kWarps * kStages * STAGE;
   static constexpr int SLOTS = kWarps * kStages * KT * 4;  // slot numbers of gathered tiles
 };
@@ -81,29 +89,28 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
   return (uint32_t)(r * D * 2 + ((c ^ (r & 7)) << 4));
 }
 
-// What one block works on: a contiguous piece [k0, k1) of a key sequence (or
-// of an id list) and up to 16*MT rows that read it.
+// What a block works on at a time: the units [u0, u1) of a key sequence (or of
+// an id list), and up to 16*MT rows that read it.
 struct StreamItem {
   const char* k;
   const char* v;
   int64_t ks, vs;   // bytes between keys
   int64_t k0, k1;
-  int part;
-  int h, b, t;      // t: token of a gathered list, b: request of private items
-  int row0, rows;   // rows row0 .. row0 + n - 1 of `rows`
+  int rows, row0;   // rows row0 .. of `rows`
 };
 
-// block: number of this item among those of its kind, row tiles of a piece next
-// to one another (they read the same keys), then the sequences, then the pieces.
+// b, t: request, and token of a gathered list; [u0, u1): this block's units of
+// the sequence's `units`; part: number of the partial result.
 template <int D, int MT, bool BF16, bool GATHER, bool PREFIX>
-__device__ __forceinline__ void stream_item(const AttnArgs& a, int64_t block) {
+__device__ __forceinline__ void stream_item(const AttnArgs& a, int h, int tile, int b, int t, int u0, int u1, int units,
+                                            int part) {
   using C = StreamCfg<D, MT>;
   constexpr int KT = C::KT, NT = KT / 8, KS = D / 16, CH = C::CH, kStages = C::kStages;
   constexpr int R = 16 * MT;
   extern __shared__ __align__(1024) char smem[];
   char* sring = smem;
   int* sslot = reinterpret_cast<int*>(smem + C::RING);
-  char* sq = smem + C::RING + (GATHER ? C::SLOTS : 0);
+  char* sq = smem + C::RING + C::SLOTS;
   __shared__ int64_t s_rowid[R];  // (b*T + t)*Hq + hq, or -1
   __shared__ int s_lim[R];        // keys below this index are visible to the row
   __shared__ float2 s_ml[kWarps][R];
@@ -111,36 +118,23 @@ __device__ __forceinline__ void stream_item(const AttnArgs& a, int64_t block) {
 
   const attn_problem& p = a.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-  // ---- the item of this block
   StreamItem it;
-  const int64_t rows_all = PREFIX ? (int64_t)p.B * p.T * a.G : GATHER ? a.G : (int64_t)p.T * a.G;
-  const int64_t seqs = PREFIX ? p.n_kv : (int64_t)p.B * (GATHER ? p.T : 1) * p.n_kv;
-  const int64_t tiles = (rows_all + R - 1) / R;
-  const int tile = (int)(block % tiles);
-  const int64_t seq = block / tiles % seqs;
-  it.part = (int)(block / tiles / seqs);
-  it.rows = (int)rows_all;
+  it.rows = PREFIX ? p.B * p.T * a.G : GATHER ? a.G : p.T * a.G;
+  it.row0 = tile * R;
+  const int nrow = min(R, it.rows - it.row0);
+  if (nrow <= 0) return;  // a tile that only other sequences have
   if (PREFIX) {
-    it.h = (int)seq;
-    it.b = it.t = 0;
-    it.k = (const char*)p.pk + 2 * it.h * p.pk_stride_h;
-    it.v = (const char*)p.pv + 2 * it.h * p.pv_stride_h;
+    it.k = (const char*)p.pk + 2 * h * p.pk_stride_h;
+    it.v = (const char*)p.pv + 2 * h * p.pv_stride_h;
     it.ks = 2 * p.pk_stride_s;
     it.vs = 2 * p.pv_stride_s;
   } else {
-    it.h = (int)(seq % p.n_kv);
-    const int64_t bt = seq / p.n_kv;
-    it.b = GATHER ? (int)(bt / p.T) : (int)bt;
-    it.t = GATHER ? (int)(bt % p.T) : 0;
-    it.k = (const char*)p.k + 2 * ((int64_t)it.b * p.k_stride_b + it.h * p.k_stride_h);
-    it.v = (const char*)p.v + 2 * ((int64_t)it.b * p.v_stride_b + it.h * p.v_stride_h);
+    it.k = (const char*)p.k + 2 * ((int64_t)b * p.k_stride_b + h * p.k_stride_h);
+    it.v = (const char*)p.v + 2 * ((int64_t)b * p.v_stride_b + h * p.v_stride_h);
     it.ks = 2 * p.k_stride_s;
     it.vs = 2 * p.v_stride_s;
   }
-  it.row0 = tile * R;
-  const int nrow = min(R, it.rows - it.row0);
-  const int64_t priv = PREFIX ? 0 : attn_len(p, it.b, it.h);
+  const int64_t priv = PREFIX ? 0 : attn_len(p, b, h);
   if (threadIdx.x < R) {
     const int i = threadIdx.x;
     int64_t id = -1;
@@ -148,40 +142,32 @@ __device__ __forceinline__ void stream_item(const AttnArgs& a, int64_t block) {
     if (i < nrow) {
       const int r = it.row0 + i;
       const int g = r % a.G, bt = r / a.G;
-      int b, t;
-      if (PREFIX) {
-        b = bt / p.T;
-        t = bt % p.T;
-        lim = (int)attn_prefix_len(p, b);
-      } else {
-        b = it.b;
-        t = GATHER ? it.t : bt;
-        lim = max(0, (int)priv - p.T + t + 1);
-      }
-      id = ((int64_t)b * p.T + t) * p.Hq + (int64_t)it.h * a.G + g;
+      const int rb = PREFIX ? bt / p.T : b, rt = PREFIX ? bt % p.T : GATHER ? t : bt;
+      lim = PREFIX ? (int)attn_prefix_len(p, rb) : max(0, (int)priv - p.T + rt + 1);
+      id = ((int64_t)rb * p.T + rt) * p.Hq + (int64_t)h * a.G + g;
     }
     s_rowid[i] = id;
     s_lim[i] = lim;
   }
   __syncthreads();
-  // The piece: the private rows' own length is split evenly, so that short
-  // rows still use every block of theirs.
   int64_t n = 0;
   if (GATHER) {
     n = s_lim[0] > 0 ? p.W : 0;
   } else {
     for (int i = 0; i < nrow; i++) n = max(n, (int64_t)s_lim[i]);
   }
-  {
-    const int64_t parts = PREFIX ? a.parts_prefix : a.parts_private;
-    const int64_t step = (((n + parts - 1) / parts) + KT - 1) / KT * KT;
-    it.k0 = min(n, step * it.part);
-    it.k1 = min(n, it.k0 + step);
-  }
+  it.k0 = (int64_t)u0 * C::UNIT;
+  it.k1 = min(n, (int64_t)u1 * C::UNIT);
   const int parts_all = a.parts_prefix + a.parts_private;
-  const int part = it.part + (PREFIX ? 0 : a.parts_prefix);
+  const int parts = PREFIX ? a.parts_prefix : a.parts_private, at = PREFIX ? 0 : a.parts_prefix;
+  // the block with a sequence's last unit marks the partial results that the
+  // sequence does not have
+  if (u1 == units && threadIdx.x < nrow)
+    for (int i = part + 1; i < parts; i++) a.pml[s_rowid[threadIdx.x] * parts_all + at + i] = make_float2(-INFINITY, 0.f);
+  part += at;
   if (it.k0 >= it.k1) {
     if (threadIdx.x < nrow) a.pml[s_rowid[threadIdx.x] * parts_all + part] = make_float2(-INFINITY, 0.f);
+    __syncthreads();
     return;
   }
 
@@ -213,8 +199,7 @@ __device__ __forceinline__ void stream_item(const AttnArgs& a, int64_t block) {
   int* slots = sslot + warp * kStages * KT;
   const int32_t* list = nullptr;
   if (GATHER)
-    list = p.ids + (p.ids_per_head ? (((int64_t)it.b * p.T + it.t) * p.n_kv + it.h) * p.W
-                                   : ((int64_t)it.b * p.T + it.t) * p.W);
+    list = p.ids + (p.ids_per_head ? (((int64_t)b * p.T + t) * p.n_kv + h) * p.W : ((int64_t)b * p.T + t) * p.W);
   const int glim = GATHER ? s_lim[0] : 0;
 
   int32_t next_id = -1;  // GATHER: lane i holds list entry i of the next tile to copy
@@ -395,22 +380,22 @@ __device__ __forceinline__ void stream_item(const AttnArgs& a, int64_t block) {
     for (int e = 0; e < 2; e++) {
       const int r = m * 16 + (lane >> 2) + 8 * e;
       if (r >= nrow) continue;
-      float t = -INFINITY;
+      float top = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kWarps; w++) t = fmaxf(t, s_ml[w][r].x);
-      const float f = t == -INFINITY ? 0.f : attn_ex2(mx[m][e] - t);
+      for (int w = 0; w < kWarps; w++) top = fmaxf(top, s_ml[w][r].x);
+      const float f = top == -INFINITY ? 0.f : attn_ex2(mx[m][e] - top);
 #pragma unroll
       for (int i = 0; i < D / 8; i++)
         *reinterpret_cast<float2*>(so + ((size_t)warp * R + r) * D + 8 * i + 2 * (lane & 3)) =
             make_float2(o[m][i][2 * e] * f, o[m][i][2 * e + 1] * f);
     }
   if (threadIdx.x < nrow) {
-    float t = -INFINITY, l = 0.f;
-    for (int w = 0; w < kWarps; w++) t = fmaxf(t, s_ml[w][threadIdx.x].x);
+    float top = -INFINITY, l = 0.f;
+    for (int w = 0; w < kWarps; w++) top = fmaxf(top, s_ml[w][threadIdx.x].x);
     for (int w = 0; w < kWarps; w++)
-      if (t != -INFINITY) l += s_ml[w][threadIdx.x].y * attn_ex2(s_ml[w][threadIdx.x].x - t);
-    s_tot[threadIdx.x] = make_float2(t, l);
-    a.pml[s_rowid[threadIdx.x] * parts_all + part] = make_float2(t, l);
+      if (top != -INFINITY) l += s_ml[w][threadIdx.x].y * attn_ex2(s_ml[w][threadIdx.x].x - top);
+    s_tot[threadIdx.x] = make_float2(top, l);
+    a.pml[s_rowid[threadIdx.x] * parts_all + part] = make_float2(top, l);
   }
   __syncthreads();
   for (int i = threadIdx.x; i < nrow * (D / 4); i += blockDim.x) {
@@ -427,56 +412,140 @@ __device__ __forceinline__ void stream_item(const AttnArgs& a, int64_t block) {
     }
     *reinterpret_cast<float4*>(a.po + (s_rowid[r] * parts_all + part) * D + d) = x;
   }
+  __syncthreads();  // the next item takes this memory
 }
 
-// Prefix items (if this kernel has them) come first: they are the longer ones.
+// Units of request b's cache: by its longest head, at least one, so that every
+// sequence has a place on the line.
+template <int UNIT>
+__device__ __forceinline__ int cache_units(const attn_problem& p, int b) {
+  int n = 0;
+  for (int h = 0; h < (p.len_per_head ? p.n_kv : 1); h++) {
+    const int x = p.len[p.len_per_head ? (int64_t)b * p.n_kv + h : b];
+    if (x <= p.S) n = max(n, x);
+  }
+  return max(1, (n + UNIT - 1) / UNIT);
+}
+
 template <int D, int MT, bool BF16, bool GATHER>
 __global__ void __launch_bounds__(32 * kWarps, MT == 1 ? 3 : 2)
-    attn_stream_kernel(const __grid_constant__ AttnArgs a, int64_t prefix_blocks) {
+    attn_stream_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ StreamLine line) {
+  using C = StreamCfg<D, MT>;
+  constexpr int NT = 32 * kWarps;
+  __shared__ int64_t s_sum[kWarps];
+  __shared__ int64_t s_start;
+  __shared__ int s_seq;
   grid_let_next_start();
-  if (blockIdx.x < prefix_blocks)
-    stream_item<D, MT, BF16, false, true>(a, blockIdx.x);
-  else
-    stream_item<D, MT, BF16, GATHER, false>(a, blockIdx.x - prefix_blocks);
+  const attn_problem& p = a.p;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int member = blockIdx.x % line.members, group = blockIdx.x / line.members;
+  const int h = member % p.n_kv, tile = member / p.n_kv;
+  const int seqs = line.seqs;                              // private sequences
+  const int list_units = (int)((p.W + C::UNIT - 1) / C::UNIT);  // of a gathered list
+
+  // the line's length, and each thread's share of the requests on it
+  int64_t mine = 0, total;
+  const int per = (seqs + NT - 1) / NT;
+  const int b0 = min(seqs, tid * per), b1 = min(seqs, b0 + per);
+  if (GATHER) {
+    total = line.prefix_units + (int64_t)seqs * list_units;
+  } else {
+    for (int b = b0; b < b1; b++) mine += cache_units<C::UNIT>(p, b);
+    int64_t incl = mine;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, incl, s);
+      if (lane >= s) incl += y;
+    }
+    if (lane == 31) s_sum[warp] = incl;
+    __syncthreads();
+    total = line.prefix_units;
+    int64_t before = line.prefix_units;
+    for (int w = 0; w < kWarps; w++) {
+      total += s_sum[w];
+      if (w < warp) before += s_sum[w];
+    }
+    mine = before + incl - mine;  // where this thread's requests begin
+  }
+  const int64_t share = max((total + line.groups - 1) / line.groups, (int64_t)line.least);
+  int64_t lo = share * group;
+  const int64_t hi = min(total, lo + share);
+  if (lo >= hi) {
+    grid_wait();
+    return;
+  }
+  if (lo < line.prefix_units) {
+    const int u1 = (int)min(hi, (int64_t)line.prefix_units);
+    stream_item<D, MT, BF16, false, true>(a, h, tile, 0, 0, (int)lo, u1, line.prefix_units, group);
+    lo = u1;
+  }
+  if (lo < hi) {
+    int seq, units;
+    int64_t start;  // of the sequence that holds lo
+    if (GATHER) {
+      seq = (int)((lo - line.prefix_units) / list_units);
+      start = line.prefix_units + (int64_t)seq * list_units;
+      units = list_units;
+    } else {
+      __syncthreads();
+      int64_t at = mine;
+      for (int b = b0; b < b1; b++) {
+        const int u = cache_units<C::UNIT>(p, b);
+        if (at <= lo && lo < at + u) {
+          s_seq = b;
+          s_start = at;
+        }
+        at += u;
+      }
+      __syncthreads();
+      seq = s_seq;
+      start = s_start;
+      units = cache_units<C::UNIT>(p, seq);
+    }
+    while (true) {
+      const int u0 = (int)(lo - start), u1 = (int)min((int64_t)units, hi - start);
+      stream_item<D, MT, BF16, GATHER, false>(a, h, tile, GATHER ? seq / p.T : seq, GATHER ? seq % p.T : 0, u0, u1, units,
+                                              group - (int)(start / share));
+      start += units;
+      lo = start;
+      if (lo >= hi) break;
+      seq++;
+      if (!GATHER) units = cache_units<C::UNIT>(p, seq);
+    }
+  }
   // the finish kernel waits for this grid alone: it ends behind the one before it
   grid_wait();
 }
 
-int64_t tiles_of(int64_t rows, int mt) { return (rows + 16 * mt - 1) / (16 * mt); }
-
 template <int D, int MT, bool BF16, bool GATHER>
-cudaError_t launch(const AttnArgs& a, bool prefix, bool after, cudaStream_t st) {
+cudaError_t launch(const AttnArgs& a, const StreamLine& line, bool after, cudaStream_t st) {
   using C = StreamCfg<D, MT>;
-  const attn_problem& p = a.p;
-  const int smem = C::RING + (GATHER ? C::SLOTS : 0) + 16 * MT * D * 2;
+  static_assert(C::UNIT == stream_unit(D), "the plan counts in these units");
+  const int smem = C::RING + C::SLOTS + 16 * MT * D * 2;
   auto kern = attn_stream_kernel<D, MT, BF16, GATHER>;
   static KernelReady ready;
   cudaError_t e = ready.once([&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
   if (e != cudaSuccess) return e;
-  const int64_t np = prefix ? a.parts_prefix * p.n_kv * tiles_of((int64_t)p.B * p.T * a.G, MT) : 0;
-  const int64_t ns = a.parts_private * (int64_t)p.B * p.n_kv *
-                     (GATHER ? p.T * tiles_of(a.G, MT) : tiles_of((int64_t)p.T * a.G, MT));
-  if (np + ns > INT32_MAX) return cudaErrorInvalidConfiguration;
-  return launch_after(kern, dim3((unsigned)(np + ns)), 32 * kWarps, smem, st, after, a, np);
+  return launch_after(kern, dim3((unsigned)(line.members * line.groups)), 32 * kWarps, smem, st, after, a, line);
 }
 
 template <int D, bool BF16, bool GATHER>
-cudaError_t launch_rows(const AttnArgs& a, bool prefix, bool after, cudaStream_t st) {
-  return a.stream_rows <= 16 ? launch<D, 1, BF16, GATHER>(a, prefix, after, st)
-                             : launch<D, 2, BF16, GATHER>(a, prefix, after, st);
+cudaError_t launch_rows(const AttnArgs& a, const StreamLine& line, bool after, cudaStream_t st) {
+  return line.row_tile == 16 ? launch<D, 1, BF16, GATHER>(a, line, after, st)
+                             : launch<D, 2, BF16, GATHER>(a, line, after, st);
 }
 
 template <int D, bool BF16>
-cudaError_t launch_kind(const AttnArgs& a, bool prefix, bool after, cudaStream_t st) {
-  return a.p.ids ? launch_rows<D, BF16, true>(a, prefix, after, st) : launch_rows<D, BF16, false>(a, prefix, after, st);
+cudaError_t launch_kind(const AttnArgs& a, const StreamLine& line, bool after, cudaStream_t st) {
+  return a.p.ids ? launch_rows<D, BF16, true>(a, line, after, st) : launch_rows<D, BF16, false>(a, line, after, st);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_stream(const AttnArgs& a, bool prefix, bool after, cudaStream_t st) {
+cudaError_t launch_attn_stream(const AttnArgs& a, const StreamLine& line, bool after, cudaStream_t st) {
   const bool bf = a.p.dtype == IDX_BF16;
-  if (a.p.D == 128) return bf ? launch_kind<128, true>(a, prefix, after, st) : launch_kind<128, false>(a, prefix, after, st);
-  return bf ? launch_kind<64, true>(a, prefix, after, st) : launch_kind<64, false>(a, prefix, after, st);
+  if (a.p.D == 128) return bf ? launch_kind<128, true>(a, line, after, st) : launch_kind<128, false>(a, line, after, st);
+  return bf ? launch_kind<64, true>(a, line, after, st) : launch_kind<64, false>(a, line, after, st);
 }
 
 }  // namespace idx
