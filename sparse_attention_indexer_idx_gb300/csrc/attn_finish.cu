@@ -17,7 +17,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSlots = 4;    // consecutive slots of a thread: one 16-byte load per row
-constexpr int kRowsAt = 128; // rows whose normalisers are held at a time
+constexpr int kRowsAt = 512; // rows whose normalisers are held at a time
 constexpr int kBatch = 8;    // rows loaded before the first is used
 
 template <int D, bool BF16>
@@ -152,83 +152,98 @@ __device__ __forceinline__ void load_rows(const AttnArgs& a, MassRows& s, int b,
 }
 
 // Mass of every slot.  A slot's rows are split over `groups` threads in equal
-// runs; each sums its own in row order, then the runs are added in order.  The
-// scores and the old masses do not depend on the normalisers: the first of
-// them are under way while those are formed.
-__device__ void mass_dense(const AttnArgs& a, int64_t block, int groups) {
+// runs; each sums its own in row order, then the runs are added in order.  A
+// block takes every per-th run of slots: the rows' normalisers, which take more
+// instructions than the sums of a few hundred slots, are formed once for them.
+__device__ __forceinline__ void mass_dense(const AttnArgs& a, int64_t block, int per, int groups) {
   __shared__ MassRows s;
   __shared__ float4 s_add[kThreads];
   const attn_problem& p = a.p;
   const int lanes = kThreads / groups;  // threads next to one another in the slots
-  const int64_t per = (p.S + lanes * kSlots - 1) / (lanes * kSlots);  // blocks of one (b, mass head)
   const int64_t bm = block / per;
   const int mine = threadIdx.x % lanes, run = threadIdx.x / lanes;
-  const int64_t slot = (block % per * lanes + mine) * kSlots;
   const int b = (int)(bm / a.mass_heads), m = (int)(bm % a.mass_heads);
   const int heads = p.Hq / a.mass_heads;  // query heads of the mass head
   const int rows = heads * p.T;
   // slots that a row of the block can see (all, where the heads differ)
-  int64_t most = p.S;
-  if (!p.len_per_head || a.mass_heads > 1) most = min(most, (int64_t)p.len[p.len_per_head ? bm : b]);
-  const bool inside = slot < most;
-  float* to = a.mass + bm * p.S + slot;
-  float old[kSlots] = {}, add[kSlots] = {};
-  float4 y[kBatch];
-  const float* sc = a.sc + ((int64_t)b * p.T * p.Hq + m * heads) * a.sc_ld + slot;
-  auto batch = [&](int r0, int n) {
-#pragma unroll
-    for (int u = 0; u < kBatch; u++) {
-      const int r = r0 + u;
-      y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (u < n && inside)
-        y[u] = *reinterpret_cast<const float4*>(sc + ((int64_t)(r / heads) * p.Hq + r % heads) * a.sc_ld);
-    }
-  };
-  if (inside && run == 0) {
-#pragma unroll
-    for (int e = 0; e < kSlots; e++)
-      if (slot + e < p.S) old[e] = to[e];
-  }
-  int seen = 0;  // the thread's slots that some row sees
+  int most = (int)p.S;
+  if (!p.len_per_head || a.mass_heads > 1) most = min(most, p.len[p.len_per_head ? bm : b]);
+  const int first = (int)(block % per) * lanes * kSlots;
+  if (first >= most) return;
   for (int r0 = 0; r0 < rows; r0 += kRowsAt) {
     const int n = min(kRowsAt, rows - r0);
-    const int step = (n + groups - 1) / groups;
-    const int i1 = min(n, run * step + step);  // this thread's rows of those held
-    batch(r0 + run * step, i1 - run * step);
-    __syncthreads();
-    load_rows(a, s, b, 0, m * heads, heads, r0, n);
-    if (slot >= s.longest) continue;
-    seen = max(seen, (int)min((int64_t)kSlots, s.longest - slot));
-    for (int i0 = run * step; i0 < i1; i0 += kBatch) {
+    const int len = (n + groups - 1) / groups;
+    // this thread's rows of those held; rows of one token lie next to one
+    // another, the next token's Hq rows on
+    const int i0 = min(n, run * len), i1 = min(n, i0 + len);
+    const int token0 = (r0 + i0) / heads, in_token0 = (r0 + i0) % heads;
+    const float* row0 = a.sc + (((int64_t)b * p.T + token0) * p.Hq + m * heads + in_token0) * a.sc_ld;
+    const int64_t next_token = (int64_t)(p.Hq - heads) * a.sc_ld;
+    float4 y[kBatch];
+    int i, in_token;
+    const float* y_at;
+    auto begin = [&](int slot) {
+      i = i0;
+      in_token = in_token0;
+      y_at = row0 + slot;
+    };
+    auto batch = [&](bool inside) {
 #pragma unroll
       for (int u = 0; u < kBatch; u++) {
-        const int i = i0 + u;
-        if (i >= i1) break;
-        const float z = s.lse2[i];
-        const int64_t left = s.lim[i] - slot;
-        if (left > 0) add[0] += attn_ex2(y[u].x - z);
-        if (left > 1) add[1] += attn_ex2(y[u].y - z);
-        if (left > 2) add[2] += attn_ex2(y[u].z - z);
-        if (left > 3) add[3] += attn_ex2(y[u].w - z);
+        y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i + u < i1 && inside) y[u] = *reinterpret_cast<const float4*>(y_at);
+        y_at += a.sc_ld;
+        if (++in_token == heads) {
+          in_token = 0;
+          y_at += next_token;
+        }
       }
-      if (i0 + kBatch < i1) batch(r0 + i0 + kBatch, i1 - i0 - kBatch);
-    }
-  }
-  if (groups > 1) {
-    s_add[threadIdx.x] = make_float4(add[0], add[1], add[2], add[3]);
+    };
+    begin(first + mine * kSlots);
+    batch(first + mine * kSlots < most);
     __syncthreads();
-    if (run > 0) return;
-    for (int g = 1; g < groups; g++) {
-      const float4 x = s_add[g * lanes + mine];
-      add[0] += x.x;
-      add[1] += x.y;
-      add[2] += x.z;
-      add[3] += x.w;
+    load_rows(a, s, b, 0, m * heads, heads, r0, n);
+    for (int at = first; at < most; at += per * lanes * kSlots) {
+      const int slot = at + mine * kSlots;
+      const bool inside = slot < most;
+      if (at != first) {
+        begin(slot);
+        batch(inside);
+      }
+      float add[kSlots] = {};
+      while (i < i1) {
+#pragma unroll
+        for (int u = 0; u < kBatch; u++) {
+          if (i + u >= i1) break;
+          const float z = s.lse2[i + u];
+          const int left = s.lim[i + u] - slot;
+          if (left > 0) add[0] += attn_ex2(y[u].x - z);
+          if (left > 1) add[1] += attn_ex2(y[u].y - z);
+          if (left > 2) add[2] += attn_ex2(y[u].z - z);
+          if (left > 3) add[3] += attn_ex2(y[u].w - z);
+        }
+        i += kBatch;
+        if (i < i1) batch(inside);
+      }
+      if (groups > 1) {
+        __syncthreads();
+        s_add[threadIdx.x] = make_float4(add[0], add[1], add[2], add[3]);
+        __syncthreads();
+        if (run > 0) continue;
+        for (int g = 1; g < groups; g++) {
+          const float4 x = s_add[g * lanes + mine];
+          add[0] += x.x;
+          add[1] += x.y;
+          add[2] += x.z;
+          add[3] += x.w;
+        }
+      }
+      float* to = a.mass + bm * p.S + slot;
+#pragma unroll
+      for (int e = 0; e < kSlots; e++)
+        if (slot + e < most) to[e] += add[e];
     }
   }
-#pragma unroll
-  for (int e = 0; e < kSlots; e++)
-    if (e < seen) to[e] = old[e] + add[e];
 }
 
 // Mass of listed slots.  One list holds a slot at most once, so its threads add
@@ -295,7 +310,7 @@ __device__ void mass_listed(const AttnArgs& a, int64_t block, int64_t per) {
 }
 
 template <int D, bool BF16, bool LISTED>
-__global__ void __launch_bounds__(kThreads, LISTED ? 2 : 3)
+__global__ void __launch_bounds__(kThreads, LISTED ? 2 : 4)
     attn_finish_kernel(const __grid_constant__ AttnArgs a, int64_t join_blocks, int64_t per, int row_groups) {
   grid_wait();
   if (blockIdx.x < join_blocks)
@@ -303,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, LISTED ? 2 : 3)
   else if (LISTED)
     mass_listed(a, blockIdx.x - join_blocks, per);
   else
-    mass_dense(a, blockIdx.x - join_blocks, row_groups);
+    mass_dense(a, blockIdx.x - join_blocks, (int)per, row_groups);
 }
 
 template <int D, bool BF16>
@@ -315,7 +330,9 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
   const int mass_rows = p.Hq / a.mass_heads * p.T, groups = mass_rows >= 32 ? 4 : mass_rows >= 16 ? 2 : 1;
   int64_t per = 0;  // mass blocks of one (b, mass head)
   if (a.mass && a.parts_private) {
-    per = (p.S + kThreads / groups * kSlots - 1) / (kThreads / groups * kSlots);
+    const int64_t bms = (int64_t)p.B * a.mass_heads;
+    per = std::min((p.S + kThreads / groups * kSlots - 1) / (kThreads / groups * kSlots),
+                   std::max<int64_t>(1, (4 * sm_count() + bms - 1) / bms));  // four blocks fit an SM
     if (p.ids) {
       const bool one = p.T == 1 && !(p.ids_per_head && a.mass_heads == 1 && p.n_kv > 1);
       per = one ? std::min<int64_t>((p.W + kThreads - 1) / kThreads, 2 * sm_count() / ((int64_t)p.B * a.mass_heads) + 1) : 1;

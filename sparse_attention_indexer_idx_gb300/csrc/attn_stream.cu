@@ -171,27 +171,6 @@ __device__ __forceinline__ void stream_item(const AttnArgs& a, int h, int tile, 
     return;
   }
 
-  // ---- queries: rows into shared memory, then operand fragments
-  for (int i = threadIdx.x; i < R * CH; i += blockDim.x) {
-    const int r = i / CH, c = i % CH;
-    const int64_t id = s_rowid[r];
-    uint4 x = make_uint4(0, 0, 0, 0);
-    if (id >= 0) {
-      const int64_t bt = id / p.Hq;
-      const int hq = (int)(id % p.Hq);
-      const int64_t e = (bt / p.T) * p.q_stride_b + (bt % p.T) * p.q_stride_t + hq * p.q_stride_h;
-      x = __ldg(reinterpret_cast<const uint4*>((const char*)p.q + 2 * e) + c);
-    }
-    *reinterpret_cast<uint4*>(sq + swz<D>(r, c)) = x;
-  }
-  __syncthreads();
-  uint32_t qf[MT][KS][4];
-#pragma unroll
-  for (int m = 0; m < MT; m++)
-#pragma unroll
-    for (int s = 0; s < KS; s++)
-      ldsm_x4(qf[m][s], smem_u32(sq) + swz<D>(m * 16 + (lane & 15), 2 * s + (lane >> 4)));
-
   // ---- this warp's tiles: w, w + kWarps, ... of the piece
   const int ntile = (int)((it.k1 - it.k0 + KT - 1) / KT);
   const int mine = (ntile - warp + kWarps - 1) / kWarps;
@@ -236,6 +215,31 @@ __device__ __forceinline__ void stream_item(const AttnArgs& a, int h, int tile, 
     cp_async_commit();
   };
 
+  load_ids(0);
+#pragma unroll
+  for (int j = 0; j < kStages - 1; j++) copy_tile(j);
+
+  // ---- queries: rows into shared memory, then operand fragments
+  for (int i = threadIdx.x; i < R * CH; i += blockDim.x) {
+    const int r = i / CH, c = i % CH;
+    const int64_t id = s_rowid[r];
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (id >= 0) {
+      const int64_t bt = id / p.Hq;
+      const int hq = (int)(id % p.Hq);
+      const int64_t e = (bt / p.T) * p.q_stride_b + (bt % p.T) * p.q_stride_t + hq * p.q_stride_h;
+      x = __ldg(reinterpret_cast<const uint4*>((const char*)p.q + 2 * e) + c);
+    }
+    *reinterpret_cast<uint4*>(sq + swz<D>(r, c)) = x;
+  }
+  __syncthreads();
+  uint32_t qf[MT][KS][4];
+#pragma unroll
+  for (int m = 0; m < MT; m++)
+#pragma unroll
+    for (int s = 0; s < KS; s++)
+      ldsm_x4(qf[m][s], smem_u32(sq) + swz<D>(m * 16 + (lane & 15), 2 * s + (lane >> 4)));
+
   float o[MT][D / 8][4];
   float mx[MT][2], sum[MT][2];
   int lim[MT][2];
@@ -256,9 +260,6 @@ __device__ __forceinline__ void stream_item(const AttnArgs& a, int h, int tile, 
     }
   }
 
-  load_ids(0);
-#pragma unroll
-  for (int j = 0; j < kStages - 1; j++) copy_tile(j);
   for (int j = 0; j < mine; j++) {
     cp_async_wait_group<kStages - 2>();
     __syncwarp();  // every lane's copies of tile j have landed, every lane is done with tile j - 1
