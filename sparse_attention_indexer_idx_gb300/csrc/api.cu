@@ -120,7 +120,7 @@ static idx_status check_attn(const attn_problem* p) {
   if (p->D != 64 && p->D != 128) return fail(IDX_ERR_UNSUPPORTED, "D=%d (64 or 128)", p->D);
   // bounds that keep grids, row counts and key indices inside 32 bits
   if (p->S > (1 << 30) || p->P > (1 << 30) || p->W > (1 << 30) ||
-      (int64_t)p->B * p->T > ((int64_t)1 << 30) / p->Hq || (int64_t)p->T * p->Hq > (1 << 20))
+      (int64_t)p->B * p->T > ((int64_t)1 << 30) / p->Hq || (int64_t)p->T * p->Hq > (1 << 20) || !attn_shared_fits(*p))
     return fail(IDX_ERR_UNSUPPORTED, "problem too large (B=%d T=%d Hq=%d S=%lld P=%lld W=%lld)", p->B, p->T, p->Hq,
                 (long long)p->S, (long long)p->P, (long long)p->W);
   if (!(p->scale == p->scale) || p->scale - p->scale != 0.f) return fail(IDX_ERR_INVALID_ARG, "scale is not finite");

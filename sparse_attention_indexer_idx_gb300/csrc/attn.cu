@@ -13,8 +13,8 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // Keys of the private part that a row can see at most.
 int64_t private_keys(const attn_problem& p) { return p.S == 0 ? 0 : p.ids ? p.W : p.S; }
 
-// Rows of a KV head that the streaming kernel takes in one pass over the keys.
-constexpr int64_t kStreamRows = 32;
+// Rows of a KV head up to which the prefix is streamed.
+constexpr int64_t kStreamRows = 16;
 
 // Whether the shared prefix goes to the tensor-core kernel.  TMA reads it
 // there, so its strides have to be ones that a tensor map can hold.
@@ -112,6 +112,15 @@ AttnArgs make_args(const attn_problem& p) {
 }  // namespace
 
 size_t attn_shared_ws(const attn_problem& p, bool mass) { return layout(make_args(p), mass).total; }
+
+bool attn_shared_fits(const attn_problem& p) {
+  // the lines of key units and tiles are counted in 32 bits
+  const int64_t unit = stream_unit(p.D), G = p.Hq / p.n_kv;
+  const int64_t seqs = (int64_t)p.B * (p.ids ? p.T : 1);
+  const int64_t line = ceil_div(p.P, unit) + seqs * std::max<int64_t>(1, ceil_div(private_keys(p), unit));
+  const int64_t tiles = ceil_div((int64_t)p.B * p.T * G, 256) * p.n_kv * ceil_div(p.P, 128);
+  return line < ((int64_t)1 << 31) && tiles < ((int64_t)1 << 31);
+}
 
 cudaError_t launch_attn_shared(const attn_problem& p, void* out, float* lse, float* mass, int mass_heads, void* ws,
                                cudaStream_t st) {

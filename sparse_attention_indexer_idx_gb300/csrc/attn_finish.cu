@@ -249,9 +249,11 @@ __device__ __forceinline__ void mass_dense(const AttnArgs& a, int64_t block, int
 // Mass of listed slots.  One list holds a slot at most once, so its threads add
 // to different slots; lists that can share a slot (another token's, or another
 // KV head's when all heads share the mass) follow one another in one block.
-__device__ void mass_listed(const AttnArgs& a, int64_t block, int64_t per) {
+// A thread takes E entries and 32 / E rows at a time.
+template <int E>
+__device__ __forceinline__ void mass_listed(const AttnArgs& a, int64_t block, int64_t per) {
   __shared__ MassRows s;
-  constexpr int E = 4;  // entries of a thread
+  constexpr int kBatch = 32 / E;
   const attn_problem& p = a.p;
   const int lists_h = p.ids_per_head && a.mass_heads == 1 ? p.n_kv : 1;
   const int lists = p.T * lists_h;
@@ -315,8 +317,10 @@ __global__ void __launch_bounds__(kThreads, LISTED ? 2 : 4)
   grid_wait();
   if (blockIdx.x < join_blocks)
     join_rows<D, BF16>(a);
+  else if (LISTED && row_groups == 1)
+    mass_listed<4>(a, blockIdx.x - join_blocks, per);
   else if (LISTED)
-    mass_listed(a, blockIdx.x - join_blocks, per);
+    mass_listed<1>(a, blockIdx.x - join_blocks, per);
   else
     mass_dense(a, blockIdx.x - join_blocks, (int)per, row_groups);
 }
@@ -327,15 +331,19 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
   const int64_t rows = (int64_t)p.B * p.T * p.Hq;
   const int64_t join = (rows + kWarps - 1) / kWarps;
   // a slot's rows are spread over up to four threads where there are many
-  const int mass_rows = p.Hq / a.mass_heads * p.T, groups = mass_rows >= 32 ? 4 : mass_rows >= 16 ? 2 : 1;
+  const int mass_rows = p.Hq / a.mass_heads * p.T;
+  int groups = mass_rows >= 32 ? 4 : mass_rows >= 16 ? 2 : 1;
   int64_t per = 0;  // mass blocks of one (b, mass head)
   if (a.mass && a.parts_private) {
     const int64_t bms = (int64_t)p.B * a.mass_heads;
     per = std::min((p.S + kThreads / groups * kSlots - 1) / (kThreads / groups * kSlots),
                    std::max<int64_t>(1, (4 * sm_count() + bms - 1) / bms));  // four blocks fit an SM
     if (p.ids) {
+      // lists that share slots follow one another in a block, four entries of
+      // up to eight rows at a time; other lists are spread over blocks by entry
       const bool one = p.T == 1 && !(p.ids_per_head && a.mass_heads == 1 && p.n_kv > 1);
-      per = one ? std::min<int64_t>((p.W + kThreads - 1) / kThreads, 2 * sm_count() / ((int64_t)p.B * a.mass_heads) + 1) : 1;
+      per = one ? (p.W + kThreads - 1) / kThreads : 1;
+      groups = one && p.Hq / a.mass_heads > 8 ? 4 : 1;
     }
   }
   const int64_t blocks = join + (int64_t)p.B * a.mass_heads * per;

@@ -111,7 +111,7 @@ __device__ __forceinline__ void stream_item(const AttnArgs& a, int h, int tile, 
   char* sring = smem;
   int* sslot = reinterpret_cast<int*>(smem + C::RING);
   char* sq = smem + C::RING + C::SLOTS;
-  __shared__ int64_t s_rowid[R];  // (b*T + t)*Hq + hq, or -1
+  __shared__ int s_rowid[R];      // (b*T + t)*Hq + hq (below 2^30), or -1
   __shared__ int s_lim[R];        // keys below this index are visible to the row
   __shared__ float2 s_ml[kWarps][R];
   __shared__ float2 s_tot[R];
@@ -137,14 +137,13 @@ __device__ __forceinline__ void stream_item(const AttnArgs& a, int h, int tile, 
   const int64_t priv = PREFIX ? 0 : attn_len(p, b, h);
   if (threadIdx.x < R) {
     const int i = threadIdx.x;
-    int64_t id = -1;
-    int lim = 0;
+    int id = -1, lim = 0;
     if (i < nrow) {
       const int r = it.row0 + i;
       const int g = r % a.G, bt = r / a.G;
       const int rb = PREFIX ? bt / p.T : b, rt = PREFIX ? bt % p.T : GATHER ? t : bt;
       lim = PREFIX ? (int)attn_prefix_len(p, rb) : max(0, (int)priv - p.T + rt + 1);
-      id = ((int64_t)rb * p.T + rt) * p.Hq + (int64_t)h * a.G + g;
+      id = (rb * p.T + rt) * p.Hq + h * a.G + g;
     }
     s_rowid[i] = id;
     s_lim[i] = lim;
@@ -163,10 +162,10 @@ __device__ __forceinline__ void stream_item(const AttnArgs& a, int h, int tile, 
   // the block with a sequence's last unit marks the partial results that the
   // sequence does not have
   if (u1 == units && threadIdx.x < nrow)
-    for (int i = part + 1; i < parts; i++) a.pml[s_rowid[threadIdx.x] * parts_all + at + i] = make_float2(-INFINITY, 0.f);
+    for (int i = part + 1; i < parts; i++) a.pml[(int64_t)s_rowid[threadIdx.x] * parts_all + at + i] = make_float2(-INFINITY, 0.f);
   part += at;
   if (it.k0 >= it.k1) {
-    if (threadIdx.x < nrow) a.pml[s_rowid[threadIdx.x] * parts_all + part] = make_float2(-INFINITY, 0.f);
+    if (threadIdx.x < nrow) a.pml[(int64_t)s_rowid[threadIdx.x] * parts_all + part] = make_float2(-INFINITY, 0.f);
     __syncthreads();
     return;
   }
@@ -222,12 +221,11 @@ __device__ __forceinline__ void stream_item(const AttnArgs& a, int h, int tile, 
   // ---- queries: rows into shared memory, then operand fragments
   for (int i = threadIdx.x; i < R * CH; i += blockDim.x) {
     const int r = i / CH, c = i % CH;
-    const int64_t id = s_rowid[r];
+    const int id = s_rowid[r];
     uint4 x = make_uint4(0, 0, 0, 0);
     if (id >= 0) {
-      const int64_t bt = id / p.Hq;
-      const int hq = (int)(id % p.Hq);
-      const int64_t e = (bt / p.T) * p.q_stride_b + (bt % p.T) * p.q_stride_t + hq * p.q_stride_h;
+      const int bt = id / p.Hq, hq = id - bt * p.Hq, rb = bt / p.T;
+      const int64_t e = rb * p.q_stride_b + (bt - rb * p.T) * p.q_stride_t + hq * p.q_stride_h;
       x = __ldg(reinterpret_cast<const uint4*>((const char*)p.q + 2 * e) + c);
     }
     *reinterpret_cast<uint4*>(sq + swz<D>(r, c)) = x;
@@ -243,7 +241,7 @@ __device__ __forceinline__ void stream_item(const AttnArgs& a, int h, int tile, 
   float o[MT][D / 8][4];
   float mx[MT][2], sum[MT][2];
   int lim[MT][2];
-  int64_t rid[MT][2];
+  int rid[MT][2];
 #pragma unroll
   for (int m = 0; m < MT; m++) {
 #pragma unroll
@@ -306,7 +304,7 @@ __device__ __forceinline__ void stream_item(const AttnArgs& a, int h, int tile, 
 #pragma unroll
           for (int e = 0; e < 2; e++)
             if (rid[m][e] >= 0 && at < it.k1)  // the pair's second half lies inside the padded row
-              *reinterpret_cast<float2*>(a.sc + rid[m][e] * a.sc_ld + at) =
+              *reinterpret_cast<float2*>(a.sc + (int64_t)rid[m][e] * a.sc_ld + at) =
                   make_float2(s[m][i][2 * e], s[m][i][2 * e + 1]);
         }
       }
@@ -396,7 +394,7 @@ __device__ __forceinline__ void stream_item(const AttnArgs& a, int h, int tile, 
     for (int w = 0; w < kWarps; w++)
       if (top != -INFINITY) l += s_ml[w][threadIdx.x].y * attn_ex2(s_ml[w][threadIdx.x].x - top);
     s_tot[threadIdx.x] = make_float2(top, l);
-    a.pml[s_rowid[threadIdx.x] * parts_all + part] = make_float2(top, l);
+    a.pml[(int64_t)s_rowid[threadIdx.x] * parts_all + part] = make_float2(top, l);
   }
   __syncthreads();
   for (int i = threadIdx.x; i < nrow * (D / 4); i += blockDim.x) {
@@ -411,7 +409,7 @@ __device__ __forceinline__ void stream_item(const AttnArgs& a, int h, int tile, 
       x.z += y.z;
       x.w += y.w;
     }
-    *reinterpret_cast<float4*>(a.po + (s_rowid[r] * parts_all + part) * D + d) = x;
+    *reinterpret_cast<float4*>(a.po + ((int64_t)s_rowid[r] * parts_all + part) * D + d) = x;
   }
   __syncthreads();  // the next item takes this memory
 }
@@ -433,63 +431,67 @@ __global__ void __launch_bounds__(32 * kWarps, MT == 1 ? 3 : 2)
     attn_stream_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ StreamLine line) {
   using C = StreamCfg<D, MT>;
   constexpr int NT = 32 * kWarps;
-  __shared__ int64_t s_sum[kWarps];
-  __shared__ int64_t s_start;
-  __shared__ int s_seq;
+  __shared__ int s_sum[kWarps];
+  __shared__ int s_start, s_seq;
   grid_let_next_start();
   const attn_problem& p = a.p;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int member = blockIdx.x % line.members, group = blockIdx.x / line.members;
-  const int h = member % p.n_kv, tile = member / p.n_kv;
-  const int seqs = line.seqs;                              // private sequences
+  const int group = blockIdx.x / line.members, member = blockIdx.x - group * line.members;
+  const int tile = member / p.n_kv, h = member - tile * p.n_kv;
+  const int seqs = line.seqs;                                   // private sequences
   const int list_units = (int)((p.W + C::UNIT - 1) / C::UNIT);  // of a gathered list
 
-  // the line's length, and each thread's share of the requests on it
-  int64_t mine = 0, total;
+  // the line's length (below 2^31, the plan checks), and where on it each
+  // thread's share of the requests begins
+  int mine = 0, total = line.prefix_units;
   const int per = (seqs + NT - 1) / NT;
   const int b0 = min(seqs, tid * per), b1 = min(seqs, b0 + per);
   if (GATHER) {
-    total = line.prefix_units + (int64_t)seqs * list_units;
+    total += seqs * list_units;
   } else {
     for (int b = b0; b < b1; b++) mine += cache_units<C::UNIT>(p, b);
-    int64_t incl = mine;
+    int incl = mine;
 #pragma unroll
     for (int s = 1; s < 32; s <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, incl, s);
+      const int y = __shfl_up_sync(0xffffffffu, incl, s);
       if (lane >= s) incl += y;
     }
     if (lane == 31) s_sum[warp] = incl;
     __syncthreads();
-    total = line.prefix_units;
-    int64_t before = line.prefix_units;
+    int before = line.prefix_units;
     for (int w = 0; w < kWarps; w++) {
       total += s_sum[w];
       if (w < warp) before += s_sum[w];
     }
-    mine = before + incl - mine;  // where this thread's requests begin
+    mine = before + incl - mine;
   }
-  const int64_t share = max((total + line.groups - 1) / line.groups, (int64_t)line.least);
-  int64_t lo = share * group;
-  const int64_t hi = min(total, lo + share);
+  // the cut: `groups` shares of `each` units, the first `extra` of them one longer
+  const int groups = min(line.groups, max(1, total / line.least));
+  const int each = total / groups, extra = total - each * groups;
+  auto group_of = [&](int u) {
+    const int head = extra * (each + 1);
+    return u < head ? u / (each + 1) : extra + (u - head) / each;
+  };
+  int lo = group * each + min(group, extra);
+  const int hi = group < groups ? lo + each + (group < extra ? 1 : 0) : lo;
   if (lo >= hi) {
     grid_wait();
     return;
   }
   if (lo < line.prefix_units) {
-    const int u1 = (int)min(hi, (int64_t)line.prefix_units);
-    stream_item<D, MT, BF16, false, true>(a, h, tile, 0, 0, (int)lo, u1, line.prefix_units, group);
+    const int u1 = min(hi, line.prefix_units);
+    stream_item<D, MT, BF16, false, true>(a, h, tile, 0, 0, lo, u1, line.prefix_units, group);
     lo = u1;
   }
   if (lo < hi) {
-    int seq, units;
-    int64_t start;  // of the sequence that holds lo
+    int seq, units, start;  // the sequence that holds lo
     if (GATHER) {
-      seq = (int)((lo - line.prefix_units) / list_units);
-      start = line.prefix_units + (int64_t)seq * list_units;
+      seq = (lo - line.prefix_units) / list_units;
+      start = line.prefix_units + seq * list_units;
       units = list_units;
     } else {
       __syncthreads();
-      int64_t at = mine;
+      int at = mine;
       for (int b = b0; b < b1; b++) {
         const int u = cache_units<C::UNIT>(p, b);
         if (at <= lo && lo < at + u) {
@@ -504,9 +506,9 @@ __global__ void __launch_bounds__(32 * kWarps, MT == 1 ? 3 : 2)
       units = cache_units<C::UNIT>(p, seq);
     }
     while (true) {
-      const int u0 = (int)(lo - start), u1 = (int)min((int64_t)units, hi - start);
-      stream_item<D, MT, BF16, GATHER, false>(a, h, tile, GATHER ? seq / p.T : seq, GATHER ? seq % p.T : 0, u0, u1, units,
-                                              group - (int)(start / share));
+      const int b = GATHER ? seq / p.T : seq;
+      stream_item<D, MT, BF16, GATHER, false>(a, h, tile, b, GATHER ? seq - b * p.T : 0, lo - start, min(units, hi - start),
+                                              units, group - group_of(start));
       start += units;
       lo = start;
       if (lo >= hi) break;

@@ -118,8 +118,8 @@ struct Run {
 // The line of units and this block's share of it.
 struct Line {
   int tiles, cells_k, rts, heads;  // key tiles, pieces of the keys, row tile pairs, KV heads
-  int64_t u, u1, total;
-  int n, c;
+  int u, u0, u1;                   // the share, and how far this role has come
+  int c;
   bool whole;
   __device__ __forceinline__ int cell_start(int kc) const { return (int)((int64_t)tiles * kc / cells_k); }
   __device__ __forceinline__ void init(int tiles_, const AttnTcArgs& a) {
@@ -127,48 +127,49 @@ struct Line {
     cells_k = min(a.cells_k, tiles);
     rts = a.row_tiles;
     heads = a.a.p.n_kv;
-    n = (int)gridDim.x;
     c = (int)blockIdx.x;
     whole = a.whole_cells;
-    total = (int64_t)heads * rts * tiles;
+    const int total = heads * rts * tiles, n = (int)gridDim.x;  // below 2^31, the plan checks
     if (tiles == 0) {
-      u = u1 = 0;
+      u0 = u1 = 0;
     } else if (whole) {
-      u = c;  // one cell: block index (h, kc, rt)
+      u0 = c;  // one cell: block index (h, kc, rt)
       u1 = c < heads * cells_k * rts ? c + 1 : c;
     } else {
-      u = total * c / n;
-      u1 = total * (c + 1) / n;
+      const int each = total / n, extra = total - each * n;
+      u0 = c * each + min(c, extra);
+      u1 = u0 + each + (c < extra ? 1 : 0);
     }
+    u = u0;
   }
   // The next run of this block; false at its end.
   __device__ __forceinline__ bool next(Run* r) {
     if (u >= u1) return false;
     if (whole) {
-      r->rt = (int)(u % rts);
-      const int kc = (int)(u / rts % cells_k);
-      r->h = (int)(u / rts / cells_k);
-      r->j0 = cell_start(kc);
-      r->j1 = cell_start(kc + 1);
-      r->part = kc;
+      const int q = u / rts;
+      r->rt = u - q * rts;
+      r->h = q / cells_k;
+      r->part = q - r->h * cells_k;
+      r->j0 = cell_start(r->part);
+      r->j1 = cell_start(r->part + 1);
       u++;
       return true;
     }
     // unit u lies in head h; in it, cells of (piece, row tile pair)
-    const int64_t per = (int64_t)rts * tiles;
-    r->h = (int)(u / per);
-    const int64_t in = u % per;
-    int kc = (int)(in / rts * cells_k / tiles);
-    while (kc > 0 && (int64_t)cell_start(kc) * rts > in) kc--;
-    while ((int64_t)cell_start(kc + 1) * rts <= in) kc++;
+    const int per = rts * tiles;
+    r->h = u / per;
+    const int in = u - r->h * per;
+    int kc = (int)((int64_t)(in / rts) * cells_k / tiles);
+    while (kc > 0 && cell_start(kc) * rts > in) kc--;
+    while (cell_start(kc + 1) * rts <= in) kc++;
     const int s = cell_start(kc), len = cell_start(kc + 1) - s;
-    const int64_t off = in - (int64_t)s * rts;
-    r->rt = (int)(off / len);
-    r->j0 = s + (int)(off % len);
-    r->j1 = (int)min((int64_t)(s + len), r->j0 + (u1 - u));
-    // the cell's first unit lies in the same block's share, or in the one before
-    const int64_t first = (int64_t)r->h * per + (int64_t)s * rts + (int64_t)r->rt * len;
-    r->part = 2 * kc + (first < total * c / n ? 1 : 0);
+    const int off = in - s * rts;
+    r->rt = off / len;
+    const int at = off - r->rt * len;
+    r->j0 = s + at;
+    r->j1 = min(s + len, r->j0 + (u1 - u));
+    // the cell's first unit lies in this block's share, or in the one before
+    r->part = 2 * kc + (u - at < u0 ? 1 : 0);
     u += r->j1 - r->j0;
     return true;
   }

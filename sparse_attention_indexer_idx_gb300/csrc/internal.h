@@ -111,6 +111,7 @@ cudaError_t launch_dosa(const idx_problem& p, int K, const dosa_params& dp, cons
                         int32_t* out_ids, float* out_scores, int32_t* row_status, dosa_stats* stats, void* ws,
                         size_t ws_bytes, cudaStream_t st);
 
+bool attn_shared_fits(const attn_problem& p);  // its work is countable in 32 bits
 size_t attn_shared_ws(const attn_problem& p, bool mass);
 cudaError_t launch_attn_shared(const attn_problem& p, void* out, float* lse, float* mass, int mass_heads, void* ws,
                                cudaStream_t st);
