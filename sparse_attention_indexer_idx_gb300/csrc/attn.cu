@@ -26,7 +26,10 @@ bool prefix_on_tc(const attn_problem& p) {
 
 // The tensor-core kernel's grid.  A whole number of pieces per (KV head, row
 // tile pair) is taken if it leaves at most a tenth of the SMs idle; otherwise
-// the key tiles are cut evenly, and a piece can end up on two blocks.
+// the key tiles are cut evenly, and a piece can end up on two blocks.  (Leaving
+// a part of the SMs to the streaming kernel, in proportion to the work, was
+// slower than one after the other: 378 against 354 us on a shared document of
+// 65536 tokens under 128 requests.)
 AttnTcArgs plan_tc(const AttnArgs& a) {
   const attn_problem& p = a.p;
   AttnTcArgs t{};
@@ -119,7 +122,12 @@ bool attn_shared_fits(const attn_problem& p) {
   const int64_t seqs = (int64_t)p.B * (p.ids ? p.T : 1);
   const int64_t line = ceil_div(p.P, unit) + seqs * std::max<int64_t>(1, ceil_div(private_keys(p), unit));
   const int64_t tiles = ceil_div((int64_t)p.B * p.T * G, 256) * p.n_kv * ceil_div(p.P, 128);
-  return line < ((int64_t)1 << 31) && tiles < ((int64_t)1 << 31);
+  if (line >= ((int64_t)1 << 31) || tiles >= ((int64_t)1 << 31)) return false;
+  // and so are the partial results, and the rows of q (in 16 bytes)
+  const AttnArgs a = make_args(p);
+  auto span = [](int64_t n, int64_t stride) { return (n - 1) * (stride < 0 ? -stride : stride); };
+  const int64_t q = span(p.B, p.q_stride_b) + span(p.T, p.q_stride_t) + span(p.Hq, p.q_stride_h);
+  return (int64_t)p.B * p.T * p.Hq * (a.parts_prefix + a.parts_private) < ((int64_t)1 << 31) && q / 8 < ((int64_t)1 << 31);
 }
 
 cudaError_t launch_attn_shared(const attn_problem& p, void* out, float* lse, float* mass, int mass_heads, void* ws,

@@ -31,6 +31,9 @@ struct AttnArgs {
   int mass_heads;
 };
 
+// Keys of a unit of the streaming kernel's work.
+__host__ __device__ constexpr int stream_unit(int D) { return D == 128 ? 64 : 128; }
+
 // Private slots that token t of request b sees under KV head h.
 __device__ __forceinline__ int attn_len(const attn_problem& p, int b, int h) {
   if (!p.len) return 0;
@@ -51,6 +54,18 @@ __device__ __forceinline__ int64_t attn_prefix_len(const attn_problem& p, int b)
   return n;
 }
 
+// Units of request b's cache on the streaming kernel's line: by its longest
+// head, at least one, so that every sequence has a place.
+template <int UNIT>
+__device__ __forceinline__ int cache_units(const attn_problem& p, int b) {
+  int n = 0;
+  for (int h = 0; h < (p.len_per_head ? p.n_kv : 1); h++) {
+    const int x = p.len[p.len_per_head ? (int64_t)b * p.n_kv + h : b];
+    if (x <= p.S) n = max(n, x);
+  }
+  return max(1, (n + UNIT - 1) / UNIT);
+}
+
 __device__ __forceinline__ float attn_ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -58,7 +73,6 @@ __device__ __forceinline__ float attn_ex2(float x) {
 }
 
 // The streaming kernel's line of key units and its cut (see attn_stream.cu).
-constexpr int stream_unit(int D) { return D == 128 ? 64 : 128; }  // keys
 struct StreamLine {
   int row_tile;      // 16 or 32 rows of a block
   int members;       // blocks of a group: KV heads times row tiles

@@ -414,18 +414,6 @@ __device__ __forceinline__ void stream_item(const AttnArgs& a, int h, int tile, 
   __syncthreads();  // the next item takes this memory
 }
 
-// Units of request b's cache: by its longest head, at least one, so that every
-// sequence has a place on the line.
-template <int UNIT>
-__device__ __forceinline__ int cache_units(const attn_problem& p, int b) {
-  int n = 0;
-  for (int h = 0; h < (p.len_per_head ? p.n_kv : 1); h++) {
-    const int x = p.len[p.len_per_head ? (int64_t)b * p.n_kv + h : b];
-    if (x <= p.S) n = max(n, x);
-  }
-  return max(1, (n + UNIT - 1) / UNIT);
-}
-
 template <int D, int MT, bool BF16, bool GATHER>
 __global__ void __launch_bounds__(32 * kWarps, MT == 1 ? 3 : 2)
     attn_stream_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ StreamLine line) {
@@ -474,8 +462,12 @@ __global__ void __launch_bounds__(32 * kWarps, MT == 1 ? 3 : 2)
   };
   int lo = group * each + min(group, extra);
   const int hi = group < groups ? lo + each + (group < extra ? 1 : 0) : lo;
+  // The finish kernel waits for this grid alone, so it has to end behind the
+  // one before it: one block waits for that (a wait of every block would keep
+  // the next ones from their places).
+  const bool waits = blockIdx.x == gridDim.x - 1;
   if (lo >= hi) {
-    grid_wait();
+    if (waits) grid_wait();
     return;
   }
   if (lo < line.prefix_units) {
@@ -516,8 +508,7 @@ __global__ void __launch_bounds__(32 * kWarps, MT == 1 ? 3 : 2)
       if (!GATHER) units = cache_units<C::UNIT>(p, seq);
     }
   }
-  // the finish kernel waits for this grid alone: it ends behind the one before it
-  grid_wait();
+  if (waits) grid_wait();
 }
 
 template <int D, int MT, bool BF16, bool GATHER>

@@ -95,6 +95,8 @@ __device__ __forceinline__ uint64_t desc_values(uint32_t addr) {
   d |= (uint64_t)2 << 61;
   return d;
 }
+// Barrier of the four warps of a row tile.
+__device__ __forceinline__ void row_tile_sync(int i) { asm volatile("bar.sync %0, 128;" ::"r"(i + 1) : "memory"); }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -119,17 +121,19 @@ struct Run {
 struct Line {
   int tiles, cells_k, rts, heads;  // key tiles, pieces of the keys, row tile pairs, KV heads
   int u, u0, u1;                   // the share, and how far this role has come
-  int c;
+  int cell, longer;                // key tiles of a piece; the first `longer` pieces have one more
   bool whole;
-  __device__ __forceinline__ int cell_start(int kc) const { return (int)((int64_t)tiles * kc / cells_k); }
+  __device__ __forceinline__ int cell_start(int kc) const { return kc * cell + min(kc, longer); }
   __device__ __forceinline__ void init(int tiles_, const AttnTcArgs& a) {
     tiles = tiles_;
     cells_k = min(a.cells_k, tiles);
     rts = a.row_tiles;
     heads = a.a.p.n_kv;
-    c = (int)blockIdx.x;
+    const int c = (int)blockIdx.x;
     whole = a.whole_cells;
-    const int total = heads * rts * tiles, n = (int)gridDim.x;  // below 2^31, the plan checks
+    cell = cells_k ? tiles / cells_k : 0;
+    longer = tiles - cell * cells_k;
+    const int total = heads * rts * tiles, n = (int)gridDim.x;  // total is below 2^31, the plan checks
     if (tiles == 0) {
       u0 = u1 = 0;
     } else if (whole) {
@@ -159,10 +163,9 @@ struct Line {
     const int per = rts * tiles;
     r->h = u / per;
     const int in = u - r->h * per;
-    int kc = (int)((int64_t)(in / rts) * cells_k / tiles);
-    while (kc > 0 && cell_start(kc) * rts > in) kc--;
-    while (cell_start(kc + 1) * rts <= in) kc++;
-    const int s = cell_start(kc), len = cell_start(kc + 1) - s;
+    const int x = in / rts, head = longer * (cell + 1);
+    const int kc = x < head ? x / (cell + 1) : longer + (x - head) / cell;
+    const int s = cell_start(kc), len = cell + (kc < longer ? 1 : 0);
     const int off = in - s * rts;
     r->rt = off / len;
     const int at = off - r->rt * len;
@@ -180,12 +183,15 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                    const __grid_constant__ AttnTcArgs args) {
   using C = TcCfg<D>;
+  constexpr int CH = D / 8;  // 16-byte pieces of a row of queries
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t* sq = smem;
   uint8_t* skv = smem + 2 * C::TILE;
   __shared__ uint64_t kv_full[C::NS], kv_empty[C::NS], q_full[2], s_full[2], p_ready[2], o_full[2], drain;
   __shared__ uint32_t s_tmem;
+  // where a row's queries begin, in 16 bytes; then the number of its partial result
+  __shared__ int s_row[2][128];
   __shared__ int s_abort, s_vis;
 
   const AttnArgs& a = args.a;
@@ -215,11 +221,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     fence_mbar_init();
   }
   if (warp == 2) tmem_alloc(&s_tmem, 512);
-  __syncthreads();
   if (p.prefix_len) {
     int v = 0;
     for (int b = threadIdx.x; b < p.B; b += kThreadsTc) v = max(v, (int)attn_prefix_len(p, b));
     v = __reduce_max_sync(0xffffffffu, v);
+    __syncthreads();
     if (lane == 0 && v) atomicMax(&s_vis, v);
   }
   tc_fence_before();
@@ -278,9 +284,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         phase ^= 1;
       }
     };
-    // S_i = Q_i K^T, then the barrier of its readers
-    auto scores = [&](int i, uint32_t k) {
-      const uint64_t q0 = dq + i * (C::TILE / 16), k0 = dk + k * (C::TILE / 16);
+    // S_i = Q_t K^T, then the barrier of its readers
+    auto scores = [&](int i, int t, uint32_t k) {
+      const uint64_t q0 = dq + t * (C::TILE / 16), k0 = dk + k * (C::TILE / 16);
 #pragma unroll
       for (int s = 0; s < D / 16; s++) {
         const uint32_t off = ((s / 4) * 16384 + (s % 4) * 32) / 16;
@@ -288,16 +294,12 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       }
       tc_commit(&s_full[i]);
     };
-    // O_i += P_i V, then the next S_i, or the barrier of O's reader
-    auto values = [&](int i, uint32_t v, uint32_t k, bool add, bool more) {
+    // O_t += P_i V
+    auto values = [&](int i, int t, uint32_t v, bool add) {
       const uint64_t v0 = dv + v * (C::TILE / 16);
 #pragma unroll
       for (int s = 0; s < 8; s++)
-        tc_mma_f16_ts(tmem + 256 + 128 * i, tmem + 128 * i + 8 * s, v0 + s * (2048 / 16), id_o, add || s > 0);
-      if (more)
-        scores(i, k);
-      else
-        tc_commit(&o_full[i]);
+        tc_mma_f16_ts(tmem + 256 + 128 * t, tmem + 128 * i + 8 * s, v0 + s * (2048 / 16), id_o, add || s > 0);
     };
     Run r;
     while (ok && line.next(&r)) {
@@ -309,8 +311,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       if (!ok) break;
       tc_fence_after();
       if (elect_one()) {
-        scores(0, slot);
-        if (two) scores(1, slot);
+        scores(0, 0, slot);
+        if (two) scores(1, 1, slot);
         tc_commit(&kv_empty[slot]);
       }
       __syncwarp();
@@ -325,23 +327,47 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
           ok = ok && wait(&kv_full[slot], phase);
           advance();
         }
-        ok = ok && wait(&p_ready[0], np++ & 1);
+        if (!ok) break;
+        if (!two) {
+          // One row tile: its scores alternate between the two places, so that
+          // the next key tile's are formed while this one's weights are.
+          tc_fence_after();
+          if (more && elect_one()) {
+            scores((j + 1) & 1, 0, k);
+            tc_commit(&kv_empty[k]);
+          }
+          __syncwarp();
+          ok = wait(&p_ready[0], np++ & 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            values(j & 1, 0, v, j > 0);
+            tc_commit(more ? &kv_empty[v] : &o_full[0]);
+            if (!more) tc_commit(&kv_empty[v]);
+          }
+          __syncwarp();
+          continue;
+        }
+        ok = wait(&p_ready[0], np++ & 1);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          values(0, v, k, j > 0, more);
-          if (!two) {
-            tc_commit(&kv_empty[v]);
-            if (more) tc_commit(&kv_empty[k]);
-          }
+          values(0, 0, v, j > 0);
+          if (more)
+            scores(0, 0, k);
+          else
+            tc_commit(&o_full[0]);
         }
         __syncwarp();
-        if (!two) continue;
         ok = wait(&p_ready[1], np1++ & 1);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          values(1, v, k, j > 0, more);
+          values(1, 1, v, j > 0);
+          if (more)
+            scores(1, 1, k);
+          else
+            tc_commit(&o_full[1]);
           tc_commit(&kv_empty[v]);
           if (more) tc_commit(&kv_empty[k]);
         }
@@ -357,44 +383,55 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     const int i = (warp - 4) >> 2;              // row tile
     const int row = threadIdx.x - 128 - 128 * i;  // its row, = TMEM lane
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lane_off + 128 * i, to = tmem + lane_off + 256 + 128 * i;
+    const uint32_t to = tmem + lane_off + 256 + 128 * i;
     // 2^(c s - m): a negative scale goes into the queries' sign, and a scale of
     // zero becomes one that takes every score to zero but leaves -inf alone
     const float c = fmaxf(fabsf(a.scale_log2), 1e-37f);
     const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
-    uint32_t ns = 0, no = 0, cnt = 0;
+    uint32_t ns0 = 0, ns1 = 0, no = 0, cnt = 0;  // ns: uses of the scores' two places
     bool ok = true;
     Run r;
     while (ok && line.next(&r)) {
       const int n = r.j1 - r.j0;
       const int rr = r.rt * 256 + i * 128 + row;
-      if (r.rt * 256 + i * 128 >= rows) {  // an empty row tile
+      const bool two = rows - r.rt * 256 > 128;
+      if (i == 1 && !two) {  // an empty row tile; the other one uses both places
         cnt += 2 * n;
+        ns1 += n / 2;
         continue;
       }
+      if (i == 0 && two) ns1 += n;  // the other tile's
       const bool live = rr < rows;
-      int64_t rid = -1;
-      int lim = 0;
-      const uint4* src = nullptr;
+      int rid = -1, lim = 0;
       if (live) {
-        const int bt = rr / a.G, g = rr % a.G;
-        const int b = bt / p.T, t = bt % p.T;
+        const int bt = rr / a.G, g = rr - bt * a.G;
+        const int b = bt / p.T, t = bt - b * p.T;
         const int hq = r.h * a.G + g;
-        rid = (int64_t)bt * p.Hq + hq;
+        rid = bt * p.Hq + hq;
         lim = (int)attn_prefix_len(p, b);
-        src = reinterpret_cast<const uint4*>((const char*)p.q +
-                                             2 * (b * p.q_stride_b + t * p.q_stride_t + hq * p.q_stride_h));
+        s_row[i][row] = (int)((b * p.q_stride_b + t * p.q_stride_t + hq * p.q_stride_h) / 8);
       }
-      // this row of the queries, in the swizzled layout of the keys
+      row_tile_sync(i);
+      // the queries, in the swizzled layout of the keys: CH lanes to a row, so
+      // that a row is read whole
+      {
+        uint4 v[CH];
 #pragma unroll
-      for (int x = 0; x < D / 8; x++) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (live) v = __ldg(src + x);
-        v.x ^= flip;
-        v.y ^= flip;
-        v.z ^= flip;
-        v.w ^= flip;
-        *reinterpret_cast<uint4*>(sq + i * C::TILE + (x / 8) * 16384 + row * 128 + (((x & 7) ^ (row & 7)) << 4)) = v;
+        for (int x = 0; x < CH; x++) {
+          const int qr = x * (128 / CH) + row / CH;
+          v[x] = make_uint4(0, 0, 0, 0);
+          if (r.rt * 256 + i * 128 + qr < rows)
+            v[x] = __ldg(reinterpret_cast<const uint4*>(p.q) + (int64_t)s_row[i][qr] + row % CH);
+        }
+#pragma unroll
+        for (int x = 0; x < CH; x++) {
+          const int qr = x * (128 / CH) + row / CH, ch = row % CH;
+          v[x].x ^= flip;
+          v[x].y ^= flip;
+          v[x].z ^= flip;
+          v[x].w ^= flip;
+          *reinterpret_cast<uint4*>(sq + i * C::TILE + (ch / 8) * 16384 + qr * 128 + (((ch & 7) ^ (qr & 7)) << 4)) = v[x];
+        }
       }
       fence_proxy_async_smem();
       mbar_arrive(&q_full[i]);
@@ -404,7 +441,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
 #pragma unroll
       for (int q = 0; q < 4; q++) l2[q] = f2_pack(0.f, 0.f);
       for (int j = r.j0; j < r.j1; j++) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[i], ns++ & 1, abort_flag));
+        const int place = two ? i : (j - r.j0) & 1;
+        const uint32_t ts = tmem + lane_off + 128 * place;
+        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[place], (place ? ns1++ : ns0++) & 1, abort_flag));
         if (!ok) break;
         tc_fence_after();
         // the row's scores, the second half on its way while the first is used;
@@ -514,21 +553,40 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         f2_unpack(l2[q], &l0, &l1);
         l += l0 + l1;
       }
-      if (live) a.pml[rid * parts_all + r.part] = make_float2(l > 0.f ? m : -INFINITY, l);
-      // a cell that one block did alone has no second part
-      if (live && !line.whole && (r.part & 1) == 0 && r.j1 == line.cell_start(r.part / 2 + 1))
-        a.pml[rid * parts_all + r.part + 1] = make_float2(-INFINITY, 0.f);
-      float* po = a.po + (rid * parts_all + r.part) * D;
+      const int64_t at = (int64_t)rid * parts_all + r.part;
+      if (live) {
+        a.pml[at] = make_float2(l > 0.f ? m : -INFINITY, l);
+        // a cell that one block did alone has no second part
+        if (!line.whole && (r.part & 1) == 0 && r.j1 == line.cell_start(r.part / 2 + 1))
+          a.pml[at + 1] = make_float2(-INFINITY, 0.f);
+      }
+      s_row[i][row] = live && l > 0.f ? (int)at : -1;
+      // the sums leave through the memory of the queries, half of a row at a
+      // time, so that CH lanes write one row's half next to one another
 #pragma unroll
-      for (int x = 0; x < D / 32; x++) {
-        uint32_t o[32];
-        tmem_ld_32x32b_x32(to + 32 * x, o);
-        tmem_ld_wait();
-        tie(o);
-        if (live && l > 0.f)
+      for (int half = 0; half < 2; half++) {
+        uint8_t* stage = sq + i * C::TILE;
 #pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<uint4*>(po + 32 * x + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        for (int x = 0; x < D / 64; x++) {
+          uint32_t o[32];
+          tmem_ld_32x32b_x32(to + half * (D / 2) + 32 * x, o);
+          tmem_ld_wait();
+          tie(o);
+#pragma unroll
+          for (int e = 0; e < 8; e++)
+            *reinterpret_cast<uint4*>(stage + row * (2 * D) + (((8 * x + e) ^ (row & 7)) << 4)) =
+                make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        }
+        row_tile_sync(i);
+#pragma unroll 4
+        for (int x = 0; x < CH; x++) {
+          const int qr = x * (128 / CH) + row / CH, ch = row % CH;
+          const int64_t to_row = s_row[i][qr];
+          if (to_row >= 0)
+            *reinterpret_cast<uint4*>(a.po + to_row * D + half * (D / 2) + 4 * ch) =
+                *reinterpret_cast<const uint4*>(stage + qr * (2 * D) + ((ch ^ (qr & 7)) << 4));
+        }
+        row_tile_sync(i);
       }
       tc_fence_before();
     }
