@@ -45,7 +45,8 @@ AttnTcArgs plan_tc(const AttnArgs& a) {
 }
 
 // The streaming kernel's groups and the parts of a sequence.  Every SM holds
-// three blocks of 16 rows or two of 32.  The share of a group depends on the
+// twelve warps of 16 rows or eight of 32 (three or two blocks), and every warp
+// gets one share of the line: cutting it finer cost 1 to 7 percent.  The share of a group depends on the
 // lengths, which only the device knows; the parts allow for lines down to a
 // quarter of the longest.
 StreamLine plan_stream(AttnArgs& a) {
@@ -62,12 +63,8 @@ StreamLine plan_stream(AttnArgs& a) {
   const int64_t longest = ceil_div(private_keys(p), unit);
   l.seqs = longest == 0 ? 0 : p.ids ? p.B * p.T : p.B;
   const int64_t total = l.prefix_units + l.seqs * longest;
-  // one group for each place: cutting the line finer cost 1 to 7 percent
-  const int64_t places = std::max<int64_t>(1, (l.row_tile == 16 ? 3 : 2) * (int64_t)sm_count() / l.members);
-  l.groups = (int)places;
-  // a unit more than a quarter of the even share, at least two: a block's start
-  // and the join of its warps cost about as much as two units do
-  l.least = (int)std::max<int64_t>(2, ceil_div(total, 4 * (int64_t)l.groups));
+  l.groups = (int)std::max<int64_t>(1, (l.row_tile == 16 ? 12 : 8) * (int64_t)sm_count() / l.members);
+  l.least = (int)std::max<int64_t>(1, ceil_div(total, 4 * (int64_t)l.groups));
   auto parts = [&](int64_t units) { return units == 0 ? 0 : (int)std::min(units, ceil_div(units - 1, l.least) + 1); };
   if (prefix) a.parts_prefix = parts(l.prefix_units);
   a.parts_private = l.seqs ? parts(longest) : 0;

@@ -74,8 +74,8 @@ __device__ __forceinline__ float attn_ex2(float x) {
 
 // The streaming kernel's line of key units and its cut (see attn_stream.cu).
 struct StreamLine {
-  int row_tile;      // 16 or 32 rows of a block
-  int members;       // blocks of a group: KV heads times row tiles
+  int row_tile;      // 16 or 32 rows of a warp
+  int members;       // warps of a group: KV heads times row tiles
   int groups;
   int prefix_units;  // 0: the prefix is not streamed
   int seqs;          // private sequences: requests, or (request, token) lists

@@ -2,19 +2,20 @@
 // the private caches of a decode step, and a shared prefix under a small batch.
 //
 // Mapping.  The key sequences (the prefix, then every request's cache or list)
-// form one line of key units; it is cut evenly over groups of blocks, with one
-// block of a group for each KV head (and tile of up to 32 rows).  The heads of a
+// form one line of key units; it is cut evenly over groups of warps, with one
+// warp of a group for each KV head (and tile of up to 32 rows).  The heads of a
 // group run side by side, so their rows of a cache, which lie next to one
 // another, are read together, and all groups end together however ragged the
 // lengths are.  A group that starts or ends inside a sequence leaves one of
 // several partial results of it.
 //
-// A block's four warps are independent streams: warp w takes every fourth tile
-// of KT keys, copies the keys and values with 16-byte cp.async into a ring of
-// its own (swizzled, so ldmatrix is free of bank conflicts) and keeps the
-// running maximum, sum and output of its keys in registers; nothing but the
-// warp itself waits for a copy.  The four results are joined through shared
-// memory at the end of a sequence or of the block's share.
+// Every warp is a stream of its own: it copies tiles of KT keys and values with
+// 16-byte cp.async into a ring (swizzled, so ldmatrix is free of bank
+// conflicts) and keeps the running maximum, sum and output in registers.
+// Nothing waits for another warp: the start and the end of one warp's sequence
+// pass while the others of the SM stream.  The keys' half of a ring slot is
+// refilled as soon as the scores are formed, the values' half after the second
+// product, so that between one and two tiles are on their way all the time.
 //
 // The products use mma.sync (16 x 8 x 16): a decode row group is 1 to 32 rows,
 // so the tensor work is a few percent of the time the bytes take, and the
@@ -70,17 +71,14 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 
 template <int D, int MT>
 struct StreamCfg {
-  // Ring slots of a warp.  With up to 16 rows two of them leave room for three
-  // blocks on an SM (registers allow no more), whose twelve tiles in flight
-  // cover the latency of HBM; with more rows two blocks fit, and a third slot.
-  static constexpr int kStages = MT == 1 ? 2 : 3;
-  static constexpr int KT = D == 128 ? 16 : 32;  // keys of a warp's tile: 4 KB of keys, 4 KB of values
-  static constexpr int ROWB = D * 2;
-  static constexpr int CH = ROWB / 16;            // 16-byte chunks of a row
-  static constexpr int STAGE = 2 * KT * ROWB;
-  static constexpr int UNIT = kWarps * KT;        // keys of the four warps' tiles
-  static constexpr int RING = kWarps * kStages * STAGE;
-  static constexpr int SLOTS = kWarps * kStages * KT * 4;  // slot numbers of gathered tiles
+  static constexpr int KT = D == 128 ? 16 : 32;  // keys of a tile: 4 KB of keys, 4 KB of values
+  static constexpr int UNIT = stream_unit(D);    // a warp's work is cut in units of four tiles
+  static constexpr int CH = D / 8;                // 16-byte chunks of a row
+  static constexpr int HALF = KT * D * 2;         // bytes of a tile's keys, and of its values
+  static constexpr int RING = 2 * 2 * HALF;       // two slots
+  static constexpr int SLOTS = 4 * KT;            // slot numbers of gathered tiles
+  static constexpr int WARP_BYTES = RING + SLOTS * 4;
+  static_assert(UNIT == 4 * KT, "four tiles");
 };
 
 // Chunk c of row r in a swizzled tile of rows of CH chunks.
@@ -89,159 +87,146 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
   return (uint32_t)(r * D * 2 + ((c ^ (r & 7)) << 4));
 }
 
-// What a block works on at a time: the units [u0, u1) of a key sequence (or of
-// an id list), and up to 16*MT rows that read it.
-struct StreamItem {
-  const char* k;
-  const char* v;
-  int64_t ks, vs;   // bytes between keys
-  int64_t k0, k1;
-  int rows, row0;   // rows row0 .. of `rows`
-};
-
-// b, t: request, and token of a gathered list; [u0, u1): this block's units of
-// the sequence's `units`; part: number of the partial result.
+// One warp's part of a key sequence (or of an id list) for up to 16*MT rows: its
+// units [u0, u1) of the sequence's `units`.  b, t: request, and token of a
+// gathered list; part: number of the partial result.
 template <int D, int MT, bool BF16, bool GATHER, bool PREFIX>
 __device__ __forceinline__ void stream_item(const AttnArgs& a, int h, int tile, int b, int t, int u0, int u1, int units,
                                             int part) {
   using C = StreamCfg<D, MT>;
-  constexpr int KT = C::KT, NT = KT / 8, KS = D / 16, CH = C::CH, kStages = C::kStages;
+  constexpr int KT = C::KT, NT = KT / 8, KS = D / 16, CH = C::CH;
   constexpr int R = 16 * MT;
   extern __shared__ __align__(1024) char smem[];
-  char* sring = smem;
-  int* sslot = reinterpret_cast<int*>(smem + C::RING);
-  char* sq = smem + C::RING + C::SLOTS;
-  __shared__ int s_rowid[R];      // (b*T + t)*Hq + hq (below 2^30), or -1
-  __shared__ int s_lim[R];        // keys below this index are visible to the row
-  __shared__ float2 s_ml[kWarps][R];
-  __shared__ float2 s_tot[R];
-
   const attn_problem& p = a.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  StreamItem it;
-  it.rows = PREFIX ? p.B * p.T * a.G : GATHER ? a.G : p.T * a.G;
-  it.row0 = tile * R;
-  const int nrow = min(R, it.rows - it.row0);
+  const uint32_t ring = smem_u32(smem) + warp * C::RING;
+  int* slots = reinterpret_cast<int*>(smem + kWarps * C::RING) + warp * C::SLOTS;
+  const int rows = PREFIX ? p.B * p.T * a.G : GATHER ? a.G : p.T * a.G;
+  const int row0 = tile * R;
+  const int nrow = min(R, rows - row0);
   if (nrow <= 0) return;  // a tile that only other sequences have
-  if (PREFIX) {
-    it.k = (const char*)p.pk + 2 * h * p.pk_stride_h;
-    it.v = (const char*)p.pv + 2 * h * p.pv_stride_h;
-    it.ks = 2 * p.pk_stride_s;
-    it.vs = 2 * p.pv_stride_s;
-  } else {
-    it.k = (const char*)p.k + 2 * ((int64_t)b * p.k_stride_b + h * p.k_stride_h);
-    it.v = (const char*)p.v + 2 * ((int64_t)b * p.v_stride_b + h * p.v_stride_h);
-    it.ks = 2 * p.k_stride_s;
-    it.vs = 2 * p.v_stride_s;
-  }
-  const int64_t priv = PREFIX ? 0 : attn_len(p, b, h);
-  if (threadIdx.x < R) {
-    const int i = threadIdx.x;
-    int id = -1, lim = 0;
-    if (i < nrow) {
-      const int r = it.row0 + i;
-      const int g = r % a.G, bt = r / a.G;
-      const int rb = PREFIX ? bt / p.T : b, rt = PREFIX ? bt % p.T : GATHER ? t : bt;
-      lim = PREFIX ? (int)attn_prefix_len(p, rb) : max(0, (int)priv - p.T + rt + 1);
-      id = (rb * p.T + rt) * p.Hq + h * a.G + g;
+
+  // lane r holds row r: its number, its queries, and how many keys it sees
+  int rid_l = -1, lim_l = 0;
+  int64_t q_l = 0;
+  if (lane < nrow) {
+    const int r = row0 + lane, bt = r / a.G, g = r - bt * a.G;
+    int rb = b, rt = GATHER ? t : bt;
+    if (PREFIX) {
+      rb = bt / p.T;
+      rt = bt - rb * p.T;
+      lim_l = (int)attn_prefix_len(p, rb);
+    } else {
+      lim_l = max(0, attn_len(p, b, h) - p.T + rt + 1);
     }
-    s_rowid[i] = id;
-    s_lim[i] = lim;
+    const int hq = h * a.G + g;
+    rid_l = (rb * p.T + rt) * p.Hq + hq;
+    q_l = rb * p.q_stride_b + rt * p.q_stride_t + hq * p.q_stride_h;
   }
-  __syncthreads();
-  int64_t n = 0;
-  if (GATHER) {
-    n = s_lim[0] > 0 ? p.W : 0;
-  } else {
-    for (int i = 0; i < nrow; i++) n = max(n, (int64_t)s_lim[i]);
-  }
-  it.k0 = (int64_t)u0 * C::UNIT;
-  it.k1 = min(n, (int64_t)u1 * C::UNIT);
+  const int most = __reduce_max_sync(0xffffffffu, lim_l);
+  const int n = GATHER ? (most > 0 ? (int)p.W : 0) : most;  // keys of the sequence
+  const int k0 = u0 * C::UNIT, k1 = min(n, u1 * C::UNIT);
   const int parts_all = a.parts_prefix + a.parts_private;
-  const int parts = PREFIX ? a.parts_prefix : a.parts_private, at = PREFIX ? 0 : a.parts_prefix;
-  // the block with a sequence's last unit marks the partial results that the
+  const int parts = PREFIX ? a.parts_prefix : a.parts_private, at0 = PREFIX ? 0 : a.parts_prefix;
+  // the warp with a sequence's last unit marks the partial results that the
   // sequence does not have
-  if (u1 == units && threadIdx.x < nrow)
-    for (int i = part + 1; i < parts; i++) a.pml[(int64_t)s_rowid[threadIdx.x] * parts_all + at + i] = make_float2(-INFINITY, 0.f);
-  part += at;
-  if (it.k0 >= it.k1) {
-    if (threadIdx.x < nrow) a.pml[(int64_t)s_rowid[threadIdx.x] * parts_all + part] = make_float2(-INFINITY, 0.f);
-    __syncthreads();
+  if (u1 == units && lane < nrow)
+    for (int i = part + 1; i < parts; i++) a.pml[(int64_t)rid_l * parts_all + at0 + i] = make_float2(-INFINITY, 0.f);
+  part += at0;
+  if (k0 >= k1) {
+    if (lane < nrow) a.pml[(int64_t)rid_l * parts_all + part] = make_float2(-INFINITY, 0.f);
     return;
   }
 
-  // ---- this warp's tiles: w, w + kWarps, ... of the piece
-  const int ntile = (int)((it.k1 - it.k0 + KT - 1) / KT);
-  const int mine = (ntile - warp + kWarps - 1) / kWarps;
-  const uint32_t ring = smem_u32(sring) + warp * kStages * C::STAGE;
-  int* slots = sslot + warp * kStages * KT;
+  const char* kb;
+  const char* vb;
+  int64_t ks_b, vs_b;  // bytes between keys, and between values
+  if (PREFIX) {
+    kb = (const char*)p.pk + 2 * h * p.pk_stride_h;
+    vb = (const char*)p.pv + 2 * h * p.pv_stride_h;
+    ks_b = 2 * p.pk_stride_s;
+    vs_b = 2 * p.pv_stride_s;
+  } else {
+    kb = (const char*)p.k + 2 * ((int64_t)b * p.k_stride_b + h * p.k_stride_h);
+    vb = (const char*)p.v + 2 * ((int64_t)b * p.v_stride_b + h * p.v_stride_h);
+    ks_b = 2 * p.k_stride_s;
+    vs_b = 2 * p.v_stride_s;
+  }
+  const int mine = (k1 - k0 + KT - 1) / KT;  // tiles
   const int32_t* list = nullptr;
   if (GATHER)
     list = p.ids + (p.ids_per_head ? (((int64_t)b * p.T + t) * p.n_kv + h) * p.W : ((int64_t)b * p.T + t) * p.W);
-  const int glim = GATHER ? s_lim[0] : 0;
-
-  int32_t next_id = -1;  // GATHER: lane i holds list entry i of the next tile to copy
+  // GATHER: lane i holds list entry i of the tile whose keys are copied next,
+  // and its slot (-1: not a visible one) in the one whose values are
+  int key_id = -1, value_id = -1;
   auto load_ids = [&](int j) {
-    if (!GATHER) return;
-    const int64_t at = it.k0 + (int64_t)(warp + j * kWarps) * KT + lane;
-    next_id = (lane < KT && j < mine && at < it.k1) ? __ldg(list + at) : -1;
+    const int at = k0 + j * KT + lane;
+    key_id = (lane < KT && j < mine && at < k1) ? __ldg(list + at) : -1;
   };
-  auto copy_tile = [&](int j) {
-    if (j < mine) {
-      const uint32_t sk = ring + (j % kStages) * C::STAGE, sv = sk + C::STAGE / 2;
-      const int64_t base = it.k0 + (int64_t)(warp + j * kWarps) * KT;
-      if (GATHER && lane < KT) slots[(j % kStages) * KT + lane] = (next_id >= 0 && next_id < glim) ? next_id : -1;
-      constexpr int RPI = 32 / CH;  // rows of one warp-wide copy
-      const int c = lane % CH;
+  // copies tile j's keys or values into its half of the ring slot
+  auto copy = [&](int j, const char* src, int64_t stride, uint32_t dst, int ids) {
+    constexpr int RPI = 32 / CH;  // rows of one warp-wide copy
+    const int c = lane % CH, base = k0 + j * KT;
 #pragma unroll
-      for (int i = 0; i < KT / RPI; i++) {
-        const int r = i * RPI + lane / CH;
-        int64_t key;
-        bool live;
-        if (GATHER) {
-          const int id = __shfl_sync(0xffffffffu, next_id, r);
-          live = id >= 0 && id < glim;
-          key = live ? id : 0;
-        } else {
-          live = base + r < it.k1;
-          key = live ? base + r : it.k0;
-        }
-        cp_async_16z(sk + swz<D>(r, c), it.k + key * it.ks + c * 16, live);
-        cp_async_16z(sv + swz<D>(r, c), it.v + key * it.vs + c * 16, live);
+    for (int i = 0; i < KT / RPI; i++) {
+      const int r = i * RPI + lane / CH;
+      int key;
+      bool live;
+      if (GATHER) {
+        key = __shfl_sync(0xffffffffu, ids, r);
+        live = key >= 0;
+        key = max(key, 0);
+      } else {
+        key = base + r;
+        live = key < k1;
+        key = live ? key : k0;
       }
-      load_ids(j + 1);
+      cp_async_16z(dst + swz<D>(r, c), src + key * stride + c * 16, live);
+    }
+  };
+  auto copy_keys = [&](int j) {
+    if (j < mine) {
+      if (GATHER) {
+        value_id = key_id >= 0 && key_id < most ? key_id : -1;
+        if (lane < KT) slots[(j & 3) * KT + lane] = value_id;
+        load_ids(j + 1);
+      }
+      copy(j, kb, ks_b, ring + (j & 1) * 2 * C::HALF, value_id);
     }
     cp_async_commit();
   };
+  auto copy_values = [&](int j) {
+    if (j < mine) copy(j, vb, vs_b, ring + (j & 1) * 2 * C::HALF + C::HALF, value_id);
+    cp_async_commit();
+  };
+  if (GATHER) load_ids(0);
+  copy_keys(0);
+  copy_values(0);
+  copy_keys(1);
+  copy_values(1);
 
-  load_ids(0);
-#pragma unroll
-  for (int j = 0; j < kStages - 1; j++) copy_tile(j);
-
-  // ---- queries: rows into shared memory, then operand fragments
-  for (int i = threadIdx.x; i < R * CH; i += blockDim.x) {
-    const int r = i / CH, c = i % CH;
-    const int id = s_rowid[r];
-    uint4 x = make_uint4(0, 0, 0, 0);
-    if (id >= 0) {
-      const int bt = id / p.Hq, hq = id - bt * p.Hq, rb = bt / p.T;
-      const int64_t e = rb * p.q_stride_b + (bt - rb * p.T) * p.q_stride_t + hq * p.q_stride_h;
-      x = __ldg(reinterpret_cast<const uint4*>((const char*)p.q + 2 * e) + c);
-    }
-    *reinterpret_cast<uint4*>(sq + swz<D>(r, c)) = x;
-  }
-  __syncthreads();
+  // the queries, as operand fragments: row lane / 4 (and 8 on) of a 16-row tile,
+  // pairs of dims 2 (lane % 4) (and 8 on)
   uint32_t qf[MT][KS][4];
+  int lim[MT][2], rid[MT][2];
 #pragma unroll
   for (int m = 0; m < MT; m++)
 #pragma unroll
-    for (int s = 0; s < KS; s++)
-      ldsm_x4(qf[m][s], smem_u32(sq) + swz<D>(m * 16 + (lane & 15), 2 * s + (lane >> 4)));
+    for (int e = 0; e < 2; e++) {
+      const int r = m * 16 + (lane >> 2) + 8 * e;
+      rid[m][e] = __shfl_sync(0xffffffffu, rid_l, r);
+      lim[m][e] = __shfl_sync(0xffffffffu, lim_l, r);
+      const int64_t q_at = __shfl_sync(0xffffffffu, q_l, r);
+      const uint32_t* q = reinterpret_cast<const uint32_t*>((const char*)p.q + 2 * q_at) + (lane & 3);
+#pragma unroll
+      for (int ks = 0; ks < KS; ks++) {
+        qf[m][ks][e] = rid[m][e] >= 0 ? __ldg(q + 8 * ks) : 0u;
+        qf[m][ks][e + 2] = rid[m][e] >= 0 ? __ldg(q + 8 * ks + 4) : 0u;
+      }
+    }
 
   float o[MT][D / 8][4];
   float mx[MT][2], sum[MT][2];
-  int lim[MT][2];
-  int rid[MT][2];
 #pragma unroll
   for (int m = 0; m < MT; m++) {
 #pragma unroll
@@ -252,18 +237,16 @@ __device__ __forceinline__ void stream_item(const AttnArgs& a, int h, int tile, 
     for (int e = 0; e < 2; e++) {
       mx[m][e] = -INFINITY;
       sum[m][e] = 0.f;
-      const int r = m * 16 + (lane >> 2) + 8 * e;
-      lim[m][e] = GATHER ? 0 : s_lim[r];
-      rid[m][e] = s_rowid[r];
     }
   }
 
+  // Copies are committed in the order keys 0, values 0, keys 1, values 1, ...;
+  // at either wait the three youngest groups may still be on their way.
   for (int j = 0; j < mine; j++) {
-    cp_async_wait_group<kStages - 2>();
-    __syncwarp();  // every lane's copies of tile j have landed, every lane is done with tile j - 1
-    copy_tile(j + kStages - 1);
-    const uint32_t sk = ring + (j % kStages) * C::STAGE, sv = sk + C::STAGE / 2;
-    const int64_t base = it.k0 + (int64_t)(warp + j * kWarps) * KT;
+    const uint32_t sk = ring + (j & 1) * 2 * C::HALF, sv = sk + C::HALF;
+    const int base = k0 + j * KT;
+    cp_async_wait_group<3>();
+    __syncwarp();  // every lane's copies of the keys have landed
     float s[MT][NT][4];
 #pragma unroll
     for (int m = 0; m < MT; m++)
@@ -283,6 +266,8 @@ __device__ __forceinline__ void stream_item(const AttnArgs& a, int h, int tile, 
           mma16816<BF16>(s[m][i + 1], qf[m][ks], kf[2], kf[3]);
         }
       }
+    __syncwarp();  // every lane has read the keys
+    copy_keys(j + 2);
     // scores in units of log2, masked, and the running maximum
     const int c0 = 2 * (lane & 3);
 #pragma unroll
@@ -293,17 +278,17 @@ __device__ __forceinline__ void stream_item(const AttnArgs& a, int h, int tile, 
 #pragma unroll
         for (int e = 0; e < 4; e++) {
           const int col = 8 * i + c0 + (e & 1);
-          const bool see = GATHER ? slots[(j % kStages) * KT + col] >= 0 : (int)base + col < lim[m][e >> 1];
+          const bool see = GATHER ? slots[(j & 3) * KT + col] >= 0 : base + col < lim[m][e >> 1];
           s[m][i][e] = see ? s[m][i][e] * a.scale_log2 : -INFINITY;
           top[e >> 1] = fmaxf(top[e >> 1], s[m][i][e]);
         }
       if (!PREFIX && a.sc) {
 #pragma unroll
         for (int i = 0; i < NT; i++) {
-          const int64_t at = base + 8 * i + c0;
+          const int at = base + 8 * i + c0;
 #pragma unroll
           for (int e = 0; e < 2; e++)
-            if (rid[m][e] >= 0 && at < it.k1)  // the pair's second half lies inside the padded row
+            if (rid[m][e] >= 0 && at < k1)  // the pair's second half lies inside the padded row
               *reinterpret_cast<float2*>(a.sc + (int64_t)rid[m][e] * a.sc_ld + at) =
                   make_float2(s[m][i][2 * e], s[m][i][2 * e + 1]);
         }
@@ -337,6 +322,8 @@ __device__ __forceinline__ void stream_item(const AttnArgs& a, int h, int tile, 
         }
     }
     // weights (rounded to the element type) times values
+    cp_async_wait_group<3>();
+    __syncwarp();
 #pragma unroll
     for (int kk = 0; kk < KT / 16; kk++) {
       uint32_t pf[MT][4];
@@ -358,60 +345,26 @@ __device__ __forceinline__ void stream_item(const AttnArgs& a, int h, int tile, 
         }
       }
     }
+    __syncwarp();  // every lane has read the values
+    copy_values(j + 2);
   }
   cp_async_wait_group<0>();
-
-  // ---- join the four warps
 #pragma unroll
   for (int m = 0; m < MT; m++)
 #pragma unroll
     for (int e = 0; e < 2; e++) {
       sum[m][e] += __shfl_xor_sync(0xffffffffu, sum[m][e], 1);
       sum[m][e] += __shfl_xor_sync(0xffffffffu, sum[m][e], 2);
-      if ((lane & 3) == 0) s_ml[warp][m * 16 + (lane >> 2) + 8 * e] = make_float2(mx[m][e], sum[m][e]);
+      if (rid[m][e] < 0) continue;
+      const int64_t at = (int64_t)rid[m][e] * parts_all + part;
+      if ((lane & 3) == 0) a.pml[at] = make_float2(mx[m][e], sum[m][e]);
+      if (sum[m][e] > 0.f) {
+#pragma unroll
+        for (int i = 0; i < D / 8; i++)
+          *reinterpret_cast<float2*>(a.po + at * D + 8 * i + 2 * (lane & 3)) = make_float2(o[m][i][2 * e], o[m][i][2 * e + 1]);
+      }
     }
-  __syncthreads();  // every warp is done with its ring: it holds the outputs now
-  float* so = reinterpret_cast<float*>(sring);  // [warp][R][D]
-  static_assert(kWarps * R * D * 4 <= C::RING, "the ring holds the warps' outputs");
-#pragma unroll
-  for (int m = 0; m < MT; m++)
-#pragma unroll
-    for (int e = 0; e < 2; e++) {
-      const int r = m * 16 + (lane >> 2) + 8 * e;
-      if (r >= nrow) continue;
-      float top = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kWarps; w++) top = fmaxf(top, s_ml[w][r].x);
-      const float f = top == -INFINITY ? 0.f : attn_ex2(mx[m][e] - top);
-#pragma unroll
-      for (int i = 0; i < D / 8; i++)
-        *reinterpret_cast<float2*>(so + ((size_t)warp * R + r) * D + 8 * i + 2 * (lane & 3)) =
-            make_float2(o[m][i][2 * e] * f, o[m][i][2 * e + 1] * f);
-    }
-  if (threadIdx.x < nrow) {
-    float top = -INFINITY, l = 0.f;
-    for (int w = 0; w < kWarps; w++) top = fmaxf(top, s_ml[w][threadIdx.x].x);
-    for (int w = 0; w < kWarps; w++)
-      if (top != -INFINITY) l += s_ml[w][threadIdx.x].y * attn_ex2(s_ml[w][threadIdx.x].x - top);
-    s_tot[threadIdx.x] = make_float2(top, l);
-    a.pml[(int64_t)s_rowid[threadIdx.x] * parts_all + part] = make_float2(top, l);
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < nrow * (D / 4); i += blockDim.x) {
-    const int r = i / (D / 4), d = (i % (D / 4)) * 4;
-    if (s_tot[r].y == 0.f) continue;
-    float4 x = *reinterpret_cast<const float4*>(so + (size_t)r * D + d);
-#pragma unroll
-    for (int w = 1; w < kWarps; w++) {
-      const float4 y = *reinterpret_cast<const float4*>(so + ((size_t)w * R + r) * D + d);
-      x.x += y.x;
-      x.y += y.y;
-      x.z += y.z;
-      x.w += y.w;
-    }
-    *reinterpret_cast<float4*>(a.po + ((int64_t)s_rowid[r] * parts_all + part) * D + d) = x;
-  }
-  __syncthreads();  // the next item takes this memory
+  __syncwarp();
 }
 
 template <int D, int MT, bool BF16, bool GATHER>
@@ -420,23 +373,25 @@ __global__ void __launch_bounds__(32 * kWarps, MT == 1 ? 3 : 2)
   using C = StreamCfg<D, MT>;
   constexpr int NT = 32 * kWarps;
   __shared__ int s_sum[kWarps];
-  __shared__ int s_start, s_seq;
+  __shared__ int s_first[NT];
   grid_let_next_start();
   const attn_problem& p = a.p;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int group = blockIdx.x / line.members, member = blockIdx.x - group * line.members;
+  const int w = blockIdx.x * kWarps + warp;
+  const int group = w / line.members, member = w - group * line.members;
   const int tile = member / p.n_kv, h = member - tile * p.n_kv;
   const int seqs = line.seqs;                                   // private sequences
   const int list_units = (int)((p.W + C::UNIT - 1) / C::UNIT);  // of a gathered list
 
   // the line's length (below 2^31, the plan checks), and where on it each
   // thread's share of the requests begins
-  int mine = 0, total = line.prefix_units;
+  int total = line.prefix_units;
   const int per = (seqs + NT - 1) / NT;
-  const int b0 = min(seqs, tid * per), b1 = min(seqs, b0 + per);
   if (GATHER) {
     total += seqs * list_units;
-  } else {
+  } else if (seqs) {
+    const int b0 = min(seqs, tid * per), b1 = min(seqs, b0 + per);
+    int mine = 0;
     for (int b = b0; b < b1; b++) mine += cache_units<C::UNIT>(p, b);
     int incl = mine;
 #pragma unroll
@@ -447,11 +402,12 @@ __global__ void __launch_bounds__(32 * kWarps, MT == 1 ? 3 : 2)
     if (lane == 31) s_sum[warp] = incl;
     __syncthreads();
     int before = line.prefix_units;
-    for (int w = 0; w < kWarps; w++) {
-      total += s_sum[w];
-      if (w < warp) before += s_sum[w];
+    for (int x = 0; x < kWarps; x++) {
+      total += s_sum[x];
+      if (x < warp) before += s_sum[x];
     }
-    mine = before + incl - mine;
+    s_first[tid] = before + incl - mine;
+    __syncthreads();
   }
   // the cut: `groups` shares of `each` units, the first `extra` of them one longer
   const int groups = min(line.groups, max(1, total / line.least));
@@ -462,15 +418,7 @@ __global__ void __launch_bounds__(32 * kWarps, MT == 1 ? 3 : 2)
   };
   int lo = group * each + min(group, extra);
   const int hi = group < groups ? lo + each + (group < extra ? 1 : 0) : lo;
-  // The finish kernel waits for this grid alone, so it has to end behind the
-  // one before it: one block waits for that (a wait of every block would keep
-  // the next ones from their places).
-  const bool waits = blockIdx.x == gridDim.x - 1;
-  if (lo >= hi) {
-    if (waits) grid_wait();
-    return;
-  }
-  if (lo < line.prefix_units) {
+  if (lo < hi && lo < line.prefix_units) {
     const int u1 = min(hi, line.prefix_units);
     stream_item<D, MT, BF16, false, true>(a, h, tile, 0, 0, lo, u1, line.prefix_units, group);
     lo = u1;
@@ -482,20 +430,18 @@ __global__ void __launch_bounds__(32 * kWarps, MT == 1 ? 3 : 2)
       start = line.prefix_units + seq * list_units;
       units = list_units;
     } else {
-      __syncthreads();
-      int at = mine;
-      for (int b = b0; b < b1; b++) {
-        const int u = cache_units<C::UNIT>(p, b);
-        if (at <= lo && lo < at + u) {
-          s_seq = b;
-          s_start = at;
-        }
-        at += u;
-      }
-      __syncthreads();
-      seq = s_seq;
-      start = s_start;
+      // the last thread whose requests begin at or before lo, then one by one
+      int last = -1;
+#pragma unroll
+      for (int x = 0; x < NT; x += 32)
+        last += __popc(__ballot_sync(0xffffffffu, s_first[x + lane] <= lo && (x + lane) * per < seqs));
+      seq = last * per;
+      start = s_first[last];
       units = cache_units<C::UNIT>(p, seq);
+      while (start + units <= lo) {
+        start += units;
+        units = cache_units<C::UNIT>(p, ++seq);
+      }
     }
     while (true) {
       const int b = GATHER ? seq / p.T : seq;
@@ -508,19 +454,21 @@ __global__ void __launch_bounds__(32 * kWarps, MT == 1 ? 3 : 2)
       if (!GATHER) units = cache_units<C::UNIT>(p, seq);
     }
   }
-  if (waits) grid_wait();
+  // The finish kernel waits for this grid alone, so it has to end behind the
+  // one before it: one block waits for that (a wait of every block would keep
+  // the next ones from their places).
+  if (blockIdx.x == gridDim.x - 1) grid_wait();
 }
 
 template <int D, int MT, bool BF16, bool GATHER>
 cudaError_t launch(const AttnArgs& a, const StreamLine& line, bool after, cudaStream_t st) {
   using C = StreamCfg<D, MT>;
-  static_assert(C::UNIT == stream_unit(D), "the plan counts in these units");
-  const int smem = C::RING + C::SLOTS + 16 * MT * D * 2;
+  const int smem = kWarps * (GATHER ? C::WARP_BYTES : C::RING);
   auto kern = attn_stream_kernel<D, MT, BF16, GATHER>;
   static KernelReady ready;
   cudaError_t e = ready.once([&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
   if (e != cudaSuccess) return e;
-  return launch_after(kern, dim3((unsigned)(line.members * line.groups)), 32 * kWarps, smem, st, after, a, line);
+  return launch_after(kern, dim3((unsigned)((line.members * line.groups + kWarps - 1) / kWarps)), 32 * kWarps, smem, st, after, a, line);
 }
 
 template <int D, bool BF16, bool GATHER>
