@@ -65,6 +65,9 @@ StreamLine plan_stream(AttnArgs& a) {
   const int64_t total = l.prefix_units + l.seqs * longest;
   l.groups = (int)std::max<int64_t>(1, (l.row_tile == 16 ? 12 : 8) * (int64_t)sm_count() / l.members);
   l.least = (int)std::max<int64_t>(1, ceil_div(total, 4 * (int64_t)l.groups));
+  // Lists have one length; short lines are cut as if all caches were full, which
+  // saves their blocks the look at the lengths.
+  if (p.ids || total <= 2 * l.groups) l.uniform = (int)longest;
   auto parts = [&](int64_t units) { return units == 0 ? 0 : (int)std::min(units, ceil_div(units - 1, l.least) + 1); };
   if (prefix) a.parts_prefix = parts(l.prefix_units);
   a.parts_private = l.seqs ? parts(longest) : 0;

@@ -79,6 +79,7 @@ struct StreamLine {
   int groups;
   int prefix_units;  // 0: the prefix is not streamed
   int seqs;          // private sequences: requests, or (request, token) lists
+  int uniform;       // units that every private sequence counts as, or 0: as many as its length asks
   int least;         // smallest share of a group, so that no sequence has more parts than planned
 };
 // after: a kernel of the same call comes before this one, and does not write

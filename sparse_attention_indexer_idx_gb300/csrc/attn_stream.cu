@@ -13,9 +13,10 @@
 // 16-byte cp.async into a ring (swizzled, so ldmatrix is free of bank
 // conflicts) and keeps the running maximum, sum and output in registers.
 // Nothing waits for another warp: the start and the end of one warp's sequence
-// pass while the others of the SM stream.  The keys' half of a ring slot is
-// refilled as soon as the scores are formed, the values' half after the second
-// product, so that between one and two tiles are on their way all the time.
+// pass while the others of the SM stream.  One tile of each of the SM's twelve
+// warps is on its way all the time, 96 KB; refilling each half of a ring slot as
+// soon as it was used, up to twice as much, cost 8 percent (272 against 251 us
+// for 16 caches of 24,576 slots on average, 8 KV heads of 128).
 //
 // The products use mma.sync (16 x 8 x 16): a decode row group is 1 to 32 rows,
 // so the tensor work is a few percent of the time the bytes take, and the
@@ -76,7 +77,7 @@ struct StreamCfg {
   static constexpr int CH = D / 8;                // 16-byte chunks of a row
   static constexpr int HALF = KT * D * 2;         // bytes of a tile's keys, and of its values
   static constexpr int RING = 2 * 2 * HALF;       // two slots
-  static constexpr int SLOTS = 4 * KT;            // slot numbers of gathered tiles
+  static constexpr int SLOTS = 2 * KT;            // slot numbers of gathered tiles
   static constexpr int WARP_BYTES = RING + SLOTS * 4;
   static_assert(UNIT == 4 * KT, "four tiles");
 };
@@ -156,54 +157,45 @@ __device__ __forceinline__ void stream_item(const AttnArgs& a, int h, int tile, 
   const int32_t* list = nullptr;
   if (GATHER)
     list = p.ids + (p.ids_per_head ? (((int64_t)b * p.T + t) * p.n_kv + h) * p.W : ((int64_t)b * p.T + t) * p.W);
-  // GATHER: lane i holds list entry i of the tile whose keys are copied next,
-  // and its slot (-1: not a visible one) in the one whose values are
-  int key_id = -1, value_id = -1;
+  int next_id = -1;  // GATHER: lane i holds list entry i of the tile to copy next
   auto load_ids = [&](int j) {
     const int at = k0 + j * KT + lane;
-    key_id = (lane < KT && j < mine && at < k1) ? __ldg(list + at) : -1;
+    next_id = (lane < KT && j < mine && at < k1) ? __ldg(list + at) : -1;
   };
-  // copies tile j's keys or values into its half of the ring slot
-  auto copy = [&](int j, const char* src, int64_t stride, uint32_t dst, int ids) {
-    constexpr int RPI = 32 / CH;  // rows of one warp-wide copy
-    const int c = lane % CH, base = k0 + j * KT;
-#pragma unroll
-    for (int i = 0; i < KT / RPI; i++) {
-      const int r = i * RPI + lane / CH;
-      int key;
-      bool live;
-      if (GATHER) {
-        key = __shfl_sync(0xffffffffu, ids, r);
-        live = key >= 0;
-        key = max(key, 0);
-      } else {
-        key = base + r;
-        live = key < k1;
-        key = live ? key : k0;
-      }
-      cp_async_16z(dst + swz<D>(r, c), src + key * stride + c * 16, live);
-    }
-  };
-  auto copy_keys = [&](int j) {
+  // copies tile j into its ring slot
+  auto copy = [&](int j) {
     if (j < mine) {
+      constexpr int RPI = 32 / CH;  // rows of one warp-wide copy
+      const uint32_t sk = ring + (j & 1) * 2 * C::HALF, sv = sk + C::HALF;
+      const int c = lane % CH, base = k0 + j * KT;
+      int slot = -1;  // GATHER: lane i's, -1: not a visible one
       if (GATHER) {
-        value_id = key_id >= 0 && key_id < most ? key_id : -1;
-        if (lane < KT) slots[(j & 3) * KT + lane] = value_id;
+        slot = next_id >= 0 && next_id < most ? next_id : -1;
+        if (lane < KT) slots[(j & 1) * KT + lane] = slot;
         load_ids(j + 1);
       }
-      copy(j, kb, ks_b, ring + (j & 1) * 2 * C::HALF, value_id);
+#pragma unroll
+      for (int i = 0; i < KT / RPI; i++) {
+        const int r = i * RPI + lane / CH;
+        int key;
+        bool live;
+        if (GATHER) {
+          key = __shfl_sync(0xffffffffu, slot, r);
+          live = key >= 0;
+          key = max(key, 0);
+        } else {
+          key = base + r;
+          live = key < k1;
+          key = live ? key : k0;
+        }
+        cp_async_16z(sk + swz<D>(r, c), kb + key * ks_b + c * 16, live);
+        cp_async_16z(sv + swz<D>(r, c), vb + key * vs_b + c * 16, live);
+      }
     }
-    cp_async_commit();
-  };
-  auto copy_values = [&](int j) {
-    if (j < mine) copy(j, vb, vs_b, ring + (j & 1) * 2 * C::HALF + C::HALF, value_id);
     cp_async_commit();
   };
   if (GATHER) load_ids(0);
-  copy_keys(0);
-  copy_values(0);
-  copy_keys(1);
-  copy_values(1);
+  copy(0);
 
   // the queries, as operand fragments: row lane / 4 (and 8 on) of a 16-row tile,
   // pairs of dims 2 (lane % 4) (and 8 on)
@@ -240,13 +232,12 @@ __device__ __forceinline__ void stream_item(const AttnArgs& a, int h, int tile, 
     }
   }
 
-  // Copies are committed in the order keys 0, values 0, keys 1, values 1, ...;
-  // at either wait the three youngest groups may still be on their way.
   for (int j = 0; j < mine; j++) {
     const uint32_t sk = ring + (j & 1) * 2 * C::HALF, sv = sk + C::HALF;
     const int base = k0 + j * KT;
-    cp_async_wait_group<3>();
-    __syncwarp();  // every lane's copies of the keys have landed
+    cp_async_wait_group<0>();
+    __syncwarp();  // every lane's copies of tile j have landed, every lane is done with tile j - 1
+    copy(j + 1);
     float s[MT][NT][4];
 #pragma unroll
     for (int m = 0; m < MT; m++)
@@ -266,8 +257,6 @@ __device__ __forceinline__ void stream_item(const AttnArgs& a, int h, int tile, 
           mma16816<BF16>(s[m][i + 1], qf[m][ks], kf[2], kf[3]);
         }
       }
-    __syncwarp();  // every lane has read the keys
-    copy_keys(j + 2);
     // scores in units of log2, masked, and the running maximum
     const int c0 = 2 * (lane & 3);
 #pragma unroll
@@ -278,7 +267,7 @@ __device__ __forceinline__ void stream_item(const AttnArgs& a, int h, int tile, 
 #pragma unroll
         for (int e = 0; e < 4; e++) {
           const int col = 8 * i + c0 + (e & 1);
-          const bool see = GATHER ? slots[(j & 3) * KT + col] >= 0 : base + col < lim[m][e >> 1];
+          const bool see = GATHER ? slots[(j & 1) * KT + col] >= 0 : base + col < lim[m][e >> 1];
           s[m][i][e] = see ? s[m][i][e] * a.scale_log2 : -INFINITY;
           top[e >> 1] = fmaxf(top[e >> 1], s[m][i][e]);
         }
@@ -322,8 +311,6 @@ __device__ __forceinline__ void stream_item(const AttnArgs& a, int h, int tile, 
         }
     }
     // weights (rounded to the element type) times values
-    cp_async_wait_group<3>();
-    __syncwarp();
 #pragma unroll
     for (int kk = 0; kk < KT / 16; kk++) {
       uint32_t pf[MT][4];
@@ -345,8 +332,6 @@ __device__ __forceinline__ void stream_item(const AttnArgs& a, int h, int tile, 
         }
       }
     }
-    __syncwarp();  // every lane has read the values
-    copy_values(j + 2);
   }
   cp_async_wait_group<0>();
 #pragma unroll
@@ -381,15 +366,14 @@ __global__ void __launch_bounds__(32 * kWarps, MT == 1 ? 3 : 2)
   const int group = w / line.members, member = w - group * line.members;
   const int tile = member / p.n_kv, h = member - tile * p.n_kv;
   const int seqs = line.seqs;                                   // private sequences
-  const int list_units = (int)((p.W + C::UNIT - 1) / C::UNIT);  // of a gathered list
 
   // the line's length (below 2^31, the plan checks), and where on it each
   // thread's share of the requests begins
   int total = line.prefix_units;
   const int per = (seqs + NT - 1) / NT;
-  if (GATHER) {
-    total += seqs * list_units;
-  } else if (seqs) {
+  if (line.uniform) {
+    total += seqs * line.uniform;
+  } else if (!GATHER && seqs) {
     const int b0 = min(seqs, tid * per), b1 = min(seqs, b0 + per);
     int mine = 0;
     for (int b = b0; b < b1; b++) mine += cache_units<C::UNIT>(p, b);
@@ -425,10 +409,10 @@ __global__ void __launch_bounds__(32 * kWarps, MT == 1 ? 3 : 2)
   }
   if (lo < hi) {
     int seq, units, start;  // the sequence that holds lo
-    if (GATHER) {
-      seq = (lo - line.prefix_units) / list_units;
-      start = line.prefix_units + seq * list_units;
-      units = list_units;
+    if (GATHER || line.uniform) {
+      seq = (lo - line.prefix_units) / line.uniform;
+      start = line.prefix_units + seq * line.uniform;
+      units = line.uniform;
     } else {
       // the last thread whose requests begin at or before lo, then one by one
       int last = -1;
@@ -451,7 +435,7 @@ __global__ void __launch_bounds__(32 * kWarps, MT == 1 ? 3 : 2)
       lo = start;
       if (lo >= hi) break;
       seq++;
-      if (!GATHER) units = cache_units<C::UNIT>(p, seq);
+      if (!GATHER && !line.uniform) units = cache_units<C::UNIT>(p, seq);
     }
   }
   // The finish kernel waits for this grid alone, so it has to end behind the
