@@ -603,7 +603,7 @@ def attn_shared_workspace_size(p: AttnProblem, mass: bool = True) -> int:
 
 def _out(t: torch.Tensor, name: str, shape, dtype):
     """_dense for one shape, quick where the tensor is right."""
-    if t.shape == shape and t.dtype == dtype and t.is_cuda and t.is_contiguous():
+    if t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.is_cuda:
         return t.data_ptr()
     return _dense(t, name, (tuple(shape),), dtype)
 
@@ -621,8 +621,9 @@ def attn_shared(p: AttnProblem, out: torch.Tensor, lse: Optional[torch.Tensor], 
         _need(p.k is not None, "mass: there is no private cache")
         heads = mass.shape[1] if mass.dim() == 3 and mass.shape[1] == cp.n_kv else 1
         pm = _out(mass, "mass", (cp.B, heads, cp.S), torch.float32)
-    _check((_lib or lib()).attn_shared(ref, po, pl, pm, heads, _ptr(ws), ws.numel() * ws.element_size(),
-                                       _raw_stream(stream)))
+    st = (_lib or lib()).attn_shared(ref, po, pl, pm, heads, _ptr(ws), ws.nbytes, _raw_stream(stream))
+    if st:
+        _check(st)
     return out, lse, mass
 
 
@@ -685,5 +686,7 @@ def cache_evict(p: EvictProblem, out_src: torch.Tensor, out_len: Optional[torch.
         ld = out_mass.shape[-1]
         pm = _out(out_mass, "out_mass", (B, Hm, ld), torch.float32)
     _need(ld >= K, "out_pos and out_mass: rows shorter than n_keep")
-    _check((_lib or lib()).cache_evict(ref, ps, pl, pp, pm, ld, _raw_stream(stream)))
+    st = (_lib or lib()).cache_evict(ref, ps, pl, pp, pm, ld, _raw_stream(stream))
+    if st:
+        _check(st)
     return out_src, out_len, out_pos, out_mass

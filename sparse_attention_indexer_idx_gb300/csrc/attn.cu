@@ -13,15 +13,28 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // Keys of the private part that a row can see at most.
 int64_t private_keys(const attn_problem& p) { return p.S == 0 ? 0 : p.ids ? p.W : p.S; }
 
-// Rows of a KV head up to which the prefix is streamed.
+// Rows of a KV head that one warp of the streaming kernel takes.
 constexpr int64_t kStreamRows = 16;
 
-// Whether the shared prefix goes to the tensor-core kernel.  TMA reads it
-// there, so its strides have to be ones that a tensor map can hold.
-bool prefix_on_tc(const attn_problem& p) {
+// How the prefix is read.
+enum PrefixWay { kNone, kLine, kOwnLine, kTensorCore };
+
+// Up to 16 rows are one warp's: the prefix is streamed on one line with the
+// caches.  More rows would read it again for each 16: where that is little, the
+// streaming kernel still does it, beside the caches, because the tensor-core
+// kernel's launch and start take about 9 us; else it goes to that kernel, with
+// TMA, if a tensor map can hold its strides.
+PrefixWay prefix_way(const attn_problem& p) {
+  constexpr int64_t kLittle = 32 << 20;  // bytes: about 4 us from L2
+  const int64_t rows = (int64_t)p.B * p.T * (p.Hq / p.n_kv);
+  if (p.P == 0) return kNone;
+  if (rows <= kStreamRows) return kLine;
+  if (ceil_div(rows, kStreamRows) * p.n_kv * p.P * 4 * p.D <= kLittle) return kOwnLine;
   auto legal = [](int64_t n, int64_t stride) { return n <= 1 || (stride > 0 && stride < ((int64_t)1 << 38)); };
-  return p.P > 0 && (int64_t)p.B * p.T * (p.Hq / p.n_kv) > kStreamRows && legal(p.P, p.pk_stride_s) &&
-         legal(p.P, p.pv_stride_s) && legal(p.n_kv, p.pk_stride_h) && legal(p.n_kv, p.pv_stride_h);
+  return legal(p.P, p.pk_stride_s) && legal(p.P, p.pv_stride_s) && legal(p.n_kv, p.pk_stride_h) &&
+                 legal(p.n_kv, p.pv_stride_h)
+             ? kTensorCore
+             : kOwnLine;
 }
 
 // The tensor-core kernel's grid.  A whole number of pieces per (KV head, row
@@ -52,30 +65,37 @@ AttnTcArgs plan_tc(const AttnArgs& a) {
 StreamLine plan_stream(AttnArgs& a) {
   const attn_problem& p = a.p;
   StreamLine l{};
-  const bool prefix = p.P > 0 && !prefix_on_tc(p);
-  const int64_t rows_pre = prefix ? (int64_t)p.B * p.T * a.G : 0;
-  const int64_t rows_prv = p.S == 0 ? 0 : p.ids ? a.G : (int64_t)p.T * a.G;
-  const int64_t rows = std::max<int64_t>(1, std::max(rows_pre, rows_prv));
+  const PrefixWay way = prefix_way(p);
+  const int64_t rows_pre = (int64_t)p.B * p.T * a.G;
+  const int64_t rows = std::max<int64_t>(p.S == 0 ? 1 : p.ids ? a.G : (int64_t)p.T * a.G, way == kLine ? rows_pre : 1);
   l.row_tile = rows <= 16 ? 16 : 32;
   l.members = (int)(p.n_kv * ceil_div(rows, l.row_tile));
-  const int64_t unit = stream_unit(p.D);
-  l.prefix_units = prefix ? (int)ceil_div(p.P, unit) : 0;
+  const int64_t unit = stream_unit(p.D), warps = (l.row_tile == 16 ? 12 : 8) * (int64_t)sm_count();
+  if (way == kLine) l.prefix_units = (int)ceil_div(p.P, unit);
+  if (way == kOwnLine) {
+    l.own_units = (int)ceil_div(p.P, unit);
+    l.own_members = (int)(p.n_kv * ceil_div(rows_pre, l.row_tile));
+    l.own_groups = (int)std::min<int64_t>(l.own_units, std::max<int64_t>(1, warps / l.own_members));
+    l.own_blocks = (int)ceil_div((int64_t)l.own_members * l.own_groups, 4);
+    a.parts_prefix = l.own_groups;
+  }
   const int64_t longest = ceil_div(private_keys(p), unit);
   l.seqs = longest == 0 ? 0 : p.ids ? p.B * p.T : p.B;
   const int64_t total = l.prefix_units + l.seqs * longest;
-  l.groups = (int)std::max<int64_t>(1, (l.row_tile == 16 ? 12 : 8) * (int64_t)sm_count() / l.members);
-  l.least = (int)std::max<int64_t>(1, ceil_div(total, 4 * (int64_t)l.groups));
+  l.groups = total == 0 ? 0 : (int)std::max<int64_t>(1, warps / l.members);
+  l.least = (int)std::max<int64_t>(1, ceil_div(total, 4 * std::max<int64_t>(1, l.groups)));
   // Lists have one length; short lines are cut as if all caches were full, which
   // saves their blocks the look at the lengths.
   if (p.ids || total <= 2 * l.groups) l.uniform = (int)longest;
+  if (l.uniform || l.seqs == 0) l.groups = (int)std::min<int64_t>(l.groups, std::max<int64_t>(1, total / l.least));
   auto parts = [&](int64_t units) { return units == 0 ? 0 : (int)std::min(units, ceil_div(units - 1, l.least) + 1); };
-  if (prefix) a.parts_prefix = parts(l.prefix_units);
+  if (way == kLine) a.parts_prefix = parts(l.prefix_units);
   a.parts_private = l.seqs ? parts(longest) : 0;
   return l;
 }
 
 void plan_parts(AttnArgs& a) {
-  if (prefix_on_tc(a.p)) {
+  if (prefix_way(a.p) == kTensorCore) {
     const AttnTcArgs t = plan_tc(a);
     a.parts_prefix = t.cells_k * (t.whole_cells ? 1 : 2);
   }
@@ -143,10 +163,10 @@ cudaError_t launch_attn_shared(const attn_problem& p, void* out, float* lse, flo
   a.mass = mass;
   a.mass_heads = mass_heads;
   cudaError_t e = cudaSuccess;
-  const bool tc = prefix_on_tc(p);
+  const bool tc = prefix_way(p) == kTensorCore;
   if (tc) e = launch_attn_tc(plan_tc(a), st);
   const StreamLine line = plan_stream(a);
-  if (e == cudaSuccess && line.prefix_units + line.seqs > 0) e = launch_attn_stream(a, line, tc, st);
+  if (e == cudaSuccess && line.own_blocks + line.prefix_units + line.seqs > 0) e = launch_attn_stream(a, line, tc, st);
   if (e == cudaSuccess) e = launch_attn_finish(a, st);
   return e;
 }

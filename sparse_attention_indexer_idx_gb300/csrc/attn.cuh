@@ -77,10 +77,12 @@ struct StreamLine {
   int row_tile;      // 16 or 32 rows of a warp
   int members;       // warps of a group: KV heads times row tiles
   int groups;
-  int prefix_units;  // 0: the prefix is not streamed
+  int prefix_units;  // of the prefix, if its rows need no more row tiles than the caches' do
   int seqs;          // private sequences: requests, or (request, token) lists
   int uniform;       // units that every private sequence counts as, or 0: as many as its length asks
   int least;         // smallest share of a group, so that no sequence has more parts than planned
+  // a short prefix under many rows: a line of its own, taken by the first blocks
+  int own_blocks, own_members, own_groups, own_units;
 };
 // after: a kernel of the same call comes before this one, and does not write
 // what this one reads.

@@ -362,7 +362,20 @@ __global__ void __launch_bounds__(32 * kWarps, MT == 1 ? 3 : 2)
   grid_let_next_start();
   const attn_problem& p = a.p;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int w = blockIdx.x * kWarps + warp;
+  if ((int)blockIdx.x < line.own_blocks) {
+    const int x = blockIdx.x * kWarps + warp;
+    const int group = x / line.own_members, member = x - group * line.own_members;
+    const int tile = member / p.n_kv;
+    if (group < line.own_groups) {
+      const int each = line.own_units / line.own_groups, extra = line.own_units - each * line.own_groups;
+      const int lo = group * each + min(group, extra);
+      stream_item<D, MT, BF16, false, true>(a, member - tile * p.n_kv, tile, 0, 0, lo, lo + each + (group < extra ? 1 : 0),
+                                            line.own_units, group);
+    }
+    if (blockIdx.x == gridDim.x - 1) grid_wait();
+    return;
+  }
+  const int w = ((int)blockIdx.x - line.own_blocks) * kWarps + warp;
   const int group = w / line.members, member = w - group * line.members;
   const int tile = member / p.n_kv, h = member - tile * p.n_kv;
   const int seqs = line.seqs;                                   // private sequences
@@ -452,7 +465,7 @@ cudaError_t launch(const AttnArgs& a, const StreamLine& line, bool after, cudaSt
   static KernelReady ready;
   cudaError_t e = ready.once([&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
   if (e != cudaSuccess) return e;
-  return launch_after(kern, dim3((unsigned)((line.members * line.groups + kWarps - 1) / kWarps)), 32 * kWarps, smem, st, after, a, line);
+  return launch_after(kern, dim3((unsigned)(line.own_blocks + (line.members * line.groups + kWarps - 1) / kWarps)), 32 * kWarps, smem, st, after, a, line);
 }
 
 template <int D, bool BF16, bool GATHER>
