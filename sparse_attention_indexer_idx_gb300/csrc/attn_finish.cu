@@ -18,7 +18,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSlots = 4;    // consecutive slots of a thread: one 16-byte load per row
 constexpr int kRowsAt = 512; // rows whose normalisers are held at a time
-constexpr int kBatch = 8;    // rows loaded before the first is used
+constexpr int kBatch = 8;    // rows loaded before the first is used (dense masses)
 
 template <int D, bool BF16>
 __device__ void join_rows(const AttnArgs& a) {
@@ -99,7 +99,8 @@ __device__ void join_rows(const AttnArgs& a) {
 struct MassRows {
   float lse2[kRowsAt];
   int lim[kRowsAt];
-  int longest;
+  int64_t row[kRowsAt];   // (b*T + t)*Hq + hq
+  int longest, shortest;  // of lim
 };
 
 // Rows (b, t, hq): i-th of the block's, t = t0 + i / heads, hq = hq0 + i %
@@ -109,7 +110,10 @@ __device__ __forceinline__ void load_rows(const AttnArgs& a, MassRows& s, int b,
   const attn_problem& p = a.p;
   const int parts = a.parts_prefix + a.parts_private;
   const int lane = threadIdx.x & 31, sub = lane & 7;
-  if (threadIdx.x == 0) s.longest = 0;
+  if (threadIdx.x == 0) {
+    s.longest = 0;
+    s.shortest = INT32_MAX;
+  }
   __syncthreads();
   for (int i = (threadIdx.x >> 5) * 4 + (lane >> 3); i < ((n + 3) & ~3); i += kWarps * 4) {
     const bool live = i < n;
@@ -145,7 +149,9 @@ __device__ __forceinline__ void load_rows(const AttnArgs& a, MassRows& s, int b,
       const int lim = len < 0 || len > p.S ? 0 : max(0, len - p.T + t + 1);
       s.lse2[i] = m + log2f(l);
       s.lim[i] = lim;
+      s.row[i] = ((int64_t)b * p.T + t) * p.Hq + hq;
       atomicMax(&s.longest, lim);
+      atomicMin(&s.shortest, lim);
     }
   }
   __syncthreads();
@@ -173,58 +179,41 @@ __device__ __forceinline__ void mass_dense(const AttnArgs& a, int64_t block, int
   for (int r0 = 0; r0 < rows; r0 += kRowsAt) {
     const int n = min(kRowsAt, rows - r0);
     const int len = (n + groups - 1) / groups;
-    // this thread's rows of those held; rows of one token lie next to one
-    // another, the next token's Hq rows on
-    const int i0 = min(n, run * len), i1 = min(n, i0 + len);
-    const int token0 = (r0 + i0) / heads, in_token0 = (r0 + i0) % heads;
-    const float* row0 = a.sc + (((int64_t)b * p.T + token0) * p.Hq + m * heads + in_token0) * a.sc_ld;
-    const int64_t next_token = (int64_t)(p.Hq - heads) * a.sc_ld;
-    float4 y[kBatch];
-    int i, in_token;
-    const float* y_at;
-    auto begin = [&](int slot) {
-      i = i0;
-      in_token = in_token0;
-      y_at = row0 + slot;
-    };
-    auto batch = [&](bool inside) {
-#pragma unroll
-      for (int u = 0; u < kBatch; u++) {
-        y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (i + u < i1 && inside) y[u] = *reinterpret_cast<const float4*>(y_at);
-        y_at += a.sc_ld;
-        if (++in_token == heads) {
-          in_token = 0;
-          y_at += next_token;
-        }
-      }
-    };
-    begin(first + mine * kSlots);
-    batch(first + mine * kSlots < most);
+    const int i0 = min(n, run * len), i1 = min(n, i0 + len);  // this thread's rows of those held
     __syncthreads();
     load_rows(a, s, b, 0, m * heads, heads, r0, n);
     for (int at = first; at < most; at += per * lanes * kSlots) {
       const int slot = at + mine * kSlots;
-      const bool inside = slot < most;
-      if (at != first) {
-        begin(slot);
-        batch(inside);
-      }
+      const float* sc = a.sc + slot;
       float add[kSlots] = {};
-      while (i < i1) {
+      int i = i0;
+      if (slot + kSlots <= s.shortest) {  // every row sees all of the thread's slots
+        for (; i + kBatch <= i1; i += kBatch) {
+          float4 y[kBatch];
 #pragma unroll
-        for (int u = 0; u < kBatch; u++) {
-          if (i + u >= i1) break;
-          const float z = s.lse2[i + u];
-          const int left = s.lim[i + u] - slot;
-          if (left > 0) add[0] += attn_ex2(y[u].x - z);
-          if (left > 1) add[1] += attn_ex2(y[u].y - z);
-          if (left > 2) add[2] += attn_ex2(y[u].z - z);
-          if (left > 3) add[3] += attn_ex2(y[u].w - z);
+          for (int u = 0; u < kBatch; u++) y[u] = *reinterpret_cast<const float4*>(sc + s.row[i + u] * a.sc_ld);
+#pragma unroll
+          for (int u = 0; u < kBatch; u++) {
+            const float z = s.lse2[i + u];
+            add[0] += attn_ex2(y[u].x - z);
+            add[1] += attn_ex2(y[u].y - z);
+            add[2] += attn_ex2(y[u].z - z);
+            add[3] += attn_ex2(y[u].w - z);
+          }
         }
-        i += kBatch;
-        if (i < i1) batch(inside);
       }
+      if (slot < s.longest)
+#pragma unroll 4
+        for (; i < i1; i++) {
+          const int left = s.lim[i] - slot;
+          float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (left > 0) y = *reinterpret_cast<const float4*>(sc + s.row[i] * a.sc_ld);
+          const float z = s.lse2[i];
+          if (left > 0) add[0] += attn_ex2(y.x - z);
+          if (left > 1) add[1] += attn_ex2(y.y - z);
+          if (left > 2) add[2] += attn_ex2(y.z - z);
+          if (left > 3) add[3] += attn_ex2(y.w - z);
+        }
       if (groups > 1) {
         __syncthreads();
         s_add[threadIdx.x] = make_float4(add[0], add[1], add[2], add[3]);

@@ -43,7 +43,7 @@ struct SelShared {
   uint32_t wcount[32];
   uint32_t wcount2[32];
   uint32_t scan[32];
-  uint32_t found_bin, found_above;
+  uint32_t found_bin, found_above, found_count;
   uint32_t ties, late, holes;  // this block's counts, read by the cluster
 };
 
@@ -52,6 +52,9 @@ __device__ __forceinline__ uint32_t rank_key(float m, bool guard) {
   if (m != m) m = -INFINITY;
   return score_key(m);
 }
+
+// The lowest n bits, n clamped to 0..32.
+__device__ __forceinline__ unsigned low_bits(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1; }
 
 // Sum of the values of the warps before this one, and of all (a value per
 // warp, at most 32).
@@ -196,6 +199,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_select_kernel(const __gri
           if (above < need && need <= above + v[j]) {
             sh.found_bin = b0 + j;
             sh.found_above = above;
+            sh.found_count = v[j];
           }
           above += v[j];
         }
@@ -207,37 +211,43 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_select_kernel(const __gri
       need -= sh.found_above;
       prefix |= sh.found_bin << (pass == 0 ? 21 : pass == 1 ? 10 : 0);
     }
-    // ties of the last kept key: the lowest slots stay
-    uint32_t t = 0;
-#pragma unroll 4
-    for (int w = w0; w < w1; w++) {
-      const int i = w * 32 + lane;
-      t += i < cnt && keys[i] == prefix;
+    // Ties of the last kept key: the lowest slots stay.  Where all of them do
+    // (the usual case) they need no order.
+    const bool all_ties = need == sh.found_count;
+    uint32_t tie = 0;
+    if (!all_ties) {
+      uint32_t t = 0;
+      for (int w = w0; w < w1; w++) {
+        const int i = w * 32 + lane;
+        t += i < cnt && keys[i] == prefix;
+      }
+      t = __reduce_add_sync(0xffffffffu, t);
+      if (lane == 0) sh.wcount[warp] = t;
+      __syncthreads();
+      uint32_t total;
+      tie = warps_before(sh.wcount, W, warp, &total);
+      if (tid == 0) sh.ties = total;
+      cl.sync();
+      for (int r = 0; r < c; r++) tie += *cl.at(&sh.ties, r);
     }
-    t = __reduce_add_sync(0xffffffffu, t);
-    if (lane == 0) sh.wcount[warp] = t;
-    __syncthreads();
-    uint32_t total;
-    uint32_t tie = warps_before(sh.wcount, W, warp, &total);
-    if (tid == 0) sh.ties = total;
-    cl.sync();
-    for (int r = 0; r < c; r++) tie += *cl.at(&sh.ties, r);
     uint32_t late = 0, holes = 0;
-#pragma unroll 2
     for (int w = w0; w < w1; w++) {
       const int i = w * 32 + lane;
       const uint32_t k = i < cnt ? keys[i] : 0;
-      const bool eq = i < cnt && k == prefix;
-      const unsigned eqs = __ballot_sync(0xffffffffu, eq);
-      const bool stay = i < cnt && (k > prefix || (eq && tie + __popc(eqs & ((1u << lane) - 1)) < need));
-      tie += __popc(eqs);
-      const unsigned word = __ballot_sync(0xffffffffu, stay);
-      late += __popc(__ballot_sync(0xffffffffu, stay && s0 + i >= nk));
+      bool stay = k >= prefix;
+      if (!all_ties) {
+        const unsigned eqs = __ballot_sync(0xffffffffu, k == prefix && i < cnt);
+        stay = k > prefix || (k == prefix && tie + __popc(eqs & ((1u << lane) - 1)) < need);
+        tie += __popc(eqs);
+      }
+      const unsigned word = __ballot_sync(0xffffffffu, stay && i < cnt);
+      const unsigned low = low_bits(nk - (s0 + w * 32)), valid = low_bits(cnt - w * 32);
       if (lane == 0) {
         bitmap[w] = word;
         rank[w] = (uint16_t)holes;  // within the warp's words, for now
       }
-      holes += __popc(__ballot_sync(0xffffffffu, i < cnt && !stay && s0 + i < nk));
+      holes += __popc(~word & valid & low);
+      late += __popc(word & ~low);
     }
     if (lane == 0) {
       sh.wcount[warp] = late;
@@ -252,12 +262,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_select_kernel(const __gri
       sh.holes = all_holes;
     }
     for (int w = w0 + lane; w < w1; w += 32) rank[w] += (uint16_t)holes_before;
-    for (int w = w0; w < w1; w++) {
-      if (s0 + w * 32 + 31 < nk) continue;
-      const int i = w * 32 + lane;
-      const bool is = i < cnt && s0 + i >= nk && ((bitmap[w] >> lane) & 1);
-      const unsigned m = __ballot_sync(0xffffffffu, is);
-      if (is) keys[at + __popc(m & ((1u << lane) - 1))] = (uint32_t)(s0 + i);
+    for (int w = max(w0, (nk - s0) >> 5); w < w1; w++) {
+      const unsigned m = bitmap[w] & ~low_bits(nk - (s0 + w * 32));
+      if ((m >> lane) & 1) keys[at + __popc(m & ((1u << lane) - 1))] = (uint32_t)(s0 + w * 32 + lane);
       at += __popc(m);
     }
     cl.sync();
@@ -266,7 +273,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_select_kernel(const __gri
   // where each new slot comes from: words of 32 new slots in turn over the
   // warps of the whole cluster
   uint32_t holes_of = 0, late_of = 0;  // lane r: holes and late rows of the blocks before block r
-  if (trim) {
+  if (trim && !ONE) {
     uint32_t h = lane < C ? *cl.at(&sh.holes, lane) : 0;
     uint32_t l = lane < C ? *cl.at(&sh.late, lane) : 0;
     holes_of = h;
@@ -289,22 +296,22 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_select_kernel(const __gri
     for (int u = 0; u < 4; u++) {
       const int v = v0 + u * stride;
       const int s = v * 32 + lane;
-      const bool in = v < new_words && s < nk;
-      slot[u] = in ? s : -1;
+      slot[u] = v < new_words && s < nk ? s : -1;
       from[u] = s;
       if (trim && v < new_words) {
-        const int q = v * 32 / slice, w = v - q * (slice >> 5);  // the block that has this word
-        const unsigned word = cl.at(bitmap, q)[w];
-        const bool hole = in && !((word >> lane) & 1);
-        const unsigned m = __ballot_sync(0xffffffffu, hole);
+        const int q = ONE ? 0 : v * 32 / slice, w = v - q * (slice >> 5);  // the block that has this word
+        const unsigned m = ~cl.at(bitmap, q)[w] & low_bits(nk - v * 32);
         if (m) {
-          const uint32_t r = __shfl_sync(0xffffffffu, holes_of, q) + cl.at(rank, q)[w] +
+          const uint32_t r = (ONE ? 0 : __shfl_sync(0xffffffffu, holes_of, q)) + cl.at(rank, q)[w] +
                              __popc(m & ((1u << lane) - 1));
           int z = 0;  // the block that has late row r
+          uint32_t first = 0;
+          if (!ONE) {
 #pragma unroll
-          for (int x = 1; x < kMaxCluster; x++) z += x < C && r >= __shfl_sync(0xffffffffu, late_of, x);
-          const uint32_t first = __shfl_sync(0xffffffffu, late_of, z);
-          if (hole) from[u] = (int)*cl.at(keys + (r - first), z);
+            for (int x = 1; x < kMaxCluster; x++) z += x < C && r >= __shfl_sync(0xffffffffu, late_of, x);
+            first = __shfl_sync(0xffffffffu, late_of, z);
+          }
+          if ((m >> lane) & 1) from[u] = (int)*cl.at(keys + (r - first), z);
         }
       }
     }
