@@ -36,16 +36,22 @@ struct EvictArgs {
   int32_t* out_pos;
   float* out_mass;
   int64_t out_stride;
+  bool vec4;  // rows of mass and pos start on 16 bytes
 };
 
+template <bool ONE>
 struct SelShared {
   alignas(16) uint32_t hist[2][kBins];  // read several bins at a time
+  alignas(16) uint32_t sums[ONE ? 4 : kBins];  // the cluster's histogram
   uint32_t wcount[32];
-  uint32_t wcount2[32];
   uint32_t scan[32];
   uint32_t found_bin, found_above, found_count;
   uint32_t ties, late, holes;  // this block's counts, read by the cluster
 };
+
+// Words of a slice that a thread of a block of NT has at most.
+template <int NT>
+constexpr int kMaxWords = (kMaxSlice / 32 + NT - 1) / NT;
 
 __device__ __forceinline__ uint32_t rank_key(float m, bool guard) {
   if (guard) return score_key(INFINITY);
@@ -93,7 +99,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_select_kernel(const __gri
   extern __shared__ __align__(16) uint32_t keys[];
   uint32_t* bitmap = keys + slice_max;
   uint16_t* rank = reinterpret_cast<uint16_t*>(bitmap + slice_max / 32);
-  __shared__ SelShared sh;
+  __shared__ SelShared<ONE> sh;
   grid_let_next_start();
   const RowGroup<ONE> cl;
   const evict_problem& p = a.p;
@@ -121,16 +127,48 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_select_kernel(const __gri
   const int s0 = min(n, slice * c), s1 = min(n, s0 + slice);
   const int cnt = s1 - s0;
   const int words = (cnt + 31) >> 5;
-  // a warp's words [w0, w1) for the ordered passes
-  const int wper = (words + W - 1) / W;
-  const int w0 = min(words, warp * wper), w1 = min(words, w0 + wper);
 
   if (trim) {
     for (int i = tid; i < kBins; i += NT) sh.hist[0][i] = sh.hist[1][i] = 0;
     // positions from here on are protected
     const int recent = (int)max((int64_t)INT32_MIN, (p.cur ? p.cur[b] : n) - (int64_t)p.n_last);
     __syncthreads();
-    for (int i0 = tid; i0 < cnt; i0 += NT * U) {
+    auto take = [&](int i, float x, int at) {
+      const uint32_t k = rank_key(x, at < p.n_first || at >= recent);
+      keys[i] = k;
+      atomicAdd(&sh.hist[0][k >> 21], 1u);
+    };
+    int done = 0;
+    if (a.vec4) {  // four slots a load; the slice's start is a multiple of 32
+      const int quads = cnt >> 2;
+      const float4* m4 = reinterpret_cast<const float4*>(mass + s0);
+      const int4* p4 = reinterpret_cast<const int4*>(pos + s0);
+      for (int i0 = tid; i0 < quads; i0 += NT * 4) {
+        float4 x[4];
+        int4 at[4];
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+          const int i = i0 + u * NT;
+          if (i < quads) {
+            x[u] = m4[i];
+            const int s = s0 + 4 * i;
+            at[u] = pos ? p4[i] : make_int4(s, s + 1, s + 2, s + 3);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+          const int i = i0 + u * NT;
+          if (i < quads) {
+            take(4 * i, x[u].x, at[u].x);
+            take(4 * i + 1, x[u].y, at[u].y);
+            take(4 * i + 2, x[u].z, at[u].z);
+            take(4 * i + 3, x[u].w, at[u].w);
+          }
+        }
+      }
+      done = quads * 4;
+    }
+    for (int i0 = done + tid; i0 < cnt; i0 += NT * U) {
       float x[U];
       int at[U];
 #pragma unroll
@@ -140,14 +178,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_select_kernel(const __gri
         at[u] = i < cnt && pos ? pos[s0 + i] : s0 + i;
       }
 #pragma unroll
-      for (int u = 0; u < U; u++) {
-        const int i = i0 + u * NT;
-        if (i < cnt) {
-          const uint32_t k = rank_key(x[u], at[u] < p.n_first || at[u] >= recent);
-          keys[i] = k;
-          atomicAdd(&sh.hist[0][k >> 21], 1u);
-        }
-      }
+      for (int u = 0; u < U; u++)
+        if (i0 + u * NT < cnt) take(i0 + u * NT, x[u], at[u]);
     }
     // digits from the top: after each, `prefix` holds the found digits and
     // `need` how many keys of that prefix stay
@@ -159,27 +191,42 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_select_kernel(const __gri
         const int shift = pass == 1 ? 10 : 0;
         const uint32_t mask = pass == 1 ? 2047u : 1023u;
         const int top = pass == 1 ? 21 : 10;
-#pragma unroll 4
-        for (int i = tid; i < cnt; i += NT) {
-          const uint32_t k = keys[i];
+        auto look = [&](uint32_t k) {
           if ((k >> top) == (prefix >> top)) atomicAdd(&hist[(k >> shift) & mask], 1u);
+        };
+        const uint4* k4 = reinterpret_cast<const uint4*>(keys);
+        for (int i = tid; i < cnt >> 2; i += NT) {
+          const uint4 k = k4[i];
+          look(k.x);
+          look(k.y);
+          look(k.z);
+          look(k.w);
         }
+        if (tid < (cnt & 3)) look(keys[(cnt & ~3) + tid]);
       }
-      cl.sync();
-      // the cluster's histogram, a few bins a thread, largest bin first
+      if (ONE) {
+        __syncthreads();
+      } else {
+        // each block adds up its share of the bins and gives the sums to all
+        cl.sync();
+        const int share = kBins / C;
+        for (int i = c * share + tid; i < (c + 1) * share; i += NT) {
+          uint32_t sum = 0;
+          for (int r = 0; r < C; r++) sum += cl.at(hist, r)[i];
+          for (int r = 0; r < C; r++) cl.at(sh.sums, r)[i] = sum;
+        }
+        cl.sync();
+        hist = sh.sums;
+      }
+      // a few bins a thread, largest bin first
       constexpr int V = kBins / NT;  // 2 to 8
       uint32_t v[V], mine = 0;
       const int b0 = kBins - V * (tid + 1);
 #pragma unroll
-      for (int j = 0; j < V; j++) v[j] = 0;
-      for (int r = 0; r < C; r++) {
-        const uint2* h = reinterpret_cast<const uint2*>(cl.at(hist, r) + b0);
-#pragma unroll
-        for (int j = 0; j < V / 2; j++) {
-          const uint2 x = h[j];
-          v[2 * j] += x.x;
-          v[2 * j + 1] += x.y;
-        }
+      for (int j = 0; j < V / 2; j++) {
+        const uint2 x = reinterpret_cast<const uint2*>(hist + b0)[j];
+        v[2 * j] = x.x;
+        v[2 * j + 1] = x.y;
       }
 #pragma unroll
       for (int j = 0; j < V; j++) mine += v[j];
@@ -204,68 +251,110 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_select_kernel(const __gri
           above += v[j];
         }
       }
-      // every block has read hist[0] before the second pass's cluster barrier
+      // every block has read hist[0] before the second pass's barriers
       if (pass == 1)
         for (int i = tid; i < kBins; i += NT) sh.hist[0][i] = 0;
       __syncthreads();
       need -= sh.found_above;
       prefix |= sh.found_bin << (pass == 0 ? 21 : pass == 1 ? 10 : 0);
     }
-    // Ties of the last kept key: the lowest slots stay.  Where all of them do
-    // (the usual case) they need no order.
-    const bool all_ties = need == sh.found_count;
+    // A thread forms whole words of 32 slots: those above the last kept key stay,
+    // and of those equal to it the lowest.  (Lanes read their words' quads in
+    // turn, so that they meet different banks.)
     uint32_t tie = 0;
-    if (!all_ties) {
+    const bool all_ties = need == sh.found_count;
+    auto word_bits = [&](int w, uint32_t* above, uint32_t* equal) {
+      const uint4* k4 = reinterpret_cast<const uint4*>(keys) + w * 8;
+      uint32_t gt = 0, eq = 0;
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        const int q = (j + lane) & 7;
+        const uint4 k = k4[q];
+        gt |= (uint32_t)((k.x > prefix) | (k.y > prefix) << 1 | (k.z > prefix) << 2 | (k.w > prefix) << 3) << (4 * q);
+        eq |= (uint32_t)((k.x == prefix) | (k.y == prefix) << 1 | (k.z == prefix) << 2 | (k.w == prefix) << 3) << (4 * q);
+      }
+      const uint32_t valid = low_bits(cnt - w * 32);
+      *above = gt & valid;
+      *equal = eq & valid;
+    };
+    if (!ONE && !all_ties) {
+      // ties in the blocks before this one
       uint32_t t = 0;
-      for (int w = w0; w < w1; w++) {
-        const int i = w * 32 + lane;
-        t += i < cnt && keys[i] == prefix;
+      for (int w = tid; w < words; w += NT) {
+        uint32_t gt, eq;
+        word_bits(w, &gt, &eq);
+        t += __popc(eq);
       }
       t = __reduce_add_sync(0xffffffffu, t);
       if (lane == 0) sh.wcount[warp] = t;
       __syncthreads();
-      uint32_t total;
-      tie = warps_before(sh.wcount, W, warp, &total);
-      if (tid == 0) sh.ties = total;
+      uint32_t all;
+      warps_before(sh.wcount, W, warp, &all);
+      if (tid == 0) sh.ties = all;
       cl.sync();
       for (int r = 0; r < c; r++) tie += *cl.at(&sh.ties, r);
     }
-    uint32_t late = 0, holes = 0;
-    for (int w = w0; w < w1; w++) {
-      const int i = w * 32 + lane;
-      const uint32_t k = i < cnt ? keys[i] : 0;
-      bool stay = k >= prefix;
-      if (!all_ties) {
-        const unsigned eqs = __ballot_sync(0xffffffffu, k == prefix && i < cnt);
-        stay = k > prefix || (k == prefix && tie + __popc(eqs & ((1u << lane) - 1)) < need);
-        tie += __popc(eqs);
+    // sums over the threads before this one; the counts of a slice fit 16 bits
+    auto before = [&](uint32_t x, uint32_t* all) {
+      uint32_t incl = x;
+#pragma unroll
+      for (int s = 1; s < 32; s <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, incl, s);
+        if (lane >= s) incl += y;
       }
-      const unsigned word = __ballot_sync(0xffffffffu, stay && i < cnt);
-      const unsigned low = low_bits(nk - (s0 + w * 32)), valid = low_bits(cnt - w * 32);
-      if (lane == 0) {
-        bitmap[w] = word;
-        rank[w] = (uint16_t)holes;  // within the warp's words, for now
+      __syncthreads();
+      if (lane == 31) sh.wcount[warp] = incl;
+      __syncthreads();
+      return warps_before(sh.wcount, W, warp, all) + incl - x;
+    };
+    uint32_t holes_late = 0;  // of the words so far: holes, and late rows in the upper half
+    uint32_t mine[kMaxWords<NT>];
+    uint32_t at[kMaxWords<NT>];
+#pragma unroll
+    for (int x = 0; x < kMaxWords<NT>; x++) {
+      if (x * NT >= words) break;
+      const int w = x * NT + tid;
+      uint32_t gt = 0, eq = 0, all;
+      if (w < words) word_bits(w, &gt, &eq);
+      if (all_ties) {
+        gt |= eq;
+      } else {
+        const uint32_t ahead = tie + before(__popc(eq), &all);
+        uint32_t take = ahead >= need ? 0 : need - ahead, low = eq;
+        if (take >= (uint32_t)__popc(eq)) {
+          gt |= eq;
+        } else {
+          for (; take; take--) {
+            gt |= low & (0u - low);
+            low &= low - 1;
+          }
+        }
+        tie += all;
       }
-      holes += __popc(~word & valid & low);
-      late += __popc(word & ~low);
+      const uint32_t low = low_bits(nk - (s0 + w * 32)), valid = w < words ? low_bits(cnt - w * 32) : 0u;
+      const uint32_t both = __popc(~gt & valid & low) | __popc(gt & ~low) << 16;
+      const uint32_t first = holes_late + before(both, &all);
+      holes_late += all;
+      if (w < words) {
+        bitmap[w] = gt;
+        rank[w] = (uint16_t)first;
+      }
+      mine[x] = w < words ? gt & ~low : 0u;
+      at[x] = first >> 16;
     }
-    if (lane == 0) {
-      sh.wcount[warp] = late;
-      sh.wcount2[warp] = holes;
-    }
-    __syncthreads();  // the keys are read, the bitmap is whole: the late rows' slots take the keys' place
-    uint32_t all_late, all_holes;
-    uint32_t at = warps_before(sh.wcount, W, warp, &all_late);
-    const uint32_t holes_before = warps_before(sh.wcount2, W, warp, &all_holes);
     if (tid == 0) {
-      sh.late = all_late;
-      sh.holes = all_holes;
+      sh.late = holes_late >> 16;
+      sh.holes = holes_late & 0xffff;
     }
-    for (int w = w0 + lane; w < w1; w += 32) rank[w] += (uint16_t)holes_before;
-    for (int w = max(w0, (nk - s0) >> 5); w < w1; w++) {
-      const unsigned m = bitmap[w] & ~low_bits(nk - (s0 + w * 32));
-      if ((m >> lane) & 1) keys[at + __popc(m & ((1u << lane) - 1))] = (uint32_t)(s0 + w * 32 + lane);
-      at += __popc(m);
+    __syncthreads();  // the keys are read: the late rows' slots take their place
+#pragma unroll
+    for (int x = 0; x < kMaxWords<NT>; x++) {
+      if (x * NT >= words) break;
+      uint32_t m = mine[x], to = at[x];
+      while (m) {
+        keys[to++] = (uint32_t)(s0 + (x * NT + tid) * 32 + __ffs(m) - 1);
+        m &= m - 1;
+      }
     }
     cl.sync();
   }
@@ -290,10 +379,11 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_select_kernel(const __gri
     late_of -= l;
   }
   const int new_words = (nk + 31) >> 5, stride = C * W;
-  for (int v0 = c * W + warp; v0 < new_words; v0 += stride * 4) {
-    int from[4], slot[4];
+  constexpr int F = 8;
+  for (int v0 = c * W + warp; v0 < new_words; v0 += stride * F) {
+    int from[F], slot[F];
 #pragma unroll
-    for (int u = 0; u < 4; u++) {
+    for (int u = 0; u < F; u++) {
       const int v = v0 + u * stride;
       const int s = v * 32 + lane;
       slot[u] = v < new_words && s < nk ? s : -1;
@@ -315,15 +405,15 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_select_kernel(const __gri
         }
       }
     }
-    int ps[4];
-    float ms[4];
+    int ps[F];
+    float ms[F];
 #pragma unroll
-    for (int u = 0; u < 4; u++) {
+    for (int u = 0; u < F; u++) {
       ps[u] = slot[u] >= 0 && opos && pos ? pos[from[u]] : from[u];
       ms[u] = slot[u] >= 0 && omass ? mass[from[u]] : 0.f;
     }
 #pragma unroll
-    for (int u = 0; u < 4; u++)
+    for (int u = 0; u < F; u++)
       if (slot[u] >= 0) {
         src[slot[u]] = from[u];
         if (opos) opos[slot[u]] = ps[u];
@@ -356,7 +446,7 @@ struct MoveArgs {
   int64_t n_keep;
   int mass_heads, n_planes;
   evict_plane plane[IDX_MAX_PLANES];
-  int first[IDX_MAX_PLANES + 1];  // of the grid's y axis: plane i's heads start here
+  int first[IDX_MAX_PLANES + 1];  // planes' heads in one row: plane i's start here
 };
 
 template <class V>
@@ -388,9 +478,6 @@ template <int SLOTS>
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ MoveArgs a) {
   __shared__ int2 list[SLOTS];  // (new slot, slot it comes from)
   __shared__ int count;
-  int pl = 0;
-  while (pl + 1 < a.n_planes && (int)blockIdx.y >= a.first[pl + 1]) pl++;
-  const evict_plane& q = a.plane[pl];
   const int64_t chunks = (a.n_keep + SLOTS - 1) / SLOTS;
   const int64_t row = blockIdx.x / chunks;
   const int64_t s0 = (blockIdx.x % chunks) * SLOTS + threadIdx.x;
@@ -417,6 +504,9 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
   const int n = count;
   if (n == 0) return;
   const int64_t b = row / a.mass_heads;
+  int pl = 0;
+  while ((int)blockIdx.y >= a.first[pl + 1]) pl++;
+  const evict_plane& q = a.plane[pl];
   const int h = a.mass_heads == 1 ? (int)blockIdx.y - a.first[pl] : (int)(row % a.mass_heads);
   char* base = (char*)q.base + b * q.stride_b + h * q.stride_h;
   switch (q.reserved) {  // widest access that the plane's addresses allow
@@ -458,15 +548,19 @@ static cudaError_t launch_select(const EvictArgs& a, int64_t rows, int C, cudaSt
 cudaError_t launch_evict(const evict_problem& p, int32_t* src, int32_t* out_len, int32_t* out_pos, float* out_mass,
                          int64_t out_stride, cudaStream_t st) {
   const int64_t rows = (int64_t)p.B * p.mass_heads;
-  const EvictArgs a{p, src, out_len, out_pos, out_mass, out_stride};
+  const bool vec4 = p.stride % 4 == 0 && ((uintptr_t)p.mass | (uintptr_t)p.pos) % 16 == 0;
+  const EvictArgs a{p, src, out_len, out_pos, out_mass, out_stride, vec4};
   // blocks of a row: as many as its keys need, more while the rows leave SMs
   // idle and a block still has a few thousand keys
   int C = 1;
   while (C < kMaxCluster && (p.S > (int64_t)C * kMaxSlice || (rows * C < sm_count() && p.S > (int64_t)C * 4096))) C *= 2;
   cudaError_t e;
+  // a thread for each 16 keys or so: blocks of a whole SM's threads only where a
+  // slice has work for them
+  const int64_t slice = (p.S + C - 1) / C;
   if (C > 1)
-    e = launch_select<1024, false>(a, rows, C, st);
-  else if (p.S > 8192)
+    e = slice > 8192 ? launch_select<1024, false>(a, rows, C, st) : launch_select<512, false>(a, rows, C, st);
+  else if (slice > 8192)
     e = launch_select<1024, true>(a, rows, C, st);
   else
     e = launch_select<256, true>(a, rows, C, st);
@@ -487,14 +581,12 @@ cudaError_t launch_evict(const evict_problem& p, int32_t* src, int32_t* out_len,
     m.n_planes++;
   }
   if (m.n_planes == 0) return cudaSuccess;
-  // a block looks at 1024 new slots, or at 256 where that leaves SMs idle
-  const int64_t wide = rows * ((p.n_keep + 1023) / 1024);
-  if (wide * m.first[m.n_planes] >= 4 * sm_count())
-    return launch_after(evict_move_kernel<1024>, dim3((unsigned)wide, (unsigned)m.first[m.n_planes]), kMoveThreads, 0, st,
-                        true, m);
-  const int64_t narrow = rows * ((p.n_keep + 255) / 256);
-  return launch_after(evict_move_kernel<256>, dim3((unsigned)narrow, (unsigned)m.first[m.n_planes]), kMoveThreads, 0, st,
-                      true, m);
+  // a block looks at 1024 new slots, or at 256 where that leaves SMs short of blocks
+  const int64_t wide = rows * ((p.n_keep + 1023) / 1024), narrow = rows * ((p.n_keep + 255) / 256);
+  const unsigned ph = (unsigned)m.first[m.n_planes];
+  return wide * ph >= 16 * sm_count()
+             ? launch_after(evict_move_kernel<1024>, dim3((unsigned)wide, ph), kMoveThreads, 0, st, true, m)
+             : launch_after(evict_move_kernel<256>, dim3((unsigned)narrow, ph), kMoveThreads, 0, st, true, m);
 }
 
 }  // namespace idx
