@@ -9,6 +9,11 @@
 // 16-bit operands;  O += P V with P read from TMEM.  The two row tiles
 // alternate: while one's weights are formed, the other's products run.
 //
+// A tile's weights are handed over in two halves of 64 keys: the product over
+// the first runs while the second is formed, which takes the time that a row
+// tile waits for its weights (1,350 cycles for 128 keys) below the 1,024 cycles
+// of the other one's products.
+//
 // The reference m of a row moves only when a score passes it by more than 2^8
 // (weights up to 2^8 lose nothing in fp32 sums or in the 16-bit operands), so
 // the accumulator in TMEM is almost never rescaled.
@@ -188,7 +193,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t* sq = smem;
   uint8_t* skv = smem + 2 * C::TILE;
-  __shared__ uint64_t kv_full[C::NS], kv_empty[C::NS], q_full[2], s_full[2], p_ready[2], o_full[2], drain;
+  __shared__ uint64_t kv_full[C::NS], kv_empty[C::NS], q_full[2], s_full[2], p_half[2], p_ready[2], o_full[2], drain;
   __shared__ uint32_t s_tmem;
   // where a row's queries begin, in 16 bytes; then the number of its partial result
   __shared__ int s_row[2][128];
@@ -212,6 +217,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     for (int i = 0; i < 2; i++) {
       mbar_init(&q_full[i], 128);
       mbar_init(&s_full[i], 1);
+      mbar_init(&p_half[i], 128);
       mbar_init(&p_ready[i], 128);
       mbar_init(&o_full[i], 1);
     }
@@ -294,11 +300,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       }
       tc_commit(&s_full[i]);
     };
-    // O_t += P_i V
-    auto values = [&](int i, int t, uint32_t v, bool add) {
+    // O_t += P_i V over the first or the second half of the tile's keys
+    auto values = [&](int i, int t, uint32_t v, int s0, bool add) {
       const uint64_t v0 = dv + v * (C::TILE / 16);
 #pragma unroll
-      for (int s = 0; s < 8; s++)
+      for (int s = s0; s < s0 + 4; s++)
         tc_mma_f16_ts(tmem + 256 + 128 * t, tmem + 128 * i + 8 * s, v0 + s * (2048 / 16), id_o, add || s > 0);
     };
     Run r;
@@ -337,33 +343,48 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             tc_commit(&kv_empty[k]);
           }
           __syncwarp();
+          ok = wait(&p_half[0], np & 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) values(j & 1, 0, v, 0, j > 0);
+          __syncwarp();
           ok = wait(&p_ready[0], np++ & 1);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
-            values(j & 1, 0, v, j > 0);
+            values(j & 1, 0, v, 4, true);
             tc_commit(more ? &kv_empty[v] : &o_full[0]);
             if (!more) tc_commit(&kv_empty[v]);
           }
           __syncwarp();
           continue;
         }
+        ok = wait(&p_half[0], np & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) values(0, 0, v, 0, j > 0);
+        __syncwarp();
         ok = wait(&p_ready[0], np++ & 1);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          values(0, 0, v, j > 0);
+          values(0, 0, v, 4, true);
           if (more)
             scores(0, 0, k);
           else
             tc_commit(&o_full[0]);
         }
         __syncwarp();
+        ok = wait(&p_half[1], np1 & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) values(1, 1, v, 0, j > 0);
+        __syncwarp();
         ok = wait(&p_ready[1], np1++ & 1);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          values(1, 1, v, j > 0);
+          values(1, 1, v, 4, true);
           if (more)
             scores(1, 1, k);
           else
@@ -506,6 +527,20 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             }
           }
         }
+        if (i == 0 && vis < p.P && j * 128 + 128 > vis) {
+          // positions behind every row's limit are not data: their values
+          // must not reach the product, where 0 * NaN would
+          const uint32_t v = cnt + 1;
+          ok = mbar_wait(&kv_full[v % C::NS], (v / C::NS) & 1, abort_flag);
+          if (ok && row >= vis - j * 128) {
+            uint4* z = reinterpret_cast<uint4*>(skv + (v % C::NS) * C::TILE + row * 128);
+#pragma unroll
+            for (int x = 0; x < D / 64; x++)
+#pragma unroll
+              for (int e = 0; e < 8; e++) z[x * 1024 + e] = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
         const float base = m == -INFINITY ? 0.f : m;
         const uint64_t c2 = f2_pack(c, c), b2 = f2_pack(-base, -base), one = f2_pack(1.f, 1.f);
 #pragma unroll
@@ -522,20 +557,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             w[e] = pack2<BF16>(p0, p1);
           }
           tmem_st_32x32b_x32(ts + 16 * x, w);
-        }
-        if (i == 0 && vis < p.P && j * 128 + 128 > vis) {
-          // positions behind every row's limit are not data: their values
-          // must not reach the product, where 0 * NaN would
-          const uint32_t v = cnt + 1;
-          ok = mbar_wait(&kv_full[v % C::NS], (v / C::NS) & 1, abort_flag);
-          if (ok && row >= vis - j * 128) {
-            uint4* z = reinterpret_cast<uint4*>(skv + (v % C::NS) * C::TILE + row * 128);
-#pragma unroll
-            for (int x = 0; x < D / 64; x++)
-#pragma unroll
-              for (int e = 0; e < 8; e++) z[x * 1024 + e] = make_uint4(0, 0, 0, 0);
+          if (x == 0) {  // the product over the first half of the keys can start
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&p_half[i]);
           }
-          fence_proxy_async_smem();
         }
         tmem_st_wait();
         tc_fence_before();
