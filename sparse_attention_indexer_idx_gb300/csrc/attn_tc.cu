@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     const uint64_t dq = smem_desc_sw128(smem_u32(sq)), dk = smem_desc_sw128(smem_u32(skv)),
                    dv = desc_values(smem_u32(skv));
     uint32_t slot = 0, phase = 0;  // of the next ring slot
-    uint32_t np = 0, nq0 = 0, nq1 = 0, np1 = 0;
+    uint32_t np = 0, np1 = 0, nq0 = 0, nq1 = 0;  // uses of the barriers
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
@@ -327,34 +327,40 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         const uint32_t v = slot;
         ok = wait(&kv_full[slot], phase);
         advance();
-        const uint32_t k = slot;
-        const bool more = j + 1 < n;
-        if (more) {
-          ok = ok && wait(&kv_full[slot], phase);
-          advance();
-        }
         if (!ok) break;
+        const uint32_t k = slot, k_phase = phase;
+        const bool more = j + 1 < n;
+        if (more) advance();
         if (!two) {
           // One row tile: its scores alternate between the two places, so that
           // the next key tile's are formed while this one's weights are.
+          if (more) ok = wait(&kv_full[k], k_phase);
+          if (!ok) break;
           tc_fence_after();
           if (more && elect_one()) {
             scores((j + 1) & 1, 0, k);
             tc_commit(&kv_empty[k]);
           }
           __syncwarp();
-          ok = wait(&p_half[0], np & 1);
+          // (a barrier for each place: with one for both, the weights of two
+          // key tiles could arrive while this warp is between two looks at it)
+          const int pl = j & 1;
+          const uint32_t parity = (pl ? np1++ : np++) & 1;
+          ok = wait(&p_half[pl], parity);
           if (!ok) break;
           tc_fence_after();
-          if (elect_one()) values(j & 1, 0, v, 0, j > 0);
+          if (elect_one()) values(pl, 0, v, 0, j > 0);
           __syncwarp();
-          ok = wait(&p_ready[0], np++ & 1);
+          ok = wait(&p_ready[pl], parity);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
-            values(j & 1, 0, v, 4, true);
-            tc_commit(more ? &kv_empty[v] : &o_full[0]);
-            if (!more) tc_commit(&kv_empty[v]);
+            values(pl, 0, v, 4, true);
+            if (!more) {
+              tc_commit(&o_full[0]);
+              tc_commit(&o_full[1]);  // the other row tile's warps wait for the run's end
+            }
+            tc_commit(&kv_empty[v]);
           }
           __syncwarp();
           continue;
@@ -365,6 +371,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         if (elect_one()) values(0, 0, v, 0, j > 0);
         __syncwarp();
         ok = wait(&p_ready[0], np++ & 1);
+        if (ok && more) ok = wait(&kv_full[k], k_phase);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
@@ -416,9 +423,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       const int n = r.j1 - r.j0;
       const int rr = r.rt * 256 + i * 128 + row;
       const bool two = rows - r.rt * 256 > 128;
-      if (i == 1 && !two) {  // an empty row tile; the other one uses both places
-        cnt += 2 * n;
+      if (i == 1 && !two) {
+        // An empty row tile: the other one uses both places.  Its barriers are
+        // this one's again when the run is over.
         ns1 += n / 2;
+        ok = __all_sync(0xffffffffu, mbar_wait(&o_full[1], no++ & 1, abort_flag));
         continue;
       }
       if (i == 0 && two) ns1 += n;  // the other tile's
@@ -560,12 +569,12 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
           if (x == 0) {  // the product over the first half of the keys can start
             tmem_st_wait();
             tc_fence_before();
-            mbar_arrive(&p_half[i]);
+            mbar_arrive(&p_half[place]);
           }
         }
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(&p_ready[i]);
+        mbar_arrive(&p_ready[place]);
         cnt += 2;
       }
       ok = ok && mbar_wait(&o_full[i], no++ & 1, abort_flag);

@@ -259,3 +259,77 @@ def test_slots_beyond_32_bits(B):
          "dtype": "bf16"}
     check(t, out[-1:], lse[-1:], None)
     assert torch.isneginf(lse[:-1]).all() and (out[:-1] == 0).all()
+
+
+def _prefix_only(B, seed, rows, Hq, n_kv, P, D, dtype="bf16", prefix_len=None, layout="bshd"):
+    t = make(seed, B=rows, T=1, Hq=Hq, n_kv=n_kv, D=D, P=P, dtype=dtype, prefix_len=prefix_len, layout=layout,
+             garbage=prefix_len is not None)
+    out, lse, mass, p, ws = run(B, t)
+    torch.cuda.synchronize()
+    assert B.device_error() == 0
+    return t, out, lse, p, ws
+
+
+@pytest.mark.parametrize("rows,Hq,n_kv,P,D,dtype,plen", [
+    (17, 8, 8, 5000, 128, "bf16", None),       # a part of one row tile
+    (64, 4, 2, 40000, 64, "f16", None),        # one row tile, many key tiles
+    (16, 64, 8, 9001, 128, "bf16", None),      # one whole row tile, a ragged last key tile
+    (40, 32, 8, 4999, 128, "f16", None),       # two row tiles
+    (150, 8, 4, 6500, 64, "bf16", None),       # two pairs of row tiles, the last one partly empty
+    (33, 32, 4, 5000, 128, "bf16", [13 * i for i in range(33)]),           # nothing visible behind 416
+    (40, 16, 2, 12000, 64, "bf16", [0] * 39 + [7777]),                     # one request sees anything
+    (21, 16, 2, 12000, 128, "f16", [11000 - 517 * i for i in range(21)]),  # one row tile, ragged limits
+])
+def test_prefix_on_the_tensor_cores(B, rows, Hq, n_kv, P, D, dtype, plen):
+    t, out, lse, p, ws = _prefix_only(B, rows, rows, Hq, n_kv, P, D, dtype, plen)
+    # the 64-bit oracle on a few requests (rows are independent)
+    pick = [0, rows // 2, rows - 1]
+    few = dict(t, q=t["q"][pick])
+    if plen is not None:
+        few["prefix_len"] = t["prefix_len"][pick]
+    check(few, out[pick], lse[pick], None)
+    assert torch.isfinite(out.float()).all()
+
+
+def test_strides_that_no_tensor_map_holds(B):
+    # the heads share their memory: a head stride of zero is read by the streaming kernel
+    g = torch.Generator().manual_seed(3)
+    one = torch.randn(3000, 1, 128, generator=g).to(torch.bfloat16)
+    t = {"q": torch.randn(40, 1, 16, 128, generator=g).to(torch.bfloat16), "scale": 0.1, "dtype": "bf16",
+         "pk": one.expand(3000, 8, 128), "pv": one.expand(3000, 8, 128)}
+    p = B.AttnProblem(t["q"].cuda(), 0.1, pk=one.cuda().expand(3000, 8, 128), pv=one.cuda().expand(3000, 8, 128))
+    out, lse = torch.empty_like(p.q), torch.empty((40, 1, 16), device="cuda")
+    ws = torch.empty(B.attn_shared_workspace_size(p, False), dtype=torch.uint8, device="cuda")
+    B.attn_shared(p, out, lse, None, ws)
+    few = dict(t, q=t["q"][::13])
+    check(few, out[::13], lse[::13], None)
+
+
+@pytest.mark.parametrize("rows,P", [(32, 8192), (24, 5000), (64, 6000)])
+def test_many_repeats_agree(B, rows, P):
+    """The pipeline of the tensor-core kernel, run often beside other work: no
+    wait gives up and every run leaves the same bits."""
+    t, out, lse, p, ws = _prefix_only(B, 50, rows, 32, 8, P, 128)
+    other = torch.empty_like(out)
+    noise = torch.zeros(1 << 26, device="cuda")
+    for i in range(300):
+        if i % 7 == 0:
+            noise.add_(1.0)
+        B.attn_shared(p, other, lse, None, ws)
+        if i % 50 == 49:
+            assert torch.equal(out, other)
+    assert B.device_error() == 0
+
+
+def test_wait_limit_is_reported(B):
+    t, out, lse, p, ws = _prefix_only(B, 51, 64, 32, 8, 8192, 128)
+    try:
+        B.set_wait_limit_ns(0)
+        B.attn_shared(p, torch.empty_like(out), None, None, ws)
+        err = B.device_error()
+    finally:
+        B.set_wait_limit_ns(B.DEFAULT_WAIT_LIMIT_NS)
+    assert err & B.DEVERR_WAIT_TIMEOUT
+    again = torch.empty_like(out)
+    B.attn_shared(p, again, lse, None, ws)
+    assert B.device_error() == 0 and torch.equal(again, out)
