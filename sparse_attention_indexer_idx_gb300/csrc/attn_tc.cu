@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t* sq = smem;
   uint8_t* skv = smem + 2 * C::TILE;
-  __shared__ uint64_t kv_full[C::NS], kv_empty[C::NS], q_full[2], s_full[2], p_half[2], p_ready[2], o_full[2], drain;
+  __shared__ uint64_t kv_full[C::NS], kv_empty[C::NS], q_full[2], s_full[2], p_half[2], p_ready[2], o_full[2], pv_done, drain;
   __shared__ uint32_t s_tmem;
   // where a row's queries begin, in 16 bytes; then the number of its partial result
   __shared__ int s_row[2][128];
@@ -221,6 +221,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       mbar_init(&p_ready[i], 128);
       mbar_init(&o_full[i], 1);
     }
+    mbar_init(&pv_done, 1);
     mbar_init(&drain, 1);
     s_abort = 0;
     s_vis = p.prefix_len ? 0 : (int)p.P;
@@ -356,6 +357,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
           tc_fence_after();
           if (elect_one()) {
             values(pl, 0, v, 4, true);
+            tc_commit(&pv_done);
             if (!more) {
               tc_commit(&o_full[0]);
               tc_commit(&o_full[1]);  // the other row tile's warps wait for the run's end
@@ -416,7 +418,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     // zero becomes one that takes every score to zero but leaves -inf alone
     const float c = fmaxf(fabsf(a.scale_log2), 1e-37f);
     const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
-    uint32_t ns0 = 0, ns1 = 0, no = 0, cnt = 0;  // ns: uses of the scores' two places
+    // ns: uses of the scores' two places; npv: products with V of runs with one row tile
+    uint32_t ns0 = 0, ns1 = 0, no = 0, npv = 0, cnt = 0;
     bool ok = true;
     Run r;
     while (ok && line.next(&r)) {
@@ -524,6 +527,12 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
 #pragma unroll
           for (int q = 0; q < 4; q++) l2[q] = f2_fma(l2[q], f2, zero);
           if (j > r.j0) {
+            // The accumulator has to be at rest.  With two row tiles these scores
+            // were formed after the last product with V; with one they were not,
+            // and that product has to be waited for.
+            if (!two) mbar_wait(&pv_done, (npv + (j - r.j0) - 1) & 1, abort_flag);
+            __syncwarp();
+            tc_fence_after();
 #pragma unroll
             for (int x = 0; x < D / 32; x++) {
               uint32_t o[32];
@@ -581,6 +590,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
+      if (!two) npv += n;
       float l = 0.f;
 #pragma unroll
       for (int q = 0; q < 4; q++) {

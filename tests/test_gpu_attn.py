@@ -333,3 +333,21 @@ def test_wait_limit_is_reported(B):
     again = torch.empty_like(out)
     B.attn_shared(p, again, lse, None, ws)
     assert B.device_error() == 0 and torch.equal(again, out)
+
+
+@pytest.mark.parametrize("rows,Hq,n_kv,P,D,dtype", [(32, 32, 8, 8192, 128, "bf16"), (20, 8, 4, 12000, 64, "f16"),
+                                                   (24, 16, 16, 5000, 128, "bf16"), (160, 16, 8, 3000, 128, "bf16")])
+def test_steep_scores_on_the_tensor_cores(B, rows, Hq, n_kv, P, D, dtype):
+    # The running maximum passes its reference over and over, at other tiles for
+    # each row: the accumulator is rescaled while products are under way.
+    t = make(60, B=rows, T=1, Hq=Hq, n_kv=n_kv, D=D, P=P, dtype=dtype)
+    g = torch.Generator().manual_seed(61)
+    ramp = torch.linspace(0, 6, P).view(P, 1, 1) * (1 + torch.rand(1, n_kv, 1, generator=g))
+    t["pk"] = (ramp + 0.5 * t["pk"].float()).to(DT[dtype])
+    t["q"] = (torch.rand(rows, 1, Hq, 1, generator=g) * 2 - 0.5 + 0.3 * t["q"].float()).to(DT[dtype])
+    for _ in range(5):
+        out, lse, mass, p, ws = run(B, t)
+        pick = [0, 3, rows // 2, rows - 1]
+        few = dict(t, q=t["q"][pick])
+        check(few, out[pick], lse[pick], None)
+    assert B.device_error() == 0
