@@ -70,7 +70,15 @@ StreamLine plan_stream(AttnArgs& a) {
   const int64_t rows = std::max<int64_t>(p.S == 0 ? 1 : p.ids ? a.G : (int64_t)p.T * a.G, way == kLine ? rows_pre : 1);
   l.row_tile = rows <= 16 ? 16 : 32;
   l.members = (int)(p.n_kv * ceil_div(rows, l.row_tile));
-  const int64_t unit = stream_unit(p.D), warps = (l.row_tile == 16 ? 12 : 8) * (int64_t)sm_count();
+  const int64_t warps = (l.row_tile == 16 ? 12 : 8) * (int64_t)sm_count();
+  l.seqs = private_keys(p) == 0 ? 0 : p.ids ? p.B * p.T : p.B;
+  // A unit is a tile where every share has sixteen of them or more (an even cut
+  // matters), else four: a sequence's start takes about the time of four tiles.
+  const int64_t tile = stream_tile(p.D);
+  const int64_t tiles = (way == kLine ? ceil_div(p.P, tile) : 0) + l.seqs * ceil_div(private_keys(p), tile);
+  const bool fine = tiles * l.members >= 16 * warps;
+  l.unit_shift = (p.D == 128 ? 4 : 5) + (fine ? 0 : 2);
+  const int64_t unit = (int64_t)1 << l.unit_shift;
   if (way == kLine) l.prefix_units = (int)ceil_div(p.P, unit);
   if (way == kOwnLine) {
     l.own_units = (int)ceil_div(p.P, unit);
@@ -80,13 +88,12 @@ StreamLine plan_stream(AttnArgs& a) {
     a.parts_prefix = l.own_groups;
   }
   const int64_t longest = ceil_div(private_keys(p), unit);
-  l.seqs = longest == 0 ? 0 : p.ids ? p.B * p.T : p.B;
   const int64_t total = l.prefix_units + l.seqs * longest;
   l.groups = total == 0 ? 0 : (int)std::max<int64_t>(1, warps / l.members);
   l.least = (int)std::max<int64_t>(1, ceil_div(total, 4 * std::max<int64_t>(1, l.groups)));
   // Lists have one length; short lines are cut as if all caches were full, which
   // saves their blocks the look at the lengths.
-  if (p.ids || total <= 2 * l.groups) l.uniform = (int)longest;
+  if (p.ids || (!fine && total <= 2 * l.groups)) l.uniform = (int)longest;
   if (l.uniform || l.seqs == 0) l.groups = (int)std::min<int64_t>(l.groups, std::max<int64_t>(1, total / l.least));
   auto parts = [&](int64_t units) { return units == 0 ? 0 : (int)std::min(units, ceil_div(units - 1, l.least) + 1); };
   if (way == kLine) a.parts_prefix = parts(l.prefix_units);
@@ -138,7 +145,7 @@ size_t attn_shared_ws(const attn_problem& p, bool mass) { return layout(make_arg
 
 bool attn_shared_fits(const attn_problem& p) {
   // the lines of key units and tiles are counted in 32 bits
-  const int64_t unit = stream_unit(p.D), G = p.Hq / p.n_kv;
+  const int64_t unit = stream_tile(p.D), G = p.Hq / p.n_kv;
   const int64_t seqs = (int64_t)p.B * (p.ids ? p.T : 1);
   const int64_t line = ceil_div(p.P, unit) + seqs * std::max<int64_t>(1, ceil_div(private_keys(p), unit));
   const int64_t tiles = ceil_div((int64_t)p.B * p.T * G, 256) * p.n_kv * ceil_div(p.P, 128);

@@ -31,8 +31,8 @@ struct AttnArgs {
   int mass_heads;
 };
 
-// Keys of a unit of the streaming kernel's work.
-__host__ __device__ constexpr int stream_unit(int D) { return D == 128 ? 64 : 128; }
+// Keys of a tile of the streaming kernel.
+__host__ __device__ constexpr int stream_tile(int D) { return D == 128 ? 16 : 32; }
 
 // Private slots that token t of request b sees under KV head h.
 __device__ __forceinline__ int attn_len(const attn_problem& p, int b, int h) {
@@ -56,14 +56,13 @@ __device__ __forceinline__ int64_t attn_prefix_len(const attn_problem& p, int b)
 
 // Units of request b's cache on the streaming kernel's line: by its longest
 // head, at least one, so that every sequence has a place.
-template <int UNIT>
-__device__ __forceinline__ int cache_units(const attn_problem& p, int b) {
+__device__ __forceinline__ int cache_units(const attn_problem& p, int b, int unit_shift) {
   int n = 0;
   for (int h = 0; h < (p.len_per_head ? p.n_kv : 1); h++) {
     const int x = p.len[p.len_per_head ? (int64_t)b * p.n_kv + h : b];
     if (x <= p.S) n = max(n, x);
   }
-  return max(1, (n + UNIT - 1) / UNIT);
+  return max(1, (n + (1 << unit_shift) - 1) >> unit_shift);
 }
 
 __device__ __forceinline__ float attn_ex2(float x) {
@@ -74,6 +73,7 @@ __device__ __forceinline__ float attn_ex2(float x) {
 
 // The streaming kernel's line of key units and its cut (see attn_stream.cu).
 struct StreamLine {
+  int unit_shift;    // a unit is 2^unit_shift keys: a tile, or four
   int row_tile;      // 16 or 32 rows of a warp
   int members;       // warps of a group: KV heads times row tiles
   int groups;

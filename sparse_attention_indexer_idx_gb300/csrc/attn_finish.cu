@@ -94,31 +94,52 @@ __device__ void join_rows(const AttnArgs& a) {
   if (lane == 0 && a.lse) a.lse[r] = l > 0.f ? (top + log2f(l)) * 0.693147180559945309f : -INFINITY;
 }
 
-// What a mass block needs of a row: its log2 normaliser and how many private
-// slots it sees.
+// What a mass block needs of a row: its log2 normaliser, how many private slots
+// it sees, and its number.
 struct MassRows {
   float lse2[kRowsAt];
   int lim[kRowsAt];
-  int64_t row[kRowsAt];   // (b*T + t)*Hq + hq
+  int row[kRowsAt];       // (b*T + t)*Hq + hq
   int longest, shortest;  // of lim
 };
 
-// Rows (b, t, hq): i-th of the block's, t = t0 + i / heads, hq = hq0 + i %
-// heads.  A warp takes four rows at a time, eight lanes to a row's pieces.
-__device__ __forceinline__ void load_rows(const AttnArgs& a, MassRows& s, int b, int t0, int hq0, int heads, int i0,
-                                          int n) {
+// Rows (b, t, hq): the i-th is t = t0 + i / heads, hq = hq0 + i % heads, for i0
+// <= i < i0 + n.  Reads only the call's inputs: it runs before grid_wait().
+__device__ __forceinline__ void set_rows(const AttnArgs& a, MassRows& s, int b, int t0, int hq0, int heads, int i0,
+                                         int n) {
   const attn_problem& p = a.p;
-  const int parts = a.parts_prefix + a.parts_private;
-  const int lane = threadIdx.x & 31, sub = lane & 7;
   if (threadIdx.x == 0) {
     s.longest = 0;
     s.shortest = INT32_MAX;
   }
   __syncthreads();
+  int longest = 0, shortest = INT32_MAX;
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const int dt = (i0 + i) / heads, t = t0 + dt, hq = hq0 + (i0 + i) - dt * heads;
+    const int len = p.len[p.len_per_head ? (int64_t)b * p.n_kv + hq / a.G : b];
+    const int lim = len < 0 || len > p.S ? 0 : max(0, len - p.T + t + 1);
+    s.lim[i] = lim;
+    s.row[i] = (b * p.T + t) * p.Hq + hq;
+    longest = max(longest, lim);
+    shortest = min(shortest, lim);
+  }
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  shortest = __reduce_min_sync(0xffffffffu, shortest);
+  if ((threadIdx.x & 31) == 0) {
+    atomicMax(&s.longest, longest);
+    atomicMin(&s.shortest, shortest);
+  }
+  __syncthreads();
+}
+
+// The normalisers of the n rows.  A warp takes four rows at a time, eight lanes
+// to a row's pieces.
+__device__ __forceinline__ void load_norms(const AttnArgs& a, MassRows& s, int n) {
+  const int parts = a.parts_prefix + a.parts_private;
+  const int lane = threadIdx.x & 31, sub = lane & 7;
   for (int i = (threadIdx.x >> 5) * 4 + (lane >> 3); i < ((n + 3) & ~3); i += kWarps * 4) {
     const bool live = i < n;
-    const int t = t0 + (i0 + (live ? i : 0)) / heads, hq = hq0 + (i0 + (live ? i : 0)) % heads;
-    const float2* ml = a.pml + (((int64_t)b * p.T + t) * p.Hq + hq) * parts;
+    const float2* ml = a.pml + (int64_t)s.row[live ? i : 0] * parts;
     float top = -INFINITY, l = 0.f;
     for (int j0 = 0; j0 < parts; j0 += 32) {  // four pieces of a lane at a time
       float2 x[4];
@@ -144,15 +165,7 @@ __device__ __forceinline__ void load_rows(const AttnArgs& a, MassRows& s, int b,
     l = m == -INFINITY ? 0.f : l * attn_ex2(top - m);
 #pragma unroll
     for (int d = 1; d < 8; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-    if (live && sub == 0) {
-      const int len = p.len[p.len_per_head ? (int64_t)b * p.n_kv + hq / a.G : b];
-      const int lim = len < 0 || len > p.S ? 0 : max(0, len - p.T + t + 1);
-      s.lse2[i] = m + log2f(l);
-      s.lim[i] = lim;
-      s.row[i] = ((int64_t)b * p.T + t) * p.Hq + hq;
-      atomicMax(&s.longest, lim);
-      atomicMin(&s.shortest, lim);
-    }
+    if (live && sub == 0) s.lse2[i] = m + log2f(l);
   }
   __syncthreads();
 }
@@ -161,6 +174,8 @@ __device__ __forceinline__ void load_rows(const AttnArgs& a, MassRows& s, int b,
 // runs; each sums its own in row order, then the runs are added in order.  A
 // block takes every per-th run of slots: the rows' normalisers, which take more
 // instructions than the sums of a few hundred slots, are formed once for them.
+// The old masses are fetched before the kernels that come first are done, the
+// first scores beside the pieces of the normalisers.
 __device__ __forceinline__ void mass_dense(const AttnArgs& a, int64_t block, int per, int groups) {
   __shared__ MassRows s;
   __shared__ float4 s_add[kThreads];
@@ -171,27 +186,40 @@ __device__ __forceinline__ void mass_dense(const AttnArgs& a, int64_t block, int
   const int b = (int)(bm / a.mass_heads), m = (int)(bm % a.mass_heads);
   const int heads = p.Hq / a.mass_heads;  // query heads of the mass head
   const int rows = heads * p.T;
-  // slots that a row of the block can see (all, where the heads differ)
-  int most = (int)p.S;
-  if (!p.len_per_head || a.mass_heads > 1) most = min(most, p.len[p.len_per_head ? bm : b]);
   const int first = (int)(block % per) * lanes * kSlots;
-  if (first >= most) return;
   for (int r0 = 0; r0 < rows; r0 += kRowsAt) {
     const int n = min(kRowsAt, rows - r0);
     const int len = (n + groups - 1) / groups;
     const int i0 = min(n, run * len), i1 = min(n, i0 + len);  // this thread's rows of those held
     __syncthreads();
-    load_rows(a, s, b, 0, m * heads, heads, r0, n);
-    for (int at = first; at < most; at += per * lanes * kSlots) {
+    set_rows(a, s, b, 0, m * heads, heads, r0, n);
+    if (first >= s.longest) continue;
+    float old[kSlots];
+    auto fetch_old = [&](int slot) {
+      const float* from = a.mass + bm * p.S + slot;
+#pragma unroll
+      for (int e = 0; e < kSlots; e++) old[e] = run == 0 && slot + e < s.longest ? from[e] : 0.f;
+    };
+    float4 y[kBatch];
+    auto fetch = [&](int slot, int i) {  // rows i .. of a thread whose slots all of them see
+#pragma unroll
+      for (int u = 0; u < kBatch; u++)
+        y[u] = *reinterpret_cast<const float4*>(a.sc + (int64_t)s.row[i + u] * a.sc_ld + slot);
+    };
+    const int slot0 = first + mine * kSlots;
+    const bool ahead = slot0 + kSlots <= s.shortest && i0 + kBatch <= i1;
+    fetch_old(slot0);
+    grid_wait();
+    if (ahead) fetch(slot0, i0);
+    load_norms(a, s, n);
+    for (int at = first; at < s.longest; at += per * lanes * kSlots) {
       const int slot = at + mine * kSlots;
-      const float* sc = a.sc + slot;
+      if (at != first) fetch_old(slot);
       float add[kSlots] = {};
       int i = i0;
-      if (slot + kSlots <= s.shortest) {  // every row sees all of the thread's slots
+      if (slot + kSlots <= s.shortest) {
         for (; i + kBatch <= i1; i += kBatch) {
-          float4 y[kBatch];
-#pragma unroll
-          for (int u = 0; u < kBatch; u++) y[u] = *reinterpret_cast<const float4*>(sc + s.row[i + u] * a.sc_ld);
+          if (at != first || i != i0) fetch(slot, i);
 #pragma unroll
           for (int u = 0; u < kBatch; u++) {
             const float z = s.lse2[i + u];
@@ -206,13 +234,13 @@ __device__ __forceinline__ void mass_dense(const AttnArgs& a, int64_t block, int
 #pragma unroll 4
         for (; i < i1; i++) {
           const int left = s.lim[i] - slot;
-          float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (left > 0) y = *reinterpret_cast<const float4*>(sc + s.row[i] * a.sc_ld);
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (left > 0) x = *reinterpret_cast<const float4*>(a.sc + (int64_t)s.row[i] * a.sc_ld + slot);
           const float z = s.lse2[i];
-          if (left > 0) add[0] += attn_ex2(y.x - z);
-          if (left > 1) add[1] += attn_ex2(y.y - z);
-          if (left > 2) add[2] += attn_ex2(y.z - z);
-          if (left > 3) add[3] += attn_ex2(y.w - z);
+          if (left > 0) add[0] += attn_ex2(x.x - z);
+          if (left > 1) add[1] += attn_ex2(x.y - z);
+          if (left > 2) add[2] += attn_ex2(x.z - z);
+          if (left > 3) add[3] += attn_ex2(x.w - z);
         }
       if (groups > 1) {
         __syncthreads();
@@ -230,19 +258,20 @@ __device__ __forceinline__ void mass_dense(const AttnArgs& a, int64_t block, int
       float* to = a.mass + bm * p.S + slot;
 #pragma unroll
       for (int e = 0; e < kSlots; e++)
-        if (slot + e < most) to[e] += add[e];
+        if (slot + e < s.longest) to[e] = old[e] + add[e];
     }
   }
+  grid_wait();
 }
 
 // Mass of listed slots.  One list holds a slot at most once, so its threads add
 // to different slots; lists that can share a slot (another token's, or another
 // KV head's when all heads share the mass) follow one another in one block.
-// A thread takes E entries and 32 / E rows at a time.
+// A thread takes E entries, and several rows of each, at a time.
 template <int E>
 __device__ __forceinline__ void mass_listed(const AttnArgs& a, int64_t block, int64_t per) {
   __shared__ MassRows s;
-  constexpr int kBatch = 32 / E;
+  constexpr int kBatch = E == 1 ? 16 : 8;
   const attn_problem& p = a.p;
   const int lists_h = p.ids_per_head && a.mass_heads == 1 ? p.n_kv : 1;
   const int lists = p.T * lists_h;
@@ -254,6 +283,7 @@ __device__ __forceinline__ void mass_listed(const AttnArgs& a, int64_t block, in
   // rows (t, query head) of the mass head: list q has rows q * heads ..
   const bool once = lists * heads <= kRowsAt;
   const int64_t first = block % per * kThreads + threadIdx.x, step = per * kThreads;
+  if (once) set_rows(a, s, b, 0, m * all, all, 0, lists * heads);
   for (int q = 0; q < lists; q++) {
     const int t = q / lists_h, hq0 = m * all + (q % lists_h) * heads;
     const int32_t* list = p.ids + (p.ids_per_head ? (((int64_t)b * p.T + t) * p.n_kv + hq0 / a.G) * p.W
@@ -267,6 +297,7 @@ __device__ __forceinline__ void mass_listed(const AttnArgs& a, int64_t block, in
         float add[E] = {};
 #pragma unroll
         for (int e = 0; e < E; e++) id[e] = w0 + e * step < p.W ? list[w0 + e * step] : -1;
+        grid_wait();
         for (int i0 = 0; i0 < n; i0 += kBatch) {
           float y[kBatch][E];
 #pragma unroll
@@ -275,12 +306,9 @@ __device__ __forceinline__ void mass_listed(const AttnArgs& a, int64_t block, in
             for (int e = 0; e < E; e++)
               y[u][e] = i0 + u < n && w0 + e * step < p.W ? sc[(r0 + i0 + u) * a.sc_ld + w0 + e * step] : 0.f;
           if (w0 == first && i0 == 0) {
-            // the previous list's additions are done; this one's rows
-            __syncthreads();
-            if (!once)
-              load_rows(a, s, b, t, hq0, heads, r0, n);
-            else if (q == 0)
-              load_rows(a, s, b, 0, m * all, all, 0, lists * heads);
+            __syncthreads();  // the previous list's additions are done
+            if (!once) set_rows(a, s, b, t, hq0, heads, r0, n);
+            if (!once || q == 0) load_norms(a, s, once ? lists * heads : n);
           }
 #pragma unroll
           for (int u = 0; u < kBatch; u++)
@@ -300,18 +328,18 @@ __device__ __forceinline__ void mass_listed(const AttnArgs& a, int64_t block, in
   }
 }
 
-template <int D, bool BF16, bool LISTED>
-__global__ void __launch_bounds__(kThreads, LISTED ? 2 : 4)
+// MASS: 0 every slot, else the entries that a thread of the listed form takes.
+template <int D, bool BF16, int MASS>
+__global__ void __launch_bounds__(kThreads, MASS == 4 ? 3 : 4)
     attn_finish_kernel(const __grid_constant__ AttnArgs a, int64_t join_blocks, int64_t per, int row_groups) {
-  grid_wait();
-  if (blockIdx.x < join_blocks)
+  if (blockIdx.x < join_blocks) {
+    grid_wait();
     join_rows<D, BF16>(a);
-  else if (LISTED && row_groups == 1)
-    mass_listed<4>(a, blockIdx.x - join_blocks, per);
-  else if (LISTED)
-    mass_listed<1>(a, blockIdx.x - join_blocks, per);
-  else
+  } else if constexpr (MASS == 0) {
     mass_dense(a, blockIdx.x - join_blocks, (int)per, row_groups);
+  } else {
+    mass_listed<MASS>(a, blockIdx.x - join_blocks, per);
+  }
 }
 
 template <int D, bool BF16>
@@ -321,7 +349,8 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
   const int64_t join = (rows + kWarps - 1) / kWarps;
   // a slot's rows are spread over up to four threads where there are many
   const int mass_rows = p.Hq / a.mass_heads * p.T;
-  int groups = mass_rows >= 32 ? 4 : mass_rows >= 16 ? 2 : 1;
+  const int groups = mass_rows >= 32 ? 4 : mass_rows >= 16 ? 2 : 1;
+  auto kern = attn_finish_kernel<D, BF16, 0>;
   int64_t per = 0;  // mass blocks of one (b, mass head)
   if (a.mass && a.parts_private) {
     const int64_t bms = (int64_t)p.B * a.mass_heads;
@@ -332,12 +361,11 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
       // up to eight rows at a time; other lists are spread over blocks by entry
       const bool one = p.T == 1 && !(p.ids_per_head && a.mass_heads == 1 && p.n_kv > 1);
       per = one ? (p.W + kThreads - 1) / kThreads : 1;
-      groups = one && p.Hq / a.mass_heads > 8 ? 4 : 1;
+      kern = one && p.Hq / a.mass_heads > 8 ? attn_finish_kernel<D, BF16, 1> : attn_finish_kernel<D, BF16, 4>;
     }
   }
   const int64_t blocks = join + (int64_t)p.B * a.mass_heads * per;
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
-  auto kern = p.ids && per ? attn_finish_kernel<D, BF16, true> : attn_finish_kernel<D, BF16, false>;
   return launch_after(kern, dim3((unsigned)blocks), kThreads, 0, st, a.parts_prefix + a.parts_private > 0, a, join, per,
                       groups);
 }

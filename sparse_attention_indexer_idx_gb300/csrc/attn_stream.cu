@@ -2,7 +2,7 @@
 // the private caches of a decode step, and a shared prefix under a small batch.
 //
 // Mapping.  The key sequences (the prefix, then every request's cache or list)
-// form one line of key units; it is cut evenly over groups of warps, with one
+// form one line of units of one or four key tiles; it is cut evenly over groups of warps, with one
 // warp of a group for each KV head (and tile of up to 32 rows).  The heads of a
 // group run side by side, so their rows of a cache, which lie next to one
 // another, are read together, and all groups end together however ragged the
@@ -72,14 +72,12 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 
 template <int D, int MT>
 struct StreamCfg {
-  static constexpr int KT = D == 128 ? 16 : 32;  // keys of a tile: 4 KB of keys, 4 KB of values
-  static constexpr int UNIT = stream_unit(D);    // a warp's work is cut in units of four tiles
+  static constexpr int KT = stream_tile(D);      // keys of a tile: 4 KB of keys, 4 KB of values
   static constexpr int CH = D / 8;                // 16-byte chunks of a row
   static constexpr int HALF = KT * D * 2;         // bytes of a tile's keys, and of its values
   static constexpr int RING = 2 * 2 * HALF;       // two slots
   static constexpr int SLOTS = 2 * KT;            // slot numbers of gathered tiles
   static constexpr int WARP_BYTES = RING + SLOTS * 4;
-  static_assert(UNIT == 4 * KT, "four tiles");
 };
 
 // Chunk c of row r in a swizzled tile of rows of CH chunks.
@@ -92,8 +90,8 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
 // units [u0, u1) of the sequence's `units`.  b, t: request, and token of a
 // gathered list; part: number of the partial result.
 template <int D, int MT, bool BF16, bool GATHER, bool PREFIX>
-__device__ __forceinline__ void stream_item(const AttnArgs& a, int h, int tile, int b, int t, int u0, int u1, int units,
-                                            int part) {
+__device__ __forceinline__ void stream_item(const AttnArgs& a, int shift, int h, int tile, int b, int t, int u0, int u1,
+                                            int units, int part) {
   using C = StreamCfg<D, MT>;
   constexpr int KT = C::KT, NT = KT / 8, KS = D / 16, CH = C::CH;
   constexpr int R = 16 * MT;
@@ -126,7 +124,7 @@ __device__ __forceinline__ void stream_item(const AttnArgs& a, int h, int tile, 
   }
   const int most = __reduce_max_sync(0xffffffffu, lim_l);
   const int n = GATHER ? (most > 0 ? (int)p.W : 0) : most;  // keys of the sequence
-  const int k0 = u0 * C::UNIT, k1 = min(n, u1 * C::UNIT);
+  const int k0 = u0 << shift, k1 = (int)min((int64_t)n, (int64_t)u1 << shift);
   const int parts_all = a.parts_prefix + a.parts_private;
   const int parts = PREFIX ? a.parts_prefix : a.parts_private, at0 = PREFIX ? 0 : a.parts_prefix;
   // the warp with a sequence's last unit marks the partial results that the
@@ -369,7 +367,7 @@ __global__ void __launch_bounds__(32 * kWarps, MT == 1 ? 3 : 2)
     if (group < line.own_groups) {
       const int each = line.own_units / line.own_groups, extra = line.own_units - each * line.own_groups;
       const int lo = group * each + min(group, extra);
-      stream_item<D, MT, BF16, false, true>(a, member - tile * p.n_kv, tile, 0, 0, lo, lo + each + (group < extra ? 1 : 0),
+      stream_item<D, MT, BF16, false, true>(a, line.unit_shift, member - tile * p.n_kv, tile, 0, 0, lo, lo + each + (group < extra ? 1 : 0),
                                             line.own_units, group);
     }
     if (blockIdx.x == gridDim.x - 1) grid_wait();
@@ -389,7 +387,7 @@ __global__ void __launch_bounds__(32 * kWarps, MT == 1 ? 3 : 2)
   } else if (!GATHER && seqs) {
     const int b0 = min(seqs, tid * per), b1 = min(seqs, b0 + per);
     int mine = 0;
-    for (int b = b0; b < b1; b++) mine += cache_units<C::UNIT>(p, b);
+    for (int b = b0; b < b1; b++) mine += cache_units(p, b, line.unit_shift);
     int incl = mine;
 #pragma unroll
     for (int s = 1; s < 32; s <<= 1) {
@@ -417,7 +415,7 @@ __global__ void __launch_bounds__(32 * kWarps, MT == 1 ? 3 : 2)
   const int hi = group < groups ? lo + each + (group < extra ? 1 : 0) : lo;
   if (lo < hi && lo < line.prefix_units) {
     const int u1 = min(hi, line.prefix_units);
-    stream_item<D, MT, BF16, false, true>(a, h, tile, 0, 0, lo, u1, line.prefix_units, group);
+    stream_item<D, MT, BF16, false, true>(a, line.unit_shift, h, tile, 0, 0, lo, u1, line.prefix_units, group);
     lo = u1;
   }
   if (lo < hi) {
@@ -434,21 +432,21 @@ __global__ void __launch_bounds__(32 * kWarps, MT == 1 ? 3 : 2)
         last += __popc(__ballot_sync(0xffffffffu, s_first[x + lane] <= lo && (x + lane) * per < seqs));
       seq = last * per;
       start = s_first[last];
-      units = cache_units<C::UNIT>(p, seq);
+      units = cache_units(p, seq, line.unit_shift);
       while (start + units <= lo) {
         start += units;
-        units = cache_units<C::UNIT>(p, ++seq);
+        units = cache_units(p, ++seq, line.unit_shift);
       }
     }
     while (true) {
       const int b = GATHER ? seq / p.T : seq;
-      stream_item<D, MT, BF16, GATHER, false>(a, h, tile, b, GATHER ? seq - b * p.T : 0, lo - start, min(units, hi - start),
+      stream_item<D, MT, BF16, GATHER, false>(a, line.unit_shift, h, tile, b, GATHER ? seq - b * p.T : 0, lo - start, min(units, hi - start),
                                               units, group - group_of(start));
       start += units;
       lo = start;
       if (lo >= hi) break;
       seq++;
-      if (!GATHER && !line.uniform) units = cache_units<C::UNIT>(p, seq);
+      if (!GATHER && !line.uniform) units = cache_units(p, seq, line.unit_shift);
     }
   }
   // The finish kernel waits for this grid alone, so it has to end behind the
