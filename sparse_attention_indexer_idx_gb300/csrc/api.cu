@@ -118,6 +118,12 @@ static idx_status check_attn(const attn_problem* p) {
   if (p->dtype != IDX_BF16 && p->dtype != IDX_F16)
     return fail(IDX_ERR_UNSUPPORTED, "dtype %d (IDX_BF16 or IDX_F16)", p->dtype);
   if (p->D != 64 && p->D != 128) return fail(IDX_ERR_UNSUPPORTED, "D=%d (64 or 128)", p->D);
+  // strides whose products with any index stay far inside 64 bits
+  for (int64_t x : {p->q_stride_b, p->q_stride_t, p->q_stride_h, p->k_stride_b, p->k_stride_s, p->k_stride_h,
+                    p->v_stride_b, p->v_stride_s, p->v_stride_h, p->pk_stride_s, p->pk_stride_h, p->pv_stride_s,
+                    p->pv_stride_h})
+    if (x > ((int64_t)1 << 40) || x < -((int64_t)1 << 40))
+      return fail(IDX_ERR_UNSUPPORTED, "stride of %lld elements", (long long)x);
   // bounds that keep grids, row counts and key indices inside 32 bits
   if (p->S > (1 << 30) || p->P > (1 << 30) || p->W > (1 << 30) ||
       (int64_t)p->B * p->T > ((int64_t)1 << 30) / p->Hq || (int64_t)p->T * p->Hq > (1 << 20) || !attn_shared_fits(*p))

@@ -351,3 +351,39 @@ def test_steep_scores_on_the_tensor_cores(B, rows, Hq, n_kv, P, D, dtype):
         few = dict(t, q=t["q"][pick])
         check(few, out[pick], lse[pick], None)
     assert B.device_error() == 0
+
+
+def test_step_in_a_graph(B):
+    """Attention and eviction captured once and replayed on new contents."""
+    t = make(70, B=20, T=1, Hq=16, n_kv=2, D=128, P=9000, S=300, mass=1, lens=[300] * 20)
+    d = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in t.items()}
+    p = B.AttnProblem(d["q"], t["scale"], d["k"], d["v"], d["lens"], d["pk"], d["pv"])
+    out, lse = torch.empty_like(d["q"]), torch.empty((20, 1, 16), device="cuda")
+    ws = torch.empty(B.attn_shared_workspace_size(p, True), dtype=torch.uint8, device="cuda")
+    lens = torch.full((20, 1), 300, dtype=torch.int32, device="cuda")
+    e = B.EvictProblem(d["mass"], lens, 128, 2, 16, planes=(d["k"], d["v"]))
+    src = torch.empty((20, 1, 128), dtype=torch.int32, device="cuda")
+
+    def step():
+        B.attn_shared(p, out, lse, d["mass"], ws)
+        B.cache_evict(e, src)
+
+    start = [x.clone() for x in (d["mass"], d["k"], d["v"])]
+    step()
+    want = [x.clone() for x in (out, lse, d["mass"], src, d["k"], d["v"])]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            step()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for x, y in zip((d["mass"], d["k"], d["v"]), start):
+            x.copy_(y)
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        for x, y in zip((out, lse, d["mass"], src, d["k"], d["v"]), want):
+            assert torch.equal(x, y)
+    assert B.device_error() == 0
