@@ -37,23 +37,42 @@ PrefixWay prefix_way(const attn_problem& p) {
              : kOwnLine;
 }
 
-// The tensor-core kernel's grid.  A whole number of pieces per (KV head, row
-// tile pair) is taken if it leaves at most a tenth of the SMs idle; otherwise
-// the key tiles are cut evenly, and a piece can end up on two blocks.  (Leaving
-// a part of the SMs to the streaming kernel, in proportion to the work, was
-// slower than one after the other: 378 against 354 us on a shared document of
-// 65536 tokens under 128 requests.)
+// The tensor-core kernel's grid: a whole number of pieces of the keys per (KV
+// head, row tile pair), so that the row tiles of a piece run in step and their
+// keys come from L2, if that leaves few SMs idle; otherwise the key tiles are
+// cut evenly, and a piece can end up on two blocks.  On 65536 keys under 1024
+// rows of each of 8 heads, 128 whole pieces and an even cut over 152 SMs take
+// the same time (190 and 192 us), on 8192 keys 39 and 51 us; with heads of 64,
+// where the weights take longer than the products, the idle SMs cost more (181
+// against 164 us).
+//
+// Beside private caches the grid is smaller: the streaming kernel, which waits
+// for memory most of the time, starts on the SMs that are left.  The share
+// follows the two kernels' work (1.6 us a key tile under two row tiles, 0.9 us
+// under one; 55 bytes/ns of an SM that streams, caches taken as 0.6 full, their
+// lengths being on the device), and a block takes eight key tiles at least, so
+// that its start and end count little.  One after the other took 337 us for the
+// shared document of 128 requests, side by side 289; 53 and 41 for 32 requests.
 AttnTcArgs plan_tc(const AttnArgs& a) {
   const attn_problem& p = a.p;
   AttnTcArgs t{};
   t.a = a;
   const int64_t tiles = ceil_div(p.P, 128), n = sm_count();
-  t.row_tiles = (int)ceil_div((int64_t)p.B * p.T * a.G, 256);
-  const int64_t items = (int64_t)p.n_kv * t.row_tiles;
-  const int64_t whole = std::min(tiles, n / items);
-  t.whole_cells = whole > 0 && (whole == tiles || items * whole * 10 >= n * 9);
-  t.cells_k = (int)(t.whole_cells ? whole : std::min(tiles, ceil_div(n, items)));
-  t.blocks = (int)(t.whole_cells ? items * whole : std::min(n, items * tiles));
+  const int64_t rows = (int64_t)p.B * p.T * a.G;
+  t.row_tiles = (int)ceil_div(rows, 256);
+  const int64_t items = (int64_t)p.n_kv * t.row_tiles, most = std::min(tiles, n / items);
+  const bool whole = most > 0 && (most == tiles || items * most * 10 >= n * (p.D == 128 ? 8 : 9));
+  int64_t pieces = whole ? most : 0;
+  if (most > 0 && private_keys(p) > 0) {
+    const double keys = (p.ids ? (double)p.T * p.W : (double)p.S) * p.B * p.n_kv;
+    const double mine = items * (6.0 + tiles * (rows > 128 ? 1.6 : 0.9)), other = 0.6 * keys * 4 * p.D / 55e3;
+    const double share = std::max(0.4, mine / (mine + other));
+    const int64_t k = std::min((int64_t)(n * share / items), ceil_div(tiles, 8));
+    if (k < most && (pieces || items * k * 10 >= n * share * 7)) pieces = std::max<int64_t>(1, k);
+  }
+  t.whole_cells = pieces > 0;
+  t.cells_k = (int)(pieces ? pieces : std::min(tiles, ceil_div(n, items)));
+  t.blocks = (int)(pieces ? items * pieces : std::min(n, items * tiles));
   return t;
 }
 
@@ -89,7 +108,9 @@ StreamLine plan_stream(AttnArgs& a) {
   }
   const int64_t longest = ceil_div(private_keys(p), unit);
   const int64_t total = l.prefix_units + l.seqs * longest;
-  l.groups = total == 0 ? 0 : (int)std::max<int64_t>(1, warps / l.members);
+  // beside the tensor-core kernel two shares for each place: the second ones
+  // begin when that kernel leaves its SMs, or where a first one ends
+  l.groups = total == 0 ? 0 : (int)std::max<int64_t>(1, (way == kTensorCore ? 2 : 1) * warps / l.members);
   l.least = (int)std::max<int64_t>(1, ceil_div(total, 4 * std::max<int64_t>(1, l.groups)));
   // Lists have one length; short lines are cut as if all caches were full, which
   // saves their blocks the look at the lengths.
