@@ -241,8 +241,10 @@ _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _raw_stream(stream: Optional[torch.cuda.Stream]):
-    if stream is not None or _current_raw_stream is None:
-        return _stream(stream)
+    if stream is not None:
+        return stream.cuda_stream
+    if _current_raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
     return _current_raw_stream(torch.cuda.current_device())
 
 
@@ -541,7 +543,7 @@ class _Described:
                 return d
         self.__dict__.pop("_desc", None)
         c = self.c()
-        d = (ctypes.byref(c), [(t, t.data_ptr()) for t in self._tensors()], c)
+        d = (ctypes.byref(c), [(t, t.data_ptr()) for t in self._tensors()], c, self._shapes(c))
         self.__dict__["_desc"] = d
         return d
 
@@ -560,6 +562,11 @@ class AttnProblem(_Described):
     pv: Optional[torch.Tensor] = None
     prefix_len: Optional[torch.Tensor] = None    # [B] int32
     ids: Optional[torch.Tensor] = None           # [B, T, W] or [B, T, n_kv, W] int32
+
+    def _shapes(self, c):
+        """Shapes of out, lse, and mass with one and with n_kv mass heads."""
+        q = self.q.shape
+        return q, q[:3], torch.Size((c.B, 1, c.S)), torch.Size((c.B, c.n_kv, c.S))
 
     def c(self) -> attn_problem:
         q = self.q
@@ -612,16 +619,17 @@ def attn_shared(p: AttnProblem, out: torch.Tensor, lse: Optional[torch.Tensor], 
                 ws: torch.Tensor, stream=None):
     """out [B, T, Hq, D]; lse [B, T, Hq] float32 or None; mass [B, n_kv or 1, S]
     float32 (added to) or None."""
-    ref, _, cp = p.desc()
-    shape = p.q.shape
-    po = _out(out, "out", shape, p.q.dtype)
-    pl = None if lse is None else _out(lse, "lse", shape[:3], torch.float32)
+    ref, _, cp, (so, sl, s1, sh) = p.desc()
+    po = _out(out, "out", so, p.q.dtype)
+    pl = None if lse is None else _out(lse, "lse", sl, torch.float32)
     pm, heads = None, 1
     if mass is not None:
-        _need(p.k is not None, "mass: there is no private cache")
-        heads = mass.shape[1] if mass.dim() == 3 and mass.shape[1] == cp.n_kv else 1
-        pm = _out(mass, "mass", (cp.B, heads, cp.S), torch.float32)
-    st = (_lib or lib()).attn_shared(ref, po, pl, pm, heads, _ptr(ws), ws.nbytes, _raw_stream(stream))
+        _need(cp.S > 0, "mass: there is no private cache")
+        one = mass.shape == s1
+        heads = 1 if one else cp.n_kv
+        pm = _out(mass, "mass", s1 if one else sh, torch.float32)
+    _need(ws.is_cuda and ws.is_contiguous(), "ws: expected a contiguous CUDA tensor")
+    st = (_lib or lib()).attn_shared(ref, po, pl, pm, heads, ws.data_ptr(), ws.nbytes, _raw_stream(stream))
     if st:
         _check(st)
     return out, lse, mass
@@ -640,6 +648,10 @@ class EvictProblem(_Described):
     pos: Optional[torch.Tensor] = None           # [B, mass_heads, S] int32
     cur: Optional[torch.Tensor] = None           # [B] int32
     planes: tuple = ()
+
+    def _shapes(self, c):
+        """Shapes of out_src (and of outputs beside it), and of out_len."""
+        return torch.Size((c.B, c.mass_heads, c.n_keep)), torch.Size((c.B, c.mass_heads))
 
     def c(self) -> evict_problem:
         _need(self.mass.dim() == 3, "mass: expected [B, mass_heads, S]")
@@ -673,19 +685,19 @@ def cache_evict(p: EvictProblem, out_src: torch.Tensor, out_len: Optional[torch.
     """out_src [B, mass_heads, n_keep] int32; out_len [B, mass_heads] int32;
     out_pos / out_mass [B, mass_heads, n_keep], or the problem's pos / mass
     themselves."""
-    ref, _, ce = p.desc()
-    B, Hm, K = ce.B, ce.mass_heads, ce.n_keep
-    ps = _out(out_src, "out_src", (B, Hm, K), torch.int32)
-    pl = None if out_len is None else _out(out_len, "out_len", (B, Hm), torch.int32)
-    ld, pp, pm = K, None, None
-    if out_pos is not None:
-        ld = out_pos.shape[-1]
-        pp = _out(out_pos, "out_pos", (B, Hm, ld), torch.int32)
-    if out_mass is not None:
-        _need(out_pos is None or out_mass.shape[-1] == ld, "out_pos and out_mass: row strides differ")
-        ld = out_mass.shape[-1]
-        pm = _out(out_mass, "out_mass", (B, Hm, ld), torch.float32)
-    _need(ld >= K, "out_pos and out_mass: rows shorter than n_keep")
+    ref, _, ce, (ss, sl) = p.desc()
+    ps = _out(out_src, "out_src", ss, torch.int32)
+    pl = None if out_len is None else _out(out_len, "out_len", sl, torch.int32)
+    ld, pp, pm = ss[2], None, None
+    if out_pos is not None or out_mass is not None:
+        wide = (out_pos if out_pos is not None else out_mass).shape
+        so = ss if wide == ss else torch.Size((ss[0], ss[1], wide[-1]))
+        ld = so[2]
+        _need(ld >= ss[2], "out_pos and out_mass: rows shorter than n_keep")
+        if out_pos is not None:
+            pp = _out(out_pos, "out_pos", so, torch.int32)
+        if out_mass is not None:
+            pm = _out(out_mass, "out_mass", so, torch.float32)
     st = (_lib or lib()).cache_evict(ref, ps, pl, pp, pm, ld, _raw_stream(stream))
     if st:
         _check(st)

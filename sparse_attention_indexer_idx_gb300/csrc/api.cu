@@ -126,7 +126,7 @@ static idx_status check_attn(const attn_problem* p) {
       return fail(IDX_ERR_UNSUPPORTED, "stride of %lld elements", (long long)x);
   // bounds that keep grids, row counts and key indices inside 32 bits
   if (p->S > (1 << 30) || p->P > (1 << 30) || p->W > (1 << 30) ||
-      (int64_t)p->B * p->T > ((int64_t)1 << 30) / p->Hq || (int64_t)p->T * p->Hq > (1 << 20) || !attn_shared_fits(*p))
+      (int64_t)p->B * p->T > ((int64_t)1 << 30) / p->Hq || (int64_t)p->T * p->Hq > (1 << 20))
     return fail(IDX_ERR_UNSUPPORTED, "problem too large (B=%d T=%d Hq=%d S=%lld P=%lld W=%lld)", p->B, p->T, p->Hq,
                 (long long)p->S, (long long)p->P, (long long)p->W);
   if (!(p->scale == p->scale) || p->scale - p->scale != 0.f) return fail(IDX_ERR_INVALID_ARG, "scale is not finite");
@@ -423,10 +423,17 @@ idx_status attn_shared(const attn_problem* p, void* out, float* lse, float* mass
   if (p->B == 0) return IDX_OK;
   if (!out) return fail(IDX_ERR_INVALID_ARG, "out is NULL");
   if (p->S == 0) mass = nullptr;
-  if (ws_bytes < attn_shared_ws(*p, mass != nullptr)) return fail(IDX_ERR_WORKSPACE_TOO_SMALL, "workspace too small");
-  if (!ws) return fail(IDX_ERR_INVALID_ARG, "workspace is NULL");
-  return cuda_status(launch_attn_shared(*p, out, lse, mass, mass ? mass_heads : 1, ws, (cudaStream_t)stream),
-                     "attn_shared");
+  cudaError_t e = cudaSuccess;
+  st = launch_attn_shared(*p, out, lse, mass, mass ? mass_heads : 1, ws, ws_bytes, (cudaStream_t)stream, &e);
+  switch (st) {
+    case IDX_OK: return st;
+    case IDX_ERR_CUDA: return cuda_status(e, "attn_shared");
+    case IDX_ERR_WORKSPACE_TOO_SMALL: return fail(st, "workspace too small");
+    case IDX_ERR_INVALID_ARG: return fail(st, "workspace is NULL");
+    default:
+      return fail(st, "problem too large (B=%d T=%d Hq=%d S=%lld P=%lld W=%lld)", p->B, p->T, p->Hq, (long long)p->S,
+                  (long long)p->P, (long long)p->W);
+  }
 }
 
 idx_status cache_evict(const evict_problem* p, int32_t* out_src, int32_t* out_len, int32_t* out_pos, float* out_mass,

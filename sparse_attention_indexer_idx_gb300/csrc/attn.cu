@@ -162,26 +162,32 @@ AttnArgs make_args(const attn_problem& p) {
 
 }  // namespace
 
-size_t attn_shared_ws(const attn_problem& p, bool mass) { return layout(make_args(p), mass).total; }
-
-bool attn_shared_fits(const attn_problem& p) {
-  // the lines of key units and tiles are counted in 32 bits
-  const int64_t unit = stream_tile(p.D), G = p.Hq / p.n_kv;
+// The lines of key tiles, the partial results and the rows of q (in 16 bytes)
+// are counted in 32 bits.
+static bool fits(const AttnArgs& a) {
+  const attn_problem& p = a.p;
+  const int64_t tile = stream_tile(p.D), most = (int64_t)1 << 31;
   const int64_t seqs = (int64_t)p.B * (p.ids ? p.T : 1);
-  const int64_t line = ceil_div(p.P, unit) + seqs * std::max<int64_t>(1, ceil_div(private_keys(p), unit));
-  const int64_t tiles = ceil_div((int64_t)p.B * p.T * G, 256) * p.n_kv * ceil_div(p.P, 128);
-  if (line >= ((int64_t)1 << 31) || tiles >= ((int64_t)1 << 31)) return false;
-  // and so are the partial results, and the rows of q (in 16 bytes)
-  const AttnArgs a = make_args(p);
+  const int64_t line = ceil_div(p.P, tile) + seqs * std::max<int64_t>(1, ceil_div(private_keys(p), tile));
+  const int64_t tiles = ceil_div((int64_t)p.B * p.T * a.G, 256) * p.n_kv * ceil_div(p.P, 128);
+  const int64_t rows = (int64_t)p.B * p.T * p.Hq;
   auto span = [](int64_t n, int64_t stride) { return (n - 1) * (stride < 0 ? -stride : stride); };
   const int64_t q = span(p.B, p.q_stride_b) + span(p.T, p.q_stride_t) + span(p.Hq, p.q_stride_h);
-  return (int64_t)p.B * p.T * p.Hq * (a.parts_prefix + a.parts_private) < ((int64_t)1 << 31) && q / 8 < ((int64_t)1 << 31);
+  return line < most && tiles < most && rows * (a.parts_prefix + a.parts_private) < most && q / 8 < most;
 }
 
-cudaError_t launch_attn_shared(const attn_problem& p, void* out, float* lse, float* mass, int mass_heads, void* ws,
-                               cudaStream_t st) {
+size_t attn_shared_ws(const attn_problem& p, bool mass) {
+  const AttnArgs a = make_args(p);
+  return fits(a) ? layout(a, mass).total : 0;
+}
+
+idx_status launch_attn_shared(const attn_problem& p, void* out, float* lse, float* mass, int mass_heads, void* ws,
+                              size_t ws_bytes, cudaStream_t st, cudaError_t* err) {
   AttnArgs a = make_args(p);
+  if (!fits(a)) return IDX_ERR_UNSUPPORTED;
   const AttnWs w = layout(a, mass != nullptr);
+  if (ws_bytes < w.total) return IDX_ERR_WORKSPACE_TOO_SMALL;
+  if (!ws) return IDX_ERR_INVALID_ARG;
   char* base = (char*)(((uintptr_t)ws + 255) & ~uintptr_t(255));
   a.po = (float*)(base + w.po);
   a.pml = (float2*)(base + w.pml);
@@ -196,7 +202,8 @@ cudaError_t launch_attn_shared(const attn_problem& p, void* out, float* lse, flo
   const StreamLine line = plan_stream(a);
   if (e == cudaSuccess && line.own_blocks + line.prefix_units + line.seqs > 0) e = launch_attn_stream(a, line, tc, st);
   if (e == cudaSuccess) e = launch_attn_finish(a, st);
-  return e;
+  *err = e;
+  return e == cudaSuccess ? IDX_OK : IDX_ERR_CUDA;
 }
 
 }  // namespace idx

@@ -111,11 +111,12 @@ cudaError_t launch_dosa(const idx_problem& p, int K, const dosa_params& dp, cons
                         int32_t* out_ids, float* out_scores, int32_t* row_status, dosa_stats* stats, void* ws,
                         size_t ws_bytes, cudaStream_t st);
 
-bool attn_shared_fits(const attn_problem& p);  // its work is countable in 32 bits
+// 0: the problem's work is not countable in 32 bits
 size_t attn_shared_ws(const attn_problem& p, bool mass);
-cudaError_t launch_attn_shared(const attn_problem& p, void* out, float* lse, float* mass, int mass_heads, void* ws,
-                               cudaStream_t st);
-
+// Refuses (without a message) what does not fit 32 bits or the workspace; *err
+// with IDX_ERR_CUDA.
+idx_status launch_attn_shared(const attn_problem& p, void* out, float* lse, float* mass, int mass_heads, void* ws,
+                              size_t ws_bytes, cudaStream_t st, cudaError_t* err);
 int64_t evict_max_slots();  // longest row that cache_evict takes
 cudaError_t launch_evict(const evict_problem& p, int32_t* src, int32_t* out_len, int32_t* out_pos, float* out_mass,
                          int64_t out_stride, cudaStream_t st);
