@@ -199,7 +199,8 @@ idx_status launch_attn_shared(const attn_problem& p, void* out, float* lse, floa
   cudaError_t e = cudaSuccess;
   const bool tc = prefix_way(p) == kTensorCore;
   if (tc) e = launch_attn_tc(plan_tc(a), st);
-  const StreamLine line = plan_stream(a);
+  StreamLine line = plan_stream(a);
+  line.after = tc;
   if (e == cudaSuccess && line.own_blocks + line.prefix_units + line.seqs > 0) e = launch_attn_stream(a, line, tc, st);
   if (e == cudaSuccess) e = launch_attn_finish(a, st);
   *err = e;

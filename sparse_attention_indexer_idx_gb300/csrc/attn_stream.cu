@@ -357,6 +357,7 @@ __global__ void __launch_bounds__(32 * kWarps, MT == 1 ? 3 : 2)
   constexpr int NT = 32 * kWarps;
   __shared__ int s_sum[kWarps];
   __shared__ int s_first[NT];
+  if (!line.after) grid_wait();
   grid_let_next_start();
   const attn_problem& p = a.p;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -463,7 +464,7 @@ cudaError_t launch(const AttnArgs& a, const StreamLine& line, bool after, cudaSt
   static KernelReady ready;
   cudaError_t e = ready.once([&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
   if (e != cudaSuccess) return e;
-  return launch_after(kern, dim3((unsigned)(line.own_blocks + (line.members * line.groups + kWarps - 1) / kWarps)), 32 * kWarps, smem, st, after, a, line);
+  return launch_after(kern, dim3((unsigned)(line.own_blocks + (line.members * line.groups + kWarps - 1) / kWarps)), 32 * kWarps, smem, st, true, a, line);
 }
 
 template <int D, bool BF16, bool GATHER>

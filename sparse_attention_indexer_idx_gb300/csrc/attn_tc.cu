@@ -208,6 +208,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int parts_all = a.parts_prefix + a.parts_private;
 
+  grid_wait();
   grid_let_next_start();
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NS; i++) {
@@ -671,8 +672,7 @@ cudaError_t launch(const AttnTcArgs& t, cudaStream_t st) {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   });
   if (e != cudaSuccess) return e;
-  kern<<<t.blocks, kThreadsTc, C::SMEM, st>>>(tk, tv, t);
-  return cudaGetLastError();
+  return launch_after(kern, dim3((unsigned)t.blocks), kThreadsTc, C::SMEM, st, true, tk, tv, t);
 }
 
 }  // namespace

@@ -100,6 +100,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_select_kernel(const __gri
   uint32_t* bitmap = keys + slice_max;
   uint16_t* rank = reinterpret_cast<uint16_t*>(bitmap + slice_max / 32);
   __shared__ SelShared<ONE> sh;
+  grid_wait();
   grid_let_next_start();
   const RowGroup<ONE> cl;
   const evict_problem& p = a.p;
@@ -536,12 +537,14 @@ static cudaError_t launch_select(const EvictArgs& a, int64_t rows, int C, cudaSt
   cfg.blockDim = dim3(NT);
   cfg.dynamicSmemBytes = bytes(slice);
   cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)C;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)C;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = ONE ? 0 : 1;
+  cfg.numAttrs = ONE ? 1 : 2;
   return cudaLaunchKernelEx(&cfg, kern, a, (int)slice);
 }
 
