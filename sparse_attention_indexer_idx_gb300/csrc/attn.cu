@@ -85,6 +85,7 @@ StreamLine plan_stream(AttnArgs& a) {
   const attn_problem& p = a.p;
   StreamLine l{};
   const PrefixWay way = prefix_way(p);
+  l.after = way == kTensorCore;
   const int64_t rows_pre = (int64_t)p.B * p.T * a.G;
   const int64_t rows = std::max<int64_t>(p.S == 0 ? 1 : p.ids ? a.G : (int64_t)p.T * a.G, way == kLine ? rows_pre : 1);
   l.row_tile = rows <= 16 ? 16 : 32;
@@ -197,11 +198,9 @@ idx_status launch_attn_shared(const attn_problem& p, void* out, float* lse, floa
   a.mass = mass;
   a.mass_heads = mass_heads;
   cudaError_t e = cudaSuccess;
-  const bool tc = prefix_way(p) == kTensorCore;
-  if (tc) e = launch_attn_tc(plan_tc(a), st);
-  StreamLine line = plan_stream(a);
-  line.after = tc;
-  if (e == cudaSuccess && line.own_blocks + line.prefix_units + line.seqs > 0) e = launch_attn_stream(a, line, tc, st);
+  if (prefix_way(p) == kTensorCore) e = launch_attn_tc(plan_tc(a), st);
+  const StreamLine line = plan_stream(a);
+  if (e == cudaSuccess && line.own_blocks + line.prefix_units + line.seqs > 0) e = launch_attn_stream(a, line, st);
   if (e == cudaSuccess) e = launch_attn_finish(a, st);
   *err = e;
   return e == cudaSuccess ? IDX_OK : IDX_ERR_CUDA;

@@ -73,7 +73,7 @@ __device__ __forceinline__ float attn_ex2(float x) {
 
 // The streaming kernel's line of key units and its cut (see attn_stream.cu).
 struct StreamLine {
-  bool after;        // a kernel of the same call comes before
+  bool after;        // the tensor-core kernel comes before: it writes nothing that this one reads
   int unit_shift;    // a unit is 2^unit_shift keys: a tile, or four
   int row_tile;      // 16 or 32 rows of a warp
   int members;       // warps of a group: KV heads times row tiles
@@ -85,9 +85,7 @@ struct StreamLine {
   // a short prefix under many rows: a line of its own, taken by the first blocks
   int own_blocks, own_members, own_groups, own_units;
 };
-// after: a kernel of the same call comes before this one, and does not write
-// what this one reads.
-cudaError_t launch_attn_stream(const AttnArgs& a, const StreamLine& line, bool after, cudaStream_t st);
+cudaError_t launch_attn_stream(const AttnArgs& a, const StreamLine& line, cudaStream_t st);
 cudaError_t launch_attn_finish(const AttnArgs& a, cudaStream_t st);
 
 }  // namespace idx

@@ -366,8 +366,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
   }
   const int64_t blocks = join + (int64_t)p.B * a.mass_heads * per;
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
-  return launch_after(kern, dim3((unsigned)blocks), kThreads, 0, st, a.parts_prefix + a.parts_private > 0, a, join, per,
-                      groups);
+  return launch_early(kern, dim3((unsigned)blocks), kThreads, 0, st, a, join, per, groups);
 }
 
 }  // namespace

@@ -2,11 +2,11 @@
 // the private caches of a decode step, and a shared prefix under a small batch.
 //
 // Mapping.  The key sequences (the prefix, then every request's cache or list)
-// form one line of units of one or four key tiles; it is cut evenly over groups of warps, with one
-// warp of a group for each KV head (and tile of up to 32 rows).  The heads of a
-// group run side by side, so their rows of a cache, which lie next to one
-// another, are read together, and all groups end together however ragged the
-// lengths are.  A group that starts or ends inside a sequence leaves one of
+// form one line of units of one or four key tiles; it is cut evenly over groups
+// of warps, with one warp of a group for each KV head (and tile of up to 32
+// rows).  The heads of a group run side by side, so their rows of a cache, which
+// lie next to one another, are read together, and all groups end together
+// however ragged the lengths are.  A group that starts or ends inside a sequence leaves one of
 // several partial results of it.
 //
 // Every warp is a stream of its own: it copies tiles of KT keys and values with
@@ -368,7 +368,8 @@ __global__ void __launch_bounds__(32 * kWarps, MT == 1 ? 3 : 2)
     if (group < line.own_groups) {
       const int each = line.own_units / line.own_groups, extra = line.own_units - each * line.own_groups;
       const int lo = group * each + min(group, extra);
-      stream_item<D, MT, BF16, false, true>(a, line.unit_shift, member - tile * p.n_kv, tile, 0, 0, lo, lo + each + (group < extra ? 1 : 0),
+      const int hi = lo + each + (group < extra ? 1 : 0);
+      stream_item<D, MT, BF16, false, true>(a, line.unit_shift, member - tile * p.n_kv, tile, 0, 0, lo, hi,
                                             line.own_units, group);
     }
     if (blockIdx.x == gridDim.x - 1) grid_wait();
@@ -441,8 +442,8 @@ __global__ void __launch_bounds__(32 * kWarps, MT == 1 ? 3 : 2)
     }
     while (true) {
       const int b = GATHER ? seq / p.T : seq;
-      stream_item<D, MT, BF16, GATHER, false>(a, line.unit_shift, h, tile, b, GATHER ? seq - b * p.T : 0, lo - start, min(units, hi - start),
-                                              units, group - group_of(start));
+      stream_item<D, MT, BF16, GATHER, false>(a, line.unit_shift, h, tile, b, GATHER ? seq - b * p.T : 0, lo - start,
+                                              min(units, hi - start), units, group - group_of(start));
       start += units;
       lo = start;
       if (lo >= hi) break;
@@ -450,40 +451,41 @@ __global__ void __launch_bounds__(32 * kWarps, MT == 1 ? 3 : 2)
       if (!GATHER && !line.uniform) units = cache_units(p, seq, line.unit_shift);
     }
   }
-  // The finish kernel waits for this grid alone, so it has to end behind the
-  // one before it: one block waits for that (a wait of every block would keep
-  // the next ones from their places).
+  // The finish kernel waits for this grid alone, so behind the tensor-core
+  // kernel this one has to end later than that: one block waits for it (a wait of
+  // every block would keep the next ones from their places).
   if (blockIdx.x == gridDim.x - 1) grid_wait();
 }
 
 template <int D, int MT, bool BF16, bool GATHER>
-cudaError_t launch(const AttnArgs& a, const StreamLine& line, bool after, cudaStream_t st) {
+cudaError_t launch(const AttnArgs& a, const StreamLine& line, cudaStream_t st) {
   using C = StreamCfg<D, MT>;
   const int smem = kWarps * (GATHER ? C::WARP_BYTES : C::RING);
   auto kern = attn_stream_kernel<D, MT, BF16, GATHER>;
   static KernelReady ready;
   cudaError_t e = ready.once([&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
   if (e != cudaSuccess) return e;
-  return launch_after(kern, dim3((unsigned)(line.own_blocks + (line.members * line.groups + kWarps - 1) / kWarps)), 32 * kWarps, smem, st, true, a, line);
+  const int blocks = line.own_blocks + (line.members * line.groups + kWarps - 1) / kWarps;
+  return launch_early(kern, dim3((unsigned)blocks), 32 * kWarps, smem, st, a, line);
 }
 
 template <int D, bool BF16, bool GATHER>
-cudaError_t launch_rows(const AttnArgs& a, const StreamLine& line, bool after, cudaStream_t st) {
-  return line.row_tile == 16 ? launch<D, 1, BF16, GATHER>(a, line, after, st)
-                             : launch<D, 2, BF16, GATHER>(a, line, after, st);
+cudaError_t launch_rows(const AttnArgs& a, const StreamLine& line, cudaStream_t st) {
+  return line.row_tile == 16 ? launch<D, 1, BF16, GATHER>(a, line, st)
+                             : launch<D, 2, BF16, GATHER>(a, line, st);
 }
 
 template <int D, bool BF16>
-cudaError_t launch_kind(const AttnArgs& a, const StreamLine& line, bool after, cudaStream_t st) {
-  return a.p.ids ? launch_rows<D, BF16, true>(a, line, after, st) : launch_rows<D, BF16, false>(a, line, after, st);
+cudaError_t launch_kind(const AttnArgs& a, const StreamLine& line, cudaStream_t st) {
+  return a.p.ids ? launch_rows<D, BF16, true>(a, line, st) : launch_rows<D, BF16, false>(a, line, st);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_stream(const AttnArgs& a, const StreamLine& line, bool after, cudaStream_t st) {
+cudaError_t launch_attn_stream(const AttnArgs& a, const StreamLine& line, cudaStream_t st) {
   const bool bf = a.p.dtype == IDX_BF16;
-  if (a.p.D == 128) return bf ? launch_kind<128, true>(a, line, after, st) : launch_kind<128, false>(a, line, after, st);
-  return bf ? launch_kind<64, true>(a, line, after, st) : launch_kind<64, false>(a, line, after, st);
+  if (a.p.D == 128) return bf ? launch_kind<128, true>(a, line, st) : launch_kind<128, false>(a, line, st);
+  return bf ? launch_kind<64, true>(a, line, st) : launch_kind<64, false>(a, line, st);
 }
 
 }  // namespace idx

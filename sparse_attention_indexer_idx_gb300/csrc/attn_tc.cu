@@ -672,7 +672,7 @@ cudaError_t launch(const AttnTcArgs& t, cudaStream_t st) {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   });
   if (e != cudaSuccess) return e;
-  return launch_after(kern, dim3((unsigned)t.blocks), kThreadsTc, C::SMEM, st, true, tk, tv, t);
+  return launch_early(kern, dim3((unsigned)t.blocks), kThreadsTc, C::SMEM, st, tk, tv, t);
 }
 
 }  // namespace

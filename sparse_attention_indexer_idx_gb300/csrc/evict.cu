@@ -588,8 +588,8 @@ cudaError_t launch_evict(const evict_problem& p, int32_t* src, int32_t* out_len,
   const int64_t wide = rows * ((p.n_keep + 1023) / 1024), narrow = rows * ((p.n_keep + 255) / 256);
   const unsigned ph = (unsigned)m.first[m.n_planes];
   return wide * ph >= 16 * sm_count()
-             ? launch_after(evict_move_kernel<1024>, dim3((unsigned)wide, ph), kMoveThreads, 0, st, true, m)
-             : launch_after(evict_move_kernel<256>, dim3((unsigned)narrow, ph), kMoveThreads, 0, st, true, m);
+             ? launch_early(evict_move_kernel<1024>, dim3((unsigned)wide, ph), kMoveThreads, 0, st, m)
+             : launch_early(evict_move_kernel<256>, dim3((unsigned)narrow, ph), kMoveThreads, 0, st, m);
 }
 
 }  // namespace idx
