@@ -51,7 +51,8 @@ PrefixWay prefix_way(const attn_problem& p) {
 // follows the two kernels' work (1.6 us a key tile under two row tiles, 0.9 us
 // under one; 55 bytes/ns of an SM that streams, caches taken as 0.6 full, their
 // lengths being on the device), and a block takes eight key tiles at least, so
-// that its start and end count little.  One after the other took 337 us for the
+// that its start and end count little; but where the caches are so short that
+// they need few SMs for a moment, it gets all the others.  One after the other took 337 us for the
 // shared document of 128 requests, side by side 289; 53 and 41 for 32 requests.
 AttnTcArgs plan_tc(const AttnArgs& a) {
   const attn_problem& p = a.p;
@@ -67,7 +68,11 @@ AttnTcArgs plan_tc(const AttnArgs& a) {
     const double keys = (p.ids ? (double)p.T * p.W : (double)p.S) * p.B * p.n_kv;
     const double mine = items * (6.0 + tiles * (rows > 128 ? 1.6 : 0.9)), other = 0.6 * keys * 4 * p.D / 55e3;
     const double share = std::max(0.4, mine / (mine + other));
-    const int64_t k = std::min((int64_t)(n * share / items), ceil_div(tiles, 8));
+    int64_t k = std::min((int64_t)(n * share / items), ceil_div(tiles, 8));
+    const int64_t rows_own = p.ids ? a.G : (int64_t)p.T * a.G, row_tile = rows_own <= 16 ? 16 : 32;
+    const int64_t warps = p.B * (p.ids ? p.T : 1) * ceil_div(private_keys(p), 4 * stream_tile(p.D)) * p.n_kv *
+                          ceil_div(rows_own, row_tile);
+    k = std::max(k, std::min(most, (n - ceil_div(warps, row_tile == 16 ? 12 : 8)) / items));
     if (k < most && (pieces || items * k * 10 >= n * share * 7)) pieces = std::max<int64_t>(1, k);
   }
   t.whole_cells = pieces > 0;

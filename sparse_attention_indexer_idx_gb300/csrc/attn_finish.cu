@@ -20,14 +20,20 @@ constexpr int kSlots = 4;    // consecutive slots of a thread: one 16-byte load 
 constexpr int kRowsAt = 512; // rows whose normalisers are held at a time
 constexpr int kBatch = 8;    // rows loaded before the first is used (dense masses)
 
+// A row is the work of `share` warps (1 to 8), each of a run of its pieces.
 template <int D, bool BF16>
-__device__ void join_rows(const AttnArgs& a) {
-  const int parts = a.parts_prefix + a.parts_private;
+__device__ void join_rows(const AttnArgs& a, int share) {
+  __shared__ float s_acc[kWarps][D];
+  __shared__ float2 s_ml[kWarps];
+  const int all_parts = a.parts_prefix + a.parts_private;
   const int64_t rows = (int64_t)a.p.B * a.p.T * a.p.Hq;
-  const int64_t r = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (r >= rows) return;
-  const float2* ml = a.pml + r * parts;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t r = (int64_t)blockIdx.x * (kWarps / share) + warp / share;
+  const int sub = warp % share;
+  const int each = (all_parts + share - 1) / share;
+  const int p0 = min(all_parts, sub * each);
+  const int parts = r < rows ? min(each, all_parts - p0) : 0;  // of this warp
+  const float2* ml = a.pml + r * all_parts + p0;
   // lane i holds piece i (of the first 32; the others are read again)
   const float2 none = make_float2(-INFINITY, 0.f);
   const float2 first = lane < parts ? ml[lane] : none;
@@ -61,7 +67,7 @@ __device__ void join_rows(const AttnArgs& a) {
 #pragma unroll
         for (int e = 0; e < E; e++) v[u][e] = 0.f;
         if (i >= 0) {
-          const float* o = a.po + (r * parts + i0 + i) * D + lane * E;
+          const float* o = a.po + (r * all_parts + p0 + i0 + i) * D + lane * E;
           if constexpr (E == 4)
             *reinterpret_cast<float4*>(v[u]) = *reinterpret_cast<const float4*>(o);
           else
@@ -76,6 +82,26 @@ __device__ void join_rows(const AttnArgs& a) {
   }
 #pragma unroll
   for (int s = 16; s; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
+  if (share > 1) {
+#pragma unroll
+    for (int e = 0; e < E; e++) s_acc[warp][lane * E + e] = acc[e];
+    if (lane == 0) s_ml[warp] = make_float2(top, l);
+    __syncthreads();
+    if (sub) return;
+    for (int i = 0; i < share; i++) top = fmaxf(top, s_ml[warp + i].x);
+    const float all = top == -INFINITY ? 0.f : top;
+    l = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; e++) acc[e] = 0.f;
+    for (int i = 0; i < share; i++) {
+      const float2 x = s_ml[warp + i];
+      const float w = attn_ex2(x.x - all);
+      l += w * x.y;
+#pragma unroll
+      for (int e = 0; e < E; e++) acc[e] += w * s_acc[warp + i][lane * E + e];
+    }
+  }
+  if (r >= rows) return;
   const float inv = l > 0.f ? 1.f / l : 0.f;
   uint32_t pk[E / 2];
 #pragma unroll
@@ -266,8 +292,10 @@ __device__ __forceinline__ void mass_dense(const AttnArgs& a, int64_t block, int
 
 // Mass of listed slots.  One list holds a slot at most once, so its threads add
 // to different slots; lists that can share a slot (another token's, or another
-// KV head's when all heads share the mass) follow one another in one block.
-// A thread takes E entries, and several rows of each, at a time.
+// KV head's when all heads share the mass) are added one after the other by one
+// block.  A thread takes an entry of each of E chunks of kThreads entries, of
+// one list or of several, and several rows of each, at a time: the chunks' ids
+// and scores are loaded together, only the additions follow the lists' order.
 template <int E>
 __device__ __forceinline__ void mass_listed(const AttnArgs& a, int64_t block, int64_t per) {
   __shared__ MassRows s;
@@ -281,60 +309,67 @@ __device__ __forceinline__ void mass_listed(const AttnArgs& a, int64_t block, in
   const int heads = all / lists_h;      // of these, the ones that read one list
   float* mass = a.mass + bm * p.S;
   // rows (t, query head) of the mass head: list q has rows q * heads ..
-  const bool once = lists * heads <= kRowsAt;
-  const int64_t first = block % per * kThreads + threadIdx.x, step = per * kThreads;
-  if (once) set_rows(a, s, b, 0, m * all, all, 0, lists * heads);
-  for (int q = 0; q < lists; q++) {
-    const int t = q / lists_h, hq0 = m * all + (q % lists_h) * heads;
-    const int32_t* list = p.ids + (p.ids_per_head ? (((int64_t)b * p.T + t) * p.n_kv + hq0 / a.G) * p.W
-                                                  : ((int64_t)b * p.T + t) * p.W);
-    const float* sc = a.sc + (((int64_t)b * p.T + t) * p.Hq + hq0) * a.sc_ld;
-    for (int r0 = 0; r0 < heads; r0 += kRowsAt) {
-      const int n = min(kRowsAt, heads - r0);
-      const int base = once ? q * heads : 0;  // of the list's rows in s
-      for (int64_t w0 = first; w0 - threadIdx.x < p.W; w0 += step * E) {
-        int id[E];
+  const int held = min(heads, kRowsAt);                // rows of a list at a time
+  const int many = min(lists, kRowsAt / held);         // lists at a time
+  const int chunks = (int)((p.W + kThreads - 1) / kThreads);
+  for (int q0 = 0; q0 < lists; q0 += many)
+    for (int r0 = 0; r0 < heads; r0 += held) {
+      const int nl = min(many, lists - q0), nh = min(held, heads - r0), n = nl * nh;
+      const int64_t items = (int64_t)nl * chunks;
+      __syncthreads();
+      set_rows(a, s, b, 0, m * all, all, q0 * heads + r0, n);
+      bool ready = false;
+      for (int64_t x0 = block % per; x0 < items; x0 += per * E) {
+        int id[E], list[E];  // list: counted from q0
+        const float* sc[E];
         float add[E] = {};
 #pragma unroll
-        for (int e = 0; e < E; e++) id[e] = w0 + e * step < p.W ? list[w0 + e * step] : -1;
+        for (int e = 0; e < E; e++) {
+          const int64_t x = x0 + e * per;
+          list[e] = (int)(x / chunks);
+          const int64_t w = (x - (int64_t)list[e] * chunks) * kThreads + threadIdx.x;
+          const int t = (q0 + list[e]) / lists_h, hq = m * all + (q0 + list[e]) % lists_h * heads;
+          const bool live = x < items && w < p.W;
+          const int64_t bt = (int64_t)b * p.T + t;
+          sc[e] = a.sc + (bt * p.Hq + hq + r0) * a.sc_ld + w;
+          id[e] = live ? p.ids[(p.ids_per_head ? bt * p.n_kv + hq / a.G : bt) * p.W + w] : -1;
+        }
         grid_wait();
-        for (int i0 = 0; i0 < n; i0 += kBatch) {
+        for (int i0 = 0; i0 < nh; i0 += kBatch) {
           float y[kBatch][E];
 #pragma unroll
           for (int u = 0; u < kBatch; u++)
 #pragma unroll
-            for (int e = 0; e < E; e++)
-              y[u][e] = i0 + u < n && w0 + e * step < p.W ? sc[(r0 + i0 + u) * a.sc_ld + w0 + e * step] : 0.f;
-          if (w0 == first && i0 == 0) {
-            __syncthreads();  // the previous list's additions are done
-            if (!once) set_rows(a, s, b, t, hq0, heads, r0, n);
-            if (!once || q == 0) load_norms(a, s, once ? lists * heads : n);
-          }
+            for (int e = 0; e < E; e++) y[u][e] = i0 + u < nh && id[e] >= 0 ? sc[e][(i0 + u) * a.sc_ld] : 0.f;
+          if (!ready) load_norms(a, s, n);
+          ready = true;
 #pragma unroll
           for (int u = 0; u < kBatch; u++)
-            if (i0 + u < n) {
-              const float z = s.lse2[base + i0 + u];
-              const int lim = s.lim[base + i0 + u];
+            if (i0 + u < nh)
 #pragma unroll
-              for (int e = 0; e < E; e++)
-                if (id[e] < lim) add[e] += attn_ex2(y[u][e] - z);
-            }
+              for (int e = 0; e < E; e++) {
+                const int i = (x0 + e * per < items ? list[e] : 0) * nh + i0 + u;
+                if (id[e] < s.lim[i]) add[e] += attn_ex2(y[u][e] - s.lse2[i]);
+              }
         }
+        if (lists > 1) __syncthreads();  // the additions of the lists before are done
 #pragma unroll
-        for (int e = 0; e < E; e++)
+        for (int e = 0; e < E; e++) {
+          if (e > 0 && list[e] != list[e - 1] && x0 + e * per < items) __syncthreads();
           if (id[e] >= 0 && id[e] < s.longest) atomicAdd(mass + id[e], add[e]);
+        }
       }
     }
-  }
+  grid_wait();
 }
 
 // MASS: 0 every slot, else the entries that a thread of the listed form takes.
 template <int D, bool BF16, int MASS>
 __global__ void __launch_bounds__(kThreads, MASS == 4 ? 3 : 4)
-    attn_finish_kernel(const __grid_constant__ AttnArgs a, int64_t join_blocks, int64_t per, int row_groups) {
+    attn_finish_kernel(const __grid_constant__ AttnArgs a, int64_t join_blocks, int share, int64_t per, int row_groups) {
   if (blockIdx.x < join_blocks) {
     grid_wait();
-    join_rows<D, BF16>(a);
+    join_rows<D, BF16>(a, share);
   } else if constexpr (MASS == 0) {
     mass_dense(a, blockIdx.x - join_blocks, (int)per, row_groups);
   } else {
@@ -346,7 +381,10 @@ template <int D, bool BF16>
 cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
   const attn_problem& p = a.p;
   const int64_t rows = (int64_t)p.B * p.T * p.Hq;
-  const int64_t join = (rows + kWarps - 1) / kWarps;
+  // a warp for each 16 pieces of a row
+  const int parts = a.parts_prefix + a.parts_private;
+  const int share = parts <= 16 ? 1 : parts <= 32 ? 2 : parts <= 64 ? 4 : 8;
+  const int64_t join = (rows * share + kWarps - 1) / kWarps;
   // a slot's rows are spread over up to four threads where there are many
   const int mass_rows = p.Hq / a.mass_heads * p.T;
   const int groups = mass_rows >= 32 ? 4 : mass_rows >= 16 ? 2 : 1;
@@ -357,8 +395,8 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
     per = std::min((p.S + kThreads / groups * kSlots - 1) / (kThreads / groups * kSlots),
                    std::max<int64_t>(1, (4 * sm_count() + bms - 1) / bms));  // four blocks fit an SM
     if (p.ids) {
-      // lists that share slots follow one another in a block, four entries of
-      // up to eight rows at a time; other lists are spread over blocks by entry
+      // lists that share slots are one block's; another list's entries are spread
+      // over blocks
       const bool one = p.T == 1 && !(p.ids_per_head && a.mass_heads == 1 && p.n_kv > 1);
       per = one ? (p.W + kThreads - 1) / kThreads : 1;
       kern = one && p.Hq / a.mass_heads > 8 ? attn_finish_kernel<D, BF16, 1> : attn_finish_kernel<D, BF16, 4>;
@@ -366,7 +404,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
   }
   const int64_t blocks = join + (int64_t)p.B * a.mass_heads * per;
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
-  return launch_early(kern, dim3((unsigned)blocks), kThreads, 0, st, a, join, per, groups);
+  return launch_early(kern, dim3((unsigned)blocks), kThreads, 0, st, a, join, share, per, groups);
 }
 
 }  // namespace
