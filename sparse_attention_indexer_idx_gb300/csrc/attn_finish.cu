@@ -123,7 +123,7 @@ __device__ void join_rows(const AttnArgs& a, int share) {
 // What a mass block needs of a row: its log2 normaliser, how many private slots
 // it sees, and its number.
 struct MassRows {
-  float lse2[kRowsAt];
+  float lse2[kRowsAt];    // +inf for a row that sees no private slot
   int lim[kRowsAt];
   int row[kRowsAt];       // (b*T + t)*Hq + hq
   int longest, shortest;  // of lim
@@ -159,10 +159,33 @@ __device__ __forceinline__ void set_rows(const AttnArgs& a, MassRows& s, int b, 
 }
 
 // The normalisers of the n rows.  A warp takes four rows at a time, eight lanes
-// to a row's pieces.
+// to a row's pieces, or sixteen rows where eight lanes hold all of them.
 __device__ __forceinline__ void load_norms(const AttnArgs& a, MassRows& s, int n) {
   const int parts = a.parts_prefix + a.parts_private;
   const int lane = threadIdx.x & 31, sub = lane & 7;
+  if (parts <= 8) {
+    for (int i0 = (threadIdx.x >> 5) * 4; i0 < n; i0 += kWarps * 16) {
+      float2 x[4];
+#pragma unroll
+      for (int u = 0; u < 4; u++) {
+        const int i = i0 + u * kWarps * 4 + (lane >> 3);
+        x[u] = i < n && sub < parts ? a.pml[(int64_t)s.row[i] * parts + sub] : make_float2(-INFINITY, 0.f);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; u++) {
+        const int i = i0 + u * kWarps * 4 + (lane >> 3);
+        float m = x[u].y > 0.f ? x[u].x : -INFINITY;
+#pragma unroll
+        for (int d = 1; d < 8; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        float l = x[u].y > 0.f ? x[u].y * attn_ex2(x[u].x - m) : 0.f;
+#pragma unroll
+        for (int d = 1; d < 8; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+        if (i < n && sub == 0) s.lse2[i] = s.lim[i] > 0 ? m + log2f(l) : INFINITY;
+      }
+    }
+    __syncthreads();
+    return;
+  }
   for (int i = (threadIdx.x >> 5) * 4 + (lane >> 3); i < ((n + 3) & ~3); i += kWarps * 4) {
     const bool live = i < n;
     const float2* ml = a.pml + (int64_t)s.row[live ? i : 0] * parts;
@@ -191,7 +214,7 @@ __device__ __forceinline__ void load_norms(const AttnArgs& a, MassRows& s, int n
     l = m == -INFINITY ? 0.f : l * attn_ex2(top - m);
 #pragma unroll
     for (int d = 1; d < 8; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-    if (live && sub == 0) s.lse2[i] = m + log2f(l);
+    if (live && sub == 0) s.lse2[i] = s.lim[i] > 0 ? m + log2f(l) : INFINITY;
   }
   __syncthreads();
 }
@@ -293,9 +316,9 @@ __device__ __forceinline__ void mass_dense(const AttnArgs& a, int64_t block, int
 // Mass of listed slots.  One list holds a slot at most once, so its threads add
 // to different slots; lists that can share a slot (another token's, or another
 // KV head's when all heads share the mass) are added one after the other by one
-// block.  A thread takes an entry of each of E chunks of kThreads entries, of
-// one list or of several, and several rows of each, at a time: the chunks' ids
-// and scores are loaded together, only the additions follow the lists' order.
+// block.  The lists' entries form one line; a thread takes E of them, and several
+// rows of each, at a time: ids and scores of whatever lists they belong to are
+// loaded together, only the additions follow the lists' order.
 template <int E>
 __device__ __forceinline__ void mass_listed(const AttnArgs& a, int64_t block, int64_t per) {
   __shared__ MassRows s;
@@ -309,29 +332,34 @@ __device__ __forceinline__ void mass_listed(const AttnArgs& a, int64_t block, in
   const int heads = all / lists_h;      // of these, the ones that read one list
   float* mass = a.mass + bm * p.S;
   // rows (t, query head) of the mass head: list q has rows q * heads ..
-  const int held = min(heads, kRowsAt);                // rows of a list at a time
-  const int many = min(lists, kRowsAt / held);         // lists at a time
-  const int chunks = (int)((p.W + kThreads - 1) / kThreads);
+  const int held = min(heads, kRowsAt);            // rows of a list at a time
+  const int many = min(lists, kRowsAt / held);     // lists at a time
+  const uint32_t W = ((uint32_t)p.W + 31) & ~31u;  // below 2^31; a warp's entries are of one list
   for (int q0 = 0; q0 < lists; q0 += many)
     for (int r0 = 0; r0 < heads; r0 += held) {
       const int nl = min(many, lists - q0), nh = min(held, heads - r0), n = nl * nh;
-      const int64_t items = (int64_t)nl * chunks;
       __syncthreads();
       set_rows(a, s, b, 0, m * all, all, q0 * heads + r0, n);
+      const int64_t line = nl * (int64_t)W;
       bool ready = false;
-      for (int64_t x0 = block % per; x0 < items; x0 += per * E) {
-        int id[E], list[E];  // list: counted from q0
+      for (int64_t x0 = block % per * kThreads; x0 < line; x0 += per * kThreads * E) {
+        // the round's first entry: entry w0 of list l0 (counted from q0)
+        const int l0 = lists > 1 ? (int)(x0 / W) : 0;
+        const uint32_t w0 = (uint32_t)(x0 - (int64_t)l0 * W);
+        int id[E], list[E];
         const float* sc[E];
         float add[E] = {};
 #pragma unroll
         for (int e = 0; e < E; e++) {
-          const int64_t x = x0 + e * per;
-          list[e] = (int)(x / chunks);
-          const int64_t w = (x - (int64_t)list[e] * chunks) * kThreads + threadIdx.x;
-          const int t = (q0 + list[e]) / lists_h, hq = m * all + (q0 + list[e]) % lists_h * heads;
-          const bool live = x < items && w < p.W;
+          const uint32_t off = __shfl_sync(0xffffffffu, (uint32_t)(e * per) * kThreads + threadIdx.x, 0);
+          const uint32_t d = lists > 1 ? (w0 + off) / W : 0;
+          const uint32_t w = w0 + off - d * W + (threadIdx.x & 31);
+          const bool live = l0 + (int)d < nl && w < p.W;
+          const int q = q0 + min(l0 + (int)d, nl - 1);
+          const int t = q / lists_h, hq = m * all + (q - t * lists_h) * heads;
           const int64_t bt = (int64_t)b * p.T + t;
-          sc[e] = a.sc + (bt * p.Hq + hq + r0) * a.sc_ld + w;
+          list[e] = q - q0;
+          sc[e] = a.sc + (bt * p.Hq + hq + r0) * a.sc_ld + (live ? w : 0);
           id[e] = live ? p.ids[(p.ids_per_head ? bt * p.n_kv + hq / a.G : bt) * p.W + w] : -1;
         }
         grid_wait();
@@ -340,23 +368,28 @@ __device__ __forceinline__ void mass_listed(const AttnArgs& a, int64_t block, in
 #pragma unroll
           for (int u = 0; u < kBatch; u++)
 #pragma unroll
-            for (int e = 0; e < E; e++) y[u][e] = i0 + u < nh && id[e] >= 0 ? sc[e][(i0 + u) * a.sc_ld] : 0.f;
+            for (int e = 0; e < E; e++) y[u][e] = i0 + u < nh ? sc[e][(i0 + u) * a.sc_ld] : 0.f;
           if (!ready) load_norms(a, s, n);
           ready = true;
+          // Scores of entries that a row does not see are -inf; a row that sees
+          // nothing has no scores, and a normaliser of +inf (fminf: so that
+          // whatever its memory holds becomes 0).
 #pragma unroll
           for (int u = 0; u < kBatch; u++)
             if (i0 + u < nh)
 #pragma unroll
               for (int e = 0; e < E; e++) {
-                const int i = (x0 + e * per < items ? list[e] : 0) * nh + i0 + u;
-                if (id[e] < s.lim[i]) add[e] += attn_ex2(y[u][e] - s.lse2[i]);
+                const int i = list[e] * nh + i0 + u;
+                add[e] += attn_ex2(fminf(y[u][e], 3e38f) - s.lse2[i]);
               }
         }
-        if (lists > 1) __syncthreads();  // the additions of the lists before are done
+        // with several lists (then per is 1) those of this round in turn
+        const int l1 = lists > 1 ? min(nl - 1, l0 + (int)((w0 + kThreads * E - 1) / W)) : l0;
+        for (int l = l0; l <= l1; l++) {
+          if (lists > 1) __syncthreads();  // the additions of the list before are done
 #pragma unroll
-        for (int e = 0; e < E; e++) {
-          if (e > 0 && list[e] != list[e - 1] && x0 + e * per < items) __syncthreads();
-          if (id[e] >= 0 && id[e] < s.longest) atomicAdd(mass + id[e], add[e]);
+          for (int e = 0; e < E; e++)
+            if (list[e] == l && id[e] >= 0 && id[e] < s.longest) atomicAdd(mass + id[e], add[e]);
         }
       }
     }
@@ -385,15 +418,18 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
   const int parts = a.parts_prefix + a.parts_private;
   const int share = parts <= 16 ? 1 : parts <= 32 ? 2 : parts <= 64 ? 4 : 8;
   const int64_t join = (rows * share + kWarps - 1) / kWarps;
-  // a slot's rows are spread over up to four threads where there are many
+  // A slot's rows are spread over up to four threads where there are many, and
+  // over up to 32 while the slots are too few to give every SM a block (7 rows of
+  // 170 slots under 256 rows: 27 us with four threads).
   const int mass_rows = p.Hq / a.mass_heads * p.T;
-  const int groups = mass_rows >= 32 ? 4 : mass_rows >= 16 ? 2 : 1;
+  int groups = mass_rows >= 32 ? 4 : mass_rows >= 16 ? 2 : 1;
+  auto mass_blocks = [&] { return (p.S + kThreads / groups * kSlots - 1) / (kThreads / groups * kSlots); };
+  while (groups < 32 && mass_rows >= 16 * groups && (int64_t)p.B * a.mass_heads * mass_blocks() < sm_count()) groups *= 2;
   auto kern = attn_finish_kernel<D, BF16, 0>;
   int64_t per = 0;  // mass blocks of one (b, mass head)
   if (a.mass && a.parts_private) {
     const int64_t bms = (int64_t)p.B * a.mass_heads;
-    per = std::min((p.S + kThreads / groups * kSlots - 1) / (kThreads / groups * kSlots),
-                   std::max<int64_t>(1, (4 * sm_count() + bms - 1) / bms));  // four blocks fit an SM
+    per = std::min(mass_blocks(), std::max<int64_t>(1, (4 * sm_count() + bms - 1) / bms));  // four blocks fit an SM
     if (p.ids) {
       // lists that share slots are one block's; another list's entries are spread
       // over blocks
