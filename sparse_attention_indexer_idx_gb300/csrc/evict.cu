@@ -5,14 +5,23 @@
 // spread over a cluster of 1 to 8 blocks; each reads its slice of masses and
 // positions once and keeps the slice's 32-bit ranking keys in shared memory, so
 // the three digit passes (11, 11, 10 bits) of the search for the n_keep-th key
-// run on chip: per pass the blocks exchange a histogram through distributed
-// shared memory.  What stays is then a bitmap; the rows behind the new length
-// that stay ("late") and the freed slots before it ("holes") are ranked by
-// warp-wide prefix counts and paired, late row i with hole i.  Bound: 8 bytes
-// read per slot, 12 written per kept slot.
+// run on chip: per pass the blocks look up the counts of 64 groups of bins, then
+// of one group's bins, in one another's shared memory.  What stays is then a
+// bitmap; the rows behind the new length that stay ("late") and the freed slots
+// before it ("holes") are ranked by warp-wide prefix counts and paired, late row
+// i with hole i.
+//
+// The bytes (8 read per slot, 12 written per kept slot) are little; what bounds
+// it is the chain of steps that wait for one another: loads, three passes of two
+// barriers each, counts, late rows, new slots.  8 rows of 1,040 slots take 6.6
+// us, 512 rows of 4,160 (a block each, 3.4 to an SM) 18 us, 96 rows of 10,007
+// (two blocks each) 18.5 us, 4 rows of 131,072 (eight blocks each) 19 us.
 //
 // evict_move_kernel copies the rows of the planes: late rows and holes are
-// disjoint, so it needs no order.  Bound: each moved row read and written once.
+// disjoint, so it needs no order.  Bound by each moved row read and written
+// once, at rows of 128 or 256 bytes spread over a cache: 55,000 slots of 8
+// heads' keys and values and an index key, 256 bytes each (480 MB both ways),
+// take 76 us, 6.3 TB/s.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -39,12 +48,10 @@ struct EvictArgs {
   bool vec4;  // rows of mass and pos start on 16 bytes
 };
 
-template <bool ONE>
 struct SelShared {
-  alignas(16) uint32_t hist[2][kBins];  // read several bins at a time
-  alignas(16) uint32_t sums[ONE ? 4 : kBins];  // the cluster's histogram
+  alignas(16) uint32_t hist[2][kBins];        // read several bins at a time
+  alignas(16) uint32_t coarse[2][kBins / 32];  // sums of 32 bins
   uint32_t wcount[32];
-  uint32_t scan[32];
   uint32_t found_bin, found_above, found_count;
   uint32_t ties, late, holes;  // this block's counts, read by the cluster
 };
@@ -99,17 +106,19 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_select_kernel(const __gri
   extern __shared__ __align__(16) uint32_t keys[];
   uint32_t* bitmap = keys + slice_max;
   uint16_t* rank = reinterpret_cast<uint16_t*>(bitmap + slice_max / 32);
-  __shared__ SelShared<ONE> sh;
+  __shared__ SelShared sh;
   grid_wait();
   grid_let_next_start();
   const RowGroup<ONE> cl;
   const evict_problem& p = a.p;
   const int C = cl.blocks(), c = cl.rank();
-  const int64_t row = blockIdx.x / C;
-  const int b = (int)(row / p.mass_heads);
+  const int64_t row = blockIdx.x / (unsigned)C;
+  const int b = (int)((unsigned)row / (unsigned)p.mass_heads);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   int n = p.len[row];
+  const int cur = p.cur ? p.cur[b] : 0;
+  for (int i = tid; i < kBins; i += NT) sh.hist[0][i] = sh.hist[1][i] = 0;
   if (n < 0 || n > p.S) {
     if (tid == 0) atomicOr(&g_device_error, DEVERR_BAD_ROW);
     n = 0;
@@ -130,9 +139,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_select_kernel(const __gri
   const int words = (cnt + 31) >> 5;
 
   if (trim) {
-    for (int i = tid; i < kBins; i += NT) sh.hist[0][i] = sh.hist[1][i] = 0;
     // positions from here on are protected
-    const int recent = (int)max((int64_t)INT32_MIN, (p.cur ? p.cur[b] : n) - (int64_t)p.n_last);
+    const int recent = (int)max((int64_t)INT32_MIN, (p.cur ? cur : n) - (int64_t)p.n_last);
     __syncthreads();
     auto take = [&](int i, float x, int at) {
       const uint32_t k = rank_key(x, at < p.n_first || at >= recent);
@@ -205,54 +213,56 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_select_kernel(const __gri
         }
         if (tid < (cnt & 3)) look(keys[(cnt & ~3) + tid]);
       }
-      if (ONE) {
-        __syncthreads();
-      } else {
-        // each block adds up its share of the bins and gives the sums to all
-        cl.sync();
-        const int share = kBins / C;
-        for (int i = c * share + tid; i < (c + 1) * share; i += NT) {
-          uint32_t sum = 0;
-          for (int r = 0; r < C; r++) sum += cl.at(hist, r)[i];
-          for (int r = 0; r < C; r++) cl.at(sh.sums, r)[i] = sum;
-        }
-        cl.sync();
-        hist = sh.sums;
-      }
-      // a few bins a thread, largest bin first
-      constexpr int V = kBins / NT;  // 2 to 8
-      uint32_t v[V], mine = 0;
-      const int b0 = kBins - V * (tid + 1);
+      __syncthreads();
+      // Sums of 32 bins; then one warp of every block finds the group with the
+      // need-th key among all blocks' sums, and its bin among the group's 32 (the
+      // whole histograms added up in shares took 2 us longer for blocks of 5,000).
+      constexpr int V = kBins / NT;  // bins of a thread: 2 to 8
+      uint32_t sum = 0;
 #pragma unroll
       for (int j = 0; j < V / 2; j++) {
-        const uint2 x = reinterpret_cast<const uint2*>(hist + b0)[j];
-        v[2 * j] = x.x;
-        v[2 * j + 1] = x.y;
+        const uint2 x = reinterpret_cast<const uint2*>(hist + V * tid)[j];
+        sum += x.x + x.y;
       }
 #pragma unroll
-      for (int j = 0; j < V; j++) mine += v[j];
-      uint32_t incl = mine;
+      for (int d = 1; d < 32 / V; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      if (tid % (32 / V) == 0) sh.coarse[pass & 1][tid * V / 32] = sum;
+      cl.sync();
+      if (warp == 0) {
+        auto before = [&](uint32_t x) {  // sum over the lanes before this one
+          uint32_t incl = x;
 #pragma unroll
-      for (int s = 1; s < 32; s <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, incl, s);
-        if (lane >= s) incl += y;
-      }
-      if (lane == 31) sh.scan[warp] = incl;
-      __syncthreads();
-      uint32_t all;
-      uint32_t above = warps_before(sh.scan, W, warp, &all) + incl - mine;
-      if (above < need && need <= above + mine) {
-#pragma unroll
-        for (int j = V - 1; j >= 0; j--) {
-          if (above < need && need <= above + v[j]) {
-            sh.found_bin = b0 + j;
-            sh.found_above = above;
-            sh.found_count = v[j];
+          for (int s = 1; s < 32; s <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, incl, s);
+            if (lane >= s) incl += y;
           }
-          above += v[j];
+          return incl - x;
+        };
+        uint32_t hi = 0, lo = 0;  // groups 63 - 2 lane and 62 - 2 lane: the largest bins first
+#pragma unroll
+        for (int r = 0; r < (ONE ? 1 : kMaxCluster); r++)
+          if (r < C) {
+            const uint2 x = reinterpret_cast<const uint2*>(cl.at(sh.coarse[pass & 1], r))[31 - lane];
+            lo += x.x;
+            hi += x.y;
+          }
+        uint32_t above = before(hi + lo);
+        const bool upper = need <= above + hi;
+        const int at = __ffs(__ballot_sync(0xffffffffu, above < need && need <= above + hi + lo)) - 1;
+        const int g = __shfl_sync(0xffffffffu, upper ? 63 - 2 * lane : 62 - 2 * lane, at);
+        above = __shfl_sync(0xffffffffu, upper ? above : above + hi, at);
+        uint32_t v = 0;
+#pragma unroll
+        for (int r = 0; r < (ONE ? 1 : kMaxCluster); r++)
+          if (r < C) v += cl.at(hist, r)[g * 32 + 31 - lane];
+        above += before(v);
+        if (above < need && need <= above + v) {
+          sh.found_bin = g * 32 + 31 - lane;
+          sh.found_above = above;
+          sh.found_count = v;
         }
       }
-      // every block has read hist[0] before the second pass's barriers
+      // every block has read hist[0] before the second pass's cluster barrier
       if (pass == 1)
         for (int i = tid; i < kBins; i += NT) sh.hist[0][i] = 0;
       __syncthreads();
@@ -363,6 +373,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_select_kernel(const __gri
   // where each new slot comes from: words of 32 new slots in turn over the
   // warps of the whole cluster
   uint32_t holes_of = 0, late_of = 0;  // lane r: holes and late rows of the blocks before block r
+  uint32_t late_before[kMaxCluster] = {};
   if (trim && !ONE) {
     uint32_t h = lane < C ? *cl.at(&sh.holes, lane) : 0;
     uint32_t l = lane < C ? *cl.at(&sh.late, lane) : 0;
@@ -378,32 +389,41 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_select_kernel(const __gri
     }
     holes_of -= h;
     late_of -= l;
+#pragma unroll
+    for (int x = 1; x < kMaxCluster; x++) late_before[x] = x < C ? __shfl_sync(0xffffffffu, late_of, x) : ~0u;
   }
   const int new_words = (nk + 31) >> 5, stride = C * W;
   constexpr int F = 8;
   for (int v0 = c * W + warp; v0 < new_words; v0 += stride * F) {
     int from[F], slot[F];
+    // lane u: the holes of word u, and how many come before them in the row
+    uint32_t m_l = 0, nth_l = 0;
+    if (trim) {
+      const int v = min(v0 + (lane % F) * stride, new_words - 1);
+      const int q = ONE ? 0 : (int)((uint32_t)(v * 32) / (uint32_t)slice), w = v - q * (slice >> 5);  // its block
+      m_l = ~cl.at(bitmap, q)[w] & low_bits(nk - v * 32);
+      nth_l = (ONE ? 0 : __shfl_sync(0xffffffffu, holes_of, q)) + cl.at(rank, q)[w];
+    }
 #pragma unroll
     for (int u = 0; u < F; u++) {
       const int v = v0 + u * stride;
       const int s = v * 32 + lane;
       slot[u] = v < new_words && s < nk ? s : -1;
       from[u] = s;
-      if (trim && v < new_words) {
-        const int q = ONE ? 0 : v * 32 / slice, w = v - q * (slice >> 5);  // the block that has this word
-        const unsigned m = ~cl.at(bitmap, q)[w] & low_bits(nk - v * 32);
-        if (m) {
-          const uint32_t r = (ONE ? 0 : __shfl_sync(0xffffffffu, holes_of, q)) + cl.at(rank, q)[w] +
-                             __popc(m & ((1u << lane) - 1));
-          int z = 0;  // the block that has late row r
-          uint32_t first = 0;
-          if (!ONE) {
+      const uint32_t m = __shfl_sync(0xffffffffu, m_l, u);
+      const uint32_t r = __shfl_sync(0xffffffffu, nth_l, u) + __popc(m & ((1u << lane) - 1));
+      if (slot[u] >= 0 && ((m >> lane) & 1)) {
+        int z = 0;  // the block that has late row r
+        uint32_t first = 0;
+        if (!ONE) {
 #pragma unroll
-            for (int x = 1; x < kMaxCluster; x++) z += x < C && r >= __shfl_sync(0xffffffffu, late_of, x);
-            first = __shfl_sync(0xffffffffu, late_of, z);
-          }
-          if ((m >> lane) & 1) from[u] = (int)*cl.at(keys + (r - first), z);
+          for (int x = 1; x < kMaxCluster; x++)
+            if (r >= late_before[x]) {
+              z = x;
+              first = late_before[x];
+            }
         }
+        from[u] = (int)*cl.at(keys + (r - first), z);
       }
     }
     int ps[F];
