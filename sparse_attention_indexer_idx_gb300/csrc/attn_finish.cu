@@ -173,6 +173,7 @@ __device__ __forceinline__ void load_norms(const AttnArgs& a, MassRows& s, int n
       }
 #pragma unroll
       for (int u = 0; u < 4; u++) {
+        if (i0 + u * kWarps * 4 >= n) break;
         const int i = i0 + u * kWarps * 4 + (lane >> 3);
         float m = x[u].y > 0.f ? x[u].x : -INFINITY;
 #pragma unroll
@@ -326,6 +327,7 @@ __device__ __forceinline__ void mass_listed(const AttnArgs& a, int64_t block, in
   const attn_problem& p = a.p;
   const int lists_h = p.ids_per_head && a.mass_heads == 1 ? p.n_kv : 1;
   const int lists = p.T * lists_h;
+  const int lane = threadIdx.x & 31;
   const int64_t bm = block / per;
   const int b = (int)(bm / a.mass_heads), m = (int)(bm % a.mass_heads);
   const int all = p.Hq / a.mass_heads;  // query heads of the mass head
@@ -349,18 +351,27 @@ __device__ __forceinline__ void mass_listed(const AttnArgs& a, int64_t block, in
         int id[E], list[E];
         const float* sc[E];
         float add[E] = {};
+        // lane e: what the warp's entries of chunk e have in common
+        int list_l, sc_l, ids_l;
+        uint32_t w_l;
+        {
+          const uint32_t off = (uint32_t)(lane % E * per) * kThreads + (threadIdx.x & ~31u);
+          const uint32_t d = lists > 1 ? (w0 + off) / W : 0;
+          list_l = min(l0 + (int)d, nl - 1);
+          w_l = l0 + (int)d < nl ? w0 + off - d * W : W;  // W: none
+          const int q = q0 + list_l;
+          const int t = q / lists_h, hq = m * all + (q - t * lists_h) * heads, bt = b * p.T + t;
+          sc_l = bt * p.Hq + hq + r0;
+          ids_l = p.ids_per_head ? bt * p.n_kv + hq / a.G : bt;
+        }
 #pragma unroll
         for (int e = 0; e < E; e++) {
-          const uint32_t off = __shfl_sync(0xffffffffu, (uint32_t)(e * per) * kThreads + threadIdx.x, 0);
-          const uint32_t d = lists > 1 ? (w0 + off) / W : 0;
-          const uint32_t w = w0 + off - d * W + (threadIdx.x & 31);
-          const bool live = l0 + (int)d < nl && w < p.W;
-          const int q = q0 + min(l0 + (int)d, nl - 1);
-          const int t = q / lists_h, hq = m * all + (q - t * lists_h) * heads;
-          const int64_t bt = (int64_t)b * p.T + t;
-          list[e] = q - q0;
-          sc[e] = a.sc + (bt * p.Hq + hq + r0) * a.sc_ld + (live ? w : 0);
-          id[e] = live ? p.ids[(p.ids_per_head ? bt * p.n_kv + hq / a.G : bt) * p.W + w] : -1;
+          const uint32_t w = __shfl_sync(0xffffffffu, w_l, e) + lane;
+          const int64_t sc_row = __shfl_sync(0xffffffffu, sc_l, e), ids_row = __shfl_sync(0xffffffffu, ids_l, e);
+          const bool live = w < p.W;
+          list[e] = __shfl_sync(0xffffffffu, list_l, e);
+          sc[e] = a.sc + sc_row * a.sc_ld + (live ? w : 0);
+          id[e] = live ? p.ids[ids_row * p.W + w] : -1;
         }
         grid_wait();
         for (int i0 = 0; i0 < nh; i0 += kBatch) {
@@ -414,9 +425,12 @@ template <int D, bool BF16>
 cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
   const attn_problem& p = a.p;
   const int64_t rows = (int64_t)p.B * p.T * p.Hq;
-  // a warp for each 16 pieces of a row
+  // A warp for a row; where the rows leave warps free, one for each 16 pieces of
+  // it (2 requests of 28 heads behind 45,840 tokens, 456 pieces a row: 74 us for
+  // the call with one, 39 with eight).
   const int parts = a.parts_prefix + a.parts_private;
-  const int share = parts <= 16 ? 1 : parts <= 32 ? 2 : parts <= 64 ? 4 : 8;
+  int share = 1;
+  while (share < kWarps && parts > 16 * share && rows * share < 8 * sm_count()) share *= 2;
   const int64_t join = (rows * share + kWarps - 1) / kWarps;
   // A slot's rows are spread over up to four threads where there are many, and
   // over up to 32 while the slots are too few to give every SM a block (7 rows of
