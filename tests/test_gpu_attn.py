@@ -270,6 +270,23 @@ def _prefix_only(B, seed, rows, Hq, n_kv, P, D, dtype="bf16", prefix_len=None, l
     return t, out, lse, p, ws
 
 
+# many rows of a KV head over long caches: more than 48 MB of scores
+LONG = [
+    dict(B=2, T=4, Hq=64, n_kv=4, S=26001, lens=[26001, 13], mass=4, D=64, garbage=True),
+    dict(B=2, T=3, Hq=56, n_kv=2, S=40003, P=70, mass=1, per_head_lens=True, garbage=True, dtype="f16", layout="bhsd"),
+    dict(B=4, T=5, Hq=40, n_kv=4, S=16385, lens=[0, 3, 16385, 257], mass=1, D=64, layout="bhsd"),
+]
+
+
+@pytest.mark.parametrize("case", range(len(LONG)))
+def test_masses_of_long_caches_under_many_rows(B, case):
+    t = make(300 + case, **LONG[case])
+    out, lse, mass, p, ws = run(B, t)
+    torch.cuda.synchronize()
+    check(t, out, lse, mass)
+    assert B.device_error() == 0
+
+
 @pytest.mark.parametrize("rows,Hq,n_kv,P,D,dtype,plen", [
     (17, 8, 8, 5000, 128, "bf16", None),       # a part of one row tile
     (64, 4, 2, 40000, 64, "f16", None),        # one row tile, many key tiles
