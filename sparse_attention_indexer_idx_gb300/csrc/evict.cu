@@ -500,26 +500,32 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
   __shared__ int2 list[SLOTS];  // (new slot, slot it comes from)
   __shared__ int count;
   const int64_t chunks = (a.n_keep + SLOTS - 1) / SLOTS;
-  const int64_t row = blockIdx.x / chunks;
-  const int64_t s0 = (blockIdx.x % chunks) * SLOTS + threadIdx.x;
+  const int64_t row = blockIdx.x / (unsigned)chunks;
+  const int64_t s0 = (int64_t)(blockIdx.x % (unsigned)chunks) * SLOTS + threadIdx.x;
   if (threadIdx.x == 0) count = 0;
   __syncthreads();
   grid_wait();
-  int from[SLOTS / kMoveThreads];
+  constexpr int U = SLOTS / kMoveThreads;
+  int from[U];
+  bool some = false;
 #pragma unroll
-  for (int u = 0; u < SLOTS / kMoveThreads; u++) {
+  for (int u = 0; u < U; u++) {
     const int64_t s = s0 + u * kMoveThreads;
     from[u] = s < a.n_keep ? a.src[row * a.n_keep + s] : -1;
   }
 #pragma unroll
-  for (int u = 0; u < SLOTS / kMoveThreads; u++) {
-    const int s = (int)s0 + u * kMoveThreads;
-    const bool moves = from[u] >= 0 && from[u] != s;
-    const unsigned m = __ballot_sync(0xffffffffu, moves);
-    int at = 0;
-    if ((threadIdx.x & 31) == 0 && m) at = atomicAdd(&count, __popc(m));
-    at = __shfl_sync(0xffffffffu, at, 0);
-    if (moves) list[at + __popc(m & ((1u << (threadIdx.x & 31)) - 1))] = make_int2(s, from[u]);
+  for (int u = 0; u < U; u++) some |= from[u] >= 0 && from[u] != (int)s0 + u * kMoveThreads;
+  if (__any_sync(0xffffffffu, some)) {  // few do where a cache is just over its budget
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const int s = (int)s0 + u * kMoveThreads;
+      const bool moves = from[u] >= 0 && from[u] != s;
+      const unsigned m = __ballot_sync(0xffffffffu, moves);
+      int at = 0;
+      if ((threadIdx.x & 31) == 0 && m) at = atomicAdd(&count, __popc(m));
+      at = __shfl_sync(0xffffffffu, at, 0);
+      if (moves) list[at + __popc(m & ((1u << (threadIdx.x & 31)) - 1))] = make_int2(s, from[u]);
+    }
   }
   __syncthreads();
   const int n = count;
