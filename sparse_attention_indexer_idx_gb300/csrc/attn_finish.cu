@@ -1,14 +1,16 @@
 // Attention, last step: the pieces of each row joined, and the attention weight
 // of every private slot added to its mass.
 //
-// Both parts are bound by reading what the pieces left (po, and the private
-// scores: 4 bytes a row and slot).  One launch holds both: blocks 0 ..
-// join_blocks - 1 join rows, a warp each; the others add masses.  A mass block
-// takes its rows' normalisers from the pieces' (m, l) itself, so it need not
-// wait for the join.
-#include <algorithm>
-
+// Both parts read what the pieces left (po, and the private scores: 4 bytes a row
+// and slot).  One launch holds both: blocks 0 .. join_blocks - 1 join rows, a
+// warp or more each; the others add masses.  A mass block takes its rows'
+// normalisers from the pieces' (m, l) itself, so it need not wait for the join.
+// Large calls are bound by those reads and an exponential a score (16 caches of
+// 24,576 slots on average under 64 rows: 100 MB in 28 us), small ones by the
+// chain of loads from the pieces to a block's sums, 6 to 10 us.
 #include "attn.cuh"
+
+#include <algorithm>
 
 namespace idx {
 
@@ -123,7 +125,7 @@ __device__ void join_rows(const AttnArgs& a, int share) {
 // What a mass block needs of a row: its log2 normaliser, how many private slots
 // it sees, and its number.
 struct MassRows {
-  float lse2[kRowsAt];    // +inf for a row that sees no private slot
+  float lse2[kRowsAt];    // +inf for a row that sees no private slot, or nothing
   int lim[kRowsAt];
   int row[kRowsAt];       // (b*T + t)*Hq + hq
   int longest, shortest;  // of lim
@@ -181,7 +183,7 @@ __device__ __forceinline__ void load_norms(const AttnArgs& a, MassRows& s, int n
         float l = x[u].y > 0.f ? x[u].y * attn_ex2(x[u].x - m) : 0.f;
 #pragma unroll
         for (int d = 1; d < 8; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-        if (i < n && sub == 0) s.lse2[i] = s.lim[i] > 0 ? m + log2f(l) : INFINITY;
+        if (i < n && sub == 0) s.lse2[i] = s.lim[i] > 0 && l > 0.f ? m + log2f(l) : INFINITY;
       }
     }
     __syncthreads();
@@ -215,7 +217,7 @@ __device__ __forceinline__ void load_norms(const AttnArgs& a, MassRows& s, int n
     l = m == -INFINITY ? 0.f : l * attn_ex2(top - m);
 #pragma unroll
     for (int d = 1; d < 8; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-    if (live && sub == 0) s.lse2[i] = s.lim[i] > 0 ? m + log2f(l) : INFINITY;
+    if (live && sub == 0) s.lse2[i] = s.lim[i] > 0 && l > 0.f ? m + log2f(l) : INFINITY;
   }
   __syncthreads();
 }
@@ -382,9 +384,10 @@ __device__ __forceinline__ void mass_listed(const AttnArgs& a, int64_t block, in
             for (int e = 0; e < E; e++) y[u][e] = i0 + u < nh ? sc[e][(i0 + u) * a.sc_ld] : 0.f;
           if (!ready) load_norms(a, s, n);
           ready = true;
-          // Scores of entries that a row does not see are -inf; a row that sees
-          // nothing has no scores, and a normaliser of +inf (fminf: so that
-          // whatever its memory holds becomes 0).
+          // Scores of entries that a row does not see are -inf.  A row that sees no
+          // slot has no scores, and one whose list holds none of its slots may see
+          // nothing at all: their normaliser is +inf (fminf: so that whatever the
+          // memory of absent scores holds becomes 0).
 #pragma unroll
           for (int u = 0; u < kBatch; u++)
             if (i0 + u < nh)

@@ -270,6 +270,35 @@ def _prefix_only(B, seed, rows, Hq, n_kv, P, D, dtype="bf16", prefix_len=None, l
     return t, out, lse, p, ws
 
 
+# pieces, lists and slots in unusual numbers
+SHAPES = [
+    dict(B=1, T=1, Hq=4, n_kv=1, P=30011, S=50, mass=1),                              # hundreds of pieces a row
+    dict(B=2, T=1, Hq=28, n_kv=4, P=20000, D=64, prefix_len=[20000, 777], dtype="f16"),
+    dict(B=1, T=3, Hq=8, n_kv=8, S=40000, mass=8, D=64),
+    dict(B=2, T=4, Hq=64, n_kv=16, P=300, S=12, W=8, ids_per_head=True, mass=1, D=64),  # 64 short lists on 12 slots
+    dict(B=2, T=20, Hq=64, n_kv=4, S=500, W=40, ids_per_head=True, mass=1, D=64),     # more rows than are held at once
+    dict(B=2, T=1, Hq=600, n_kv=1, S=900, W=33, mass=1, D=64),                        # of one list
+    dict(B=3, T=2, Hq=8, n_kv=2, S=3000, W=1500, mass=2, lens=[0, 1, 2900]),
+    dict(B=2, T=1, Hq=256, n_kv=16, S=170, mass=1, D=64, lens=[170, 3]),              # many rows on few slots
+    dict(B=1, T=9, Hq=128, n_kv=1, S=37, mass=1, D=64),
+]
+
+
+@pytest.mark.parametrize("case", range(len(SHAPES)))
+def test_pieces_lists_and_slots(B, case):
+    t = make(200 + case, **SHAPES[case])
+    out, lse, mass, p, ws = run(B, t)
+    torch.cuda.synchronize()
+    check(t, out, lse, mass)
+    mass2 = None if mass is None else t["mass"].cuda()
+    out2, lse2 = torch.empty_like(out), torch.empty_like(lse)
+    B.attn_shared(p, out2, lse2, mass2, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+    assert mass is None or torch.equal(mass, mass2)
+    assert B.device_error() == 0
+
+
 # many rows of a KV head over long caches: more than 48 MB of scores
 LONG = [
     dict(B=2, T=4, Hq=64, n_kv=4, S=26001, lens=[26001, 13], mass=4, D=64, garbage=True),
@@ -367,6 +396,53 @@ def test_steep_scores_on_the_tensor_cores(B, rows, Hq, n_kv, P, D, dtype):
         pick = [0, 3, rows // 2, rows - 1]
         few = dict(t, q=t["q"][pick])
         check(few, out[pick], lse[pick], None)
+    assert B.device_error() == 0
+
+
+@pytest.mark.parametrize("P", [0, 500, 9000])
+def test_copies_fills_and_forks_before_a_captured_call(B, P):
+    """What comes right before a call in a graph need not be a kernel, nor one node."""
+    t = make(71, B=20, T=1, Hq=16, n_kv=2, D=128, P=P, S=300, mass=1, lens=[300] * 20)
+    d = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in t.items()}
+    p = B.AttnProblem(d["q"], t["scale"], d["k"], d["v"], d["lens"], d.get("pk"), d.get("pv"))
+    out, lse = torch.empty_like(d["q"]), torch.empty((20, 1, 16), device="cuda")
+    ws = torch.empty(B.attn_shared_workspace_size(p, True), dtype=torch.uint8, device="cuda")
+    lens = torch.full((20, 1), 300, dtype=torch.int32, device="cuda")
+    e = B.EvictProblem(d["mass"], lens, 128, 2, 16, planes=(d["k"], d["v"]))
+    src = torch.empty((20, 1, 128), dtype=torch.int32, device="cuda")
+    start = [x.clone() for x in (d["mass"], d["k"], d["v"])]
+    side = torch.cuda.Stream()
+
+    def step():
+        now = torch.cuda.current_stream()
+        side.wait_stream(now)
+        with torch.cuda.stream(side):
+            d["k"].copy_(start[1])
+        d["v"].copy_(start[2])
+        d["mass"].copy_(start[0])
+        ws.zero_()
+        now.wait_stream(side)
+        B.attn_shared(p, out, lse, d["mass"], ws)
+        src.zero_()
+        B.cache_evict(e, src)
+
+    step()
+    torch.cuda.synchronize()
+    want = [x.clone() for x in (out, lse, d["mass"], src, d["k"], d["v"])]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            step()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for x in (out, lse, d["mass"], src, d["k"], d["v"]):
+            x.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        for x, y in zip((out, lse, d["mass"], src, d["k"], d["v"]), want):
+            assert torch.equal(x, y)
     assert B.device_error() == 0
 
 
