@@ -456,7 +456,10 @@ idx_status block_select_static(const float* index_q, const float* index_k, const
  * Lengths out of range count as 0 and set IDX_DEVERR_BAD_ROW.  Memory of
  * slots that no row of the call sees may hold anything, NaN included; what
  * some row sees is finite.  Workspace: partial results, and with mass the
- * private scores (4 bytes per token, query head and slot or id). */
+ * private scores (4 bytes per token, query head and slot or id).
+ * The first kernel of attn_shared and of cache_evict may be launched while the
+ * one ahead of it on the stream still runs; it waits for that one's end before
+ * it touches memory. */
 typedef struct attn_problem {
   const void* q;
   int32_t dtype;

@@ -52,8 +52,11 @@ PrefixWay prefix_way(const attn_problem& p) {
 // under one; 55 bytes/ns of an SM that streams, caches taken as 0.6 full, their
 // lengths being on the device), and a block takes eight key tiles at least, so
 // that its start and end count little; but where the caches are so short that
-// they need few SMs for a moment, it gets all the others.  One after the other took 337 us for the
-// shared document of 128 requests, side by side 289; 53 and 41 for 32 requests.
+// they need few SMs for a moment, it gets all the others (84 requests with 18
+// listed slots each behind 3,309 tokens: 31 us, with eight key tiles a block 34).
+// One after the other took 337 us for 128 requests with caches of 2,048 slots
+// behind 65,536 tokens, side by side 289; 53 and 41 for 32 requests with 1,024
+// slots behind 8,192.
 AttnTcArgs plan_tc(const AttnArgs& a) {
   const attn_problem& p = a.p;
   AttnTcArgs t{};
@@ -83,9 +86,9 @@ AttnTcArgs plan_tc(const AttnArgs& a) {
 
 // The streaming kernel's groups and the parts of a sequence.  Every SM holds
 // twelve warps of 16 rows or eight of 32 (three or two blocks), and every warp
-// gets one share of the line: cutting it finer cost 1 to 7 percent.  The share of a group depends on the
-// lengths, which only the device knows; the parts allow for lines down to a
-// quarter of the longest.
+// gets one share of the line: cutting it finer cost 1 to 7 percent.  The share of
+// a group depends on the lengths, which only the device knows; the parts allow
+// for lines down to a quarter of the longest.
 StreamLine plan_stream(AttnArgs& a) {
   const attn_problem& p = a.p;
   StreamLine l{};

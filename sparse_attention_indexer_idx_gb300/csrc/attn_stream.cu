@@ -16,7 +16,10 @@
 // pass while the others of the SM stream.  One tile of each of the SM's twelve
 // warps is on its way all the time, 96 KB; refilling each half of a ring slot as
 // soon as it was used, up to twice as much, cost 8 percent (272 against 251 us
-// for 16 caches of 24,576 slots on average, 8 KV heads of 128).
+// for 16 caches of 24,576 slots on average, 8 KV heads of 128: 1.61 GB, 6.4 TB/s).
+// 64 lists of 2,048 ids, 4 KV heads of 128 (268 MB in rows of 256 bytes), take 53
+// us, 5.1 TB/s: a list is one warp's few dozen tiles per head, and each tile's
+// addresses wait for its ids.
 //
 // The products use mma.sync (16 x 8 x 16): a decode row group is 1 to 32 rows,
 // so the tensor work is a few percent of the time the bytes take, and the
