@@ -102,10 +102,16 @@ StreamLine plan_stream(AttnArgs& a) {
   l.seqs = private_keys(p) == 0 ? 0 : p.ids ? p.B * p.T : p.B;
   // A unit is a tile where every share has sixteen of them or more (an even cut
   // matters), else four: a sequence's start takes about the time of four tiles.
+  // Where even units of two find warps for all, and do not make a row's pieces
+  // many, two: a short call waits for its longest share (one request of 200 slots
+  // behind 1,024: 9.4 against 10.6 us).  Beside a prefix under many rows, on the
+  // tensor cores or on a line of its own, it stays four (two: 31 against 26 us).
   const int64_t tile = stream_tile(p.D);
   const int64_t tiles = (way == kLine ? ceil_div(p.P, tile) : 0) + l.seqs * ceil_div(private_keys(p), tile);
   const bool fine = tiles * l.members >= 16 * warps;
-  l.unit_shift = (p.D == 128 ? 4 : 5) + (fine ? 0 : 2);
+  const int64_t pieces = (way == kLine ? ceil_div(p.P, 2 * tile) : 0) + ceil_div(private_keys(p), 2 * tile);
+  const bool two = (way == kNone || way == kLine) && tiles * l.members <= warps && pieces <= 96;
+  l.unit_shift = (p.D == 128 ? 4 : 5) + (fine ? 0 : two ? 1 : 2);
   const int64_t unit = (int64_t)1 << l.unit_shift;
   if (way == kLine) l.prefix_units = (int)ceil_div(p.P, unit);
   if (way == kOwnLine) {

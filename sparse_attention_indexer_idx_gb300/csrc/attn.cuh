@@ -74,7 +74,7 @@ __device__ __forceinline__ float attn_ex2(float x) {
 // The streaming kernel's line of key units and its cut (see attn_stream.cu).
 struct StreamLine {
   bool after;        // the tensor-core kernel comes before: it writes nothing that this one reads
-  int unit_shift;    // a unit is 2^unit_shift keys: a tile, or four
+  int unit_shift;    // a unit is 2^unit_shift keys: a tile, two or four
   int row_tile;      // 16 or 32 rows of a warp
   int members;       // warps of a group: KV heads times row tiles
   int groups;

@@ -2,7 +2,7 @@
 // the private caches of a decode step, and a shared prefix under a small batch.
 //
 // Mapping.  The key sequences (the prefix, then every request's cache or list)
-// form one line of units of one or four key tiles; it is cut evenly over groups
+// form one line of units of one to four key tiles; it is cut evenly over groups
 // of warps, with one warp of a group for each KV head (and tile of up to 32
 // rows).  The heads of a group run side by side, so their rows of a cache, which
 // lie next to one another, are read together, and all groups end together
