@@ -253,46 +253,35 @@ __device__ __forceinline__ void mass_dense(const AttnArgs& a, int64_t block, int
       for (int e = 0; e < kSlots; e++) old[e] = run == 0 && slot + e < s.longest ? from[e] : 0.f;
     };
     float4 y[kBatch];
-    auto fetch = [&](int slot, int i) {  // rows i .. of a thread whose slots all of them see
+    // scores of rows i ..; a row's memory goes on behind its last one for these four
+    auto fetch = [&](int slot, int i) {
 #pragma unroll
       for (int u = 0; u < kBatch; u++)
-        y[u] = *reinterpret_cast<const float4*>(a.sc + (int64_t)s.row[i + u] * a.sc_ld + slot);
+        if (i + u < i1) y[u] = *reinterpret_cast<const float4*>(a.sc + (int64_t)s.row[i + u] * a.sc_ld + slot);
     };
     const int slot0 = first + mine * kSlots;
-    const bool ahead = slot0 + kSlots <= s.shortest && i0 + kBatch <= i1;
     fetch_old(slot0);
     grid_wait();
-    if (ahead) fetch(slot0, i0);
+    if (slot0 < s.longest) fetch(slot0, i0);
     load_norms(a, s, n);
     for (int at = first; at < s.longest; at += per * lanes * kSlots) {
       const int slot = at + mine * kSlots;
       if (at != first) fetch_old(slot);
       float add[kSlots] = {};
-      int i = i0;
-      if (slot + kSlots <= s.shortest) {
-        for (; i + kBatch <= i1; i += kBatch) {
+      const bool all = slot + kSlots <= s.shortest;  // every row sees all four slots
+      if (slot < s.longest)
+        for (int i = i0; i < i1; i += kBatch) {
           if (at != first || i != i0) fetch(slot, i);
 #pragma unroll
-          for (int u = 0; u < kBatch; u++) {
-            const float z = s.lse2[i + u];
-            add[0] += attn_ex2(y[u].x - z);
-            add[1] += attn_ex2(y[u].y - z);
-            add[2] += attn_ex2(y[u].z - z);
-            add[3] += attn_ex2(y[u].w - z);
-          }
-        }
-      }
-      if (slot < s.longest)
-#pragma unroll 4
-        for (; i < i1; i++) {
-          const int left = s.lim[i] - slot;
-          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (left > 0) x = *reinterpret_cast<const float4*>(a.sc + (int64_t)s.row[i] * a.sc_ld + slot);
-          const float z = s.lse2[i];
-          if (left > 0) add[0] += attn_ex2(x.x - z);
-          if (left > 1) add[1] += attn_ex2(x.y - z);
-          if (left > 2) add[2] += attn_ex2(x.z - z);
-          if (left > 3) add[3] += attn_ex2(x.w - z);
+          for (int u = 0; u < kBatch; u++)
+            if (i + u < i1) {
+              const float z = s.lse2[i + u];
+              const int left = all ? kSlots : s.lim[i + u] - slot;  // of the four, those that the row sees
+              add[0] += left > 0 ? attn_ex2(y[u].x - z) : 0.f;
+              add[1] += left > 1 ? attn_ex2(y[u].y - z) : 0.f;
+              add[2] += left > 2 ? attn_ex2(y[u].z - z) : 0.f;
+              add[3] += left > 3 ? attn_ex2(y[u].w - z) : 0.f;
+            }
         }
       if (groups > 1) {
         __syncthreads();
