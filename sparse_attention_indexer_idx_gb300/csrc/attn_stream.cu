@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(32 * kWarps, MT == 1 ? 3 : 2)
   constexpr int NT = 32 * kWarps;
   __shared__ int s_sum[kWarps];
   __shared__ int s_first[NT];
-  if (!line.after) grid_wait();
+  if (!line.after) grid_wait();  // behind the tensor-core kernel, which has waited, the call's inputs are there
   grid_let_next_start();
   const attn_problem& p = a.p;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
