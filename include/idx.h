@@ -449,6 +449,8 @@ idx_status block_select_static(const float* index_q, const float* index_k, const
  *   ids         device [B, T, W] int32, or [B, T, n_kv, W] (ids_per_head), or
  *               NULL (every slot).  Entries outside 0..n(b, t)-1 (-1 is the
  *               padding) are ignored; the others of one list are distinct.
+ *               With W == 0 no slot is selected: any address but NULL, which
+ *               is not read.
  *   out         device [B, T, Hq, D] of the same type; lse device [B, T, Hq]
  *               float32 or NULL (natural logarithm); mass device
  *               [B, mass_heads, S] float32 or NULL.

@@ -561,7 +561,7 @@ class AttnProblem(_Described):
     pk: Optional[torch.Tensor] = None            # [P, n_kv, D] shared prefix
     pv: Optional[torch.Tensor] = None
     prefix_len: Optional[torch.Tensor] = None    # [B] int32
-    ids: Optional[torch.Tensor] = None           # [B, T, W] or [B, T, n_kv, W] int32
+    ids: Optional[torch.Tensor] = None           # [B, T, W] or [B, T, n_kv, W] int32; W == 0 selects no slot
 
     def _shapes(self, c):
         """Shapes of out, lse, and mass with one and with n_kv mass heads."""
@@ -598,9 +598,12 @@ class AttnProblem(_Described):
                 a.prefix_len = _dense(self.prefix_len, "prefix_len", ((B,),), torch.int32)
         if self.ids is not None:
             W = self.ids.shape[-1]
-            a.W = W
-            a.ids = _dense(self.ids, "ids", ((B, T, W), (B, T, n_kv, W)), torch.int32)
-            a.ids_per_head = int(self.ids.dim() == 4)
+            ids = _dense(self.ids, "ids", ((B, T, W), (B, T, n_kv, W)), torch.int32)
+            if W or a.S:  # (an empty list of an empty cache says nothing)
+                # An empty tensor's address is 0, which would say that there is no
+                # list (every slot) instead of one that holds nothing.  With W == 0
+                # nothing is read through it, so any address does: the queries'.
+                a.W, a.ids, a.ids_per_head = W, ids or a.q, int(self.ids.dim() == 4)
         return a
 
 
