@@ -30,7 +30,8 @@
 //
 // Warp roles: warp 0 TMA producer, warp 1 MMA issue, warp 2 TMEM allocation,
 // warps 4..7 and 8..11 the two row tiles.  Waits are bounded as everywhere in
-// the library; on a timeout the roles stop and drain what they issued.
+// the library; on a timeout the roles stop, the four warps of a row tile
+// together, and drain what they issued.
 #include "attn_tc.cuh"
 
 namespace idx {
@@ -106,6 +107,16 @@ __device__ __forceinline__ uint64_t desc_values(uint32_t addr) {
 }
 // Barrier of the four warps of a row tile.
 __device__ __forceinline__ void row_tile_sync(int i) { asm volatile("bar.sync %0, 128;" ::"r"(i + 1) : "memory"); }
+// The same barrier, and whether `ok` holds in all its 128 threads.
+__device__ __forceinline__ bool row_tile_all(int i, bool ok) {
+  uint32_t r;
+  __syncwarp();
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+               : "=r"(r)
+               : "r"((uint32_t)ok), "r"(i + 1)
+               : "memory");
+  return r != 0;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -435,7 +446,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         // An empty row tile: the other one uses both places.  Its barriers are
         // this one's again when the run is over.
         ns1 += n / 2;
-        ok = __all_sync(0xffffffffu, mbar_wait(&o_full[1], no++ & 1, abort_flag));
+        ok = row_tile_all(i, mbar_wait(&o_full[1], no++ & 1, abort_flag));
         continue;
       }
       if (i == 0 && two) ns1 += n;  // the other tile's
@@ -591,8 +602,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         mbar_arrive(&p_ready[place]);
         cnt += 2;
       }
-      ok = ok && mbar_wait(&o_full[i], no++ & 1, abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
+      // A wait that gives up does so in one warp: another's can still succeed a
+      // moment later.  The barriers below count all four warps of the row tile, so
+      // they go on or leave together, by one vote a run that every one of them
+      // reaches, whatever its own waits returned.
+      ok = row_tile_all(i, ok && mbar_wait(&o_full[i], no++ & 1, abort_flag));
       if (!ok) break;
       tc_fence_after();
       if (!two) npv += n;
