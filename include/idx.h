@@ -456,9 +456,13 @@ idx_status block_select_static(const float* index_q, const float* index_k, const
  *               [B, mass_heads, S] float32 or NULL.
  * Base addresses and strides of q, k, v, pk, pv are multiples of 16 bytes.
  * Lengths out of range count as 0 and set IDX_DEVERR_BAD_ROW.  Memory of
- * slots that no row of the call sees may hold anything, NaN included; what
- * some row sees is finite.  Workspace: partial results, and with mass the
- * private scores (4 bytes per token, query head and slot or id).
+ * slots that no row of the call sees may hold anything, NaN included.  A row
+ * that meets a score of NaN or +inf gets NaN in out, in lse and in the masses
+ * of the slots that it sees, the other rows are as without it; a score of -inf
+ * is a weight of zero.  Values (v, pv) that some row sees are finite: one that
+ * is not can also reach rows that do not see it.  Workspace: partial results,
+ * and with mass the private scores (4 bytes per token, query head and slot or
+ * id).
  * The first kernel of attn_shared and of cache_evict may be launched while the
  * one ahead of it on the stream still runs; it waits for that one's end before
  * it touches memory. */

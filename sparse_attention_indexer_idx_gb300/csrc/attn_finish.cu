@@ -8,6 +8,9 @@
 // Large calls are bound by those reads and an exponential a score (16 caches of
 // 24,576 slots on average under 64 rows: 100 MB in 32 us), small ones by the
 // chain of loads from the pieces to a block's sums, 6 to 10 us.
+//
+// A piece is empty where its sum is 0, and only there: a sum that is NaN (a
+// score was) makes the row's output, its lse and its weights NaN.
 #include "attn.cuh"
 
 #include <algorithm>
@@ -39,10 +42,10 @@ __device__ void join_rows(const AttnArgs& a, int share) {
   // lane i holds piece i (of the first 32; the others are read again)
   const float2 none = make_float2(-INFINITY, 0.f);
   const float2 first = lane < parts ? ml[lane] : none;
-  float top = first.y > 0.f ? first.x : -INFINITY;
+  float top = first.y != 0.f ? first.x : -INFINITY;
   for (int i = lane + 32; i < parts; i += 32) {
     const float2 x = ml[i];
-    if (x.y > 0.f) top = fmaxf(top, x.x);
+    if (x.y != 0.f) top = fmaxf(top, x.x);
   }
 #pragma unroll
   for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
@@ -54,7 +57,7 @@ __device__ void join_rows(const AttnArgs& a, int share) {
   for (int e = 0; e < E; e++) acc[e] = 0.f;
   for (int i0 = 0; i0 < parts; i0 += 32) {
     const float2 x = i0 == 0 ? first : i0 + lane < parts ? ml[i0 + lane] : none;
-    const float w = x.y > 0.f ? attn_ex2(x.x - base) : 0.f;
+    const float w = x.y != 0.f ? attn_ex2(x.x - base) : 0.f;
     l += w * x.y;
     unsigned some = __ballot_sync(0xffffffffu, w != 0.f);  // empty pieces hold no data
     while (some) {
@@ -104,7 +107,7 @@ __device__ void join_rows(const AttnArgs& a, int share) {
     }
   }
   if (r >= rows) return;
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = l != 0.f ? 1.f / l : 0.f;
   uint32_t pk[E / 2];
 #pragma unroll
   for (int e = 0; e < E / 2; e++) {
@@ -119,7 +122,7 @@ __device__ void join_rows(const AttnArgs& a, int share) {
   uint32_t* out = reinterpret_cast<uint32_t*>(a.out) + (r * D + lane * E) / 2;
 #pragma unroll
   for (int e = 0; e < E / 2; e++) out[e] = pk[e];
-  if (lane == 0 && a.lse) a.lse[r] = l > 0.f ? (top + log2f(l)) * 0.693147180559945309f : -INFINITY;
+  if (lane == 0 && a.lse) a.lse[r] = l != 0.f ? (top + log2f(l)) * 0.693147180559945309f : -INFINITY;
 }
 
 // What a mass block needs of a row: its log2 normaliser, how many private slots
@@ -180,10 +183,10 @@ __device__ __forceinline__ void load_norms(const AttnArgs& a, MassRows& s, int n
         float m = x[u].y > 0.f ? x[u].x : -INFINITY;
 #pragma unroll
         for (int d = 1; d < 8; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-        float l = x[u].y > 0.f ? x[u].y * attn_ex2(x[u].x - m) : 0.f;
+        float l = x[u].y > 0.f ? x[u].y * attn_ex2(x[u].x - m) : x[u].y;  // 0 or NaN
 #pragma unroll
         for (int d = 1; d < 8; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-        if (i < n && sub == 0) s.lse2[i] = s.lim[i] > 0 && l > 0.f ? m + log2f(l) : INFINITY;
+        if (i < n && sub == 0) s.lse2[i] = s.lim[i] > 0 && l != 0.f ? m + log2f(l) : INFINITY;
       }
     }
     __syncthreads();
@@ -203,7 +206,10 @@ __device__ __forceinline__ void load_norms(const AttnArgs& a, MassRows& s, int n
       float m = top;
 #pragma unroll
       for (int u = 0; u < 4; u++)
-        if (x[u].y > 0.f) m = fmaxf(m, x[u].x);
+        if (x[u].y > 0.f)
+          m = fmaxf(m, x[u].x);
+        else
+          l += x[u].y;  // 0 or NaN
       if (m == -INFINITY) continue;
       l *= attn_ex2(top - m);
       top = m;
@@ -214,10 +220,10 @@ __device__ __forceinline__ void load_norms(const AttnArgs& a, MassRows& s, int n
     float m = top;
 #pragma unroll
     for (int d = 1; d < 8; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    l = m == -INFINITY ? 0.f : l * attn_ex2(top - m);
+    l = m == -INFINITY ? l : l * attn_ex2(top - m);
 #pragma unroll
     for (int d = 1; d < 8; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-    if (live && sub == 0) s.lse2[i] = s.lim[i] > 0 && l > 0.f ? m + log2f(l) : INFINITY;
+    if (live && sub == 0) s.lse2[i] = s.lim[i] > 0 && l != 0.f ? m + log2f(l) : INFINITY;
   }
   __syncthreads();
 }
@@ -305,6 +311,17 @@ __device__ __forceinline__ void mass_dense(const AttnArgs& a, int64_t block, int
   grid_wait();
 }
 
+// Sum of an entry's weights over those of n rows that see it.
+__device__ __forceinline__ float seen_only(const float* sc, int64_t ld, const float* lse2, int n) {
+  float add = 0.f;
+#pragma unroll 1
+  for (int i = 0; i < n; i++) {
+    const float y = sc[i * ld];
+    if (y != -INFINITY) add += attn_ex2(fminf(y, 3e38f) - lse2[i]);
+  }
+  return add;
+}
+
 // Mass of listed slots.  One list holds a slot at most once, so its threads add
 // to different slots; lists that can share a slot (another token's, or another
 // KV head's when all heads share the mass) are added one after the other by one
@@ -386,6 +403,11 @@ __device__ __forceinline__ void mass_listed(const AttnArgs& a, int64_t block, in
                 add[e] += attn_ex2(fminf(y[u][e], 3e38f) - s.lse2[i]);
               }
         }
+        // A row whose normaliser is NaN counts only where it sees the entry.  (The
+        // choice in the loop above took 1.5 us of 27 and of 65.)
+#pragma unroll
+        for (int e = 0; e < E; e++)
+          if (add[e] != add[e]) add[e] = seen_only(sc[e], a.sc_ld, s.lse2 + list[e] * nh, nh);
         // with several lists (then per is 1) those of this round in turn
         const int l1 = lists > 1 ? min(nl - 1, l0 + (int)((w0 + kThreads * E - 1) / W)) : l0;
         for (int l = l0; l <= l1; l++) {

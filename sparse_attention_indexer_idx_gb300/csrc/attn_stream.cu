@@ -344,7 +344,7 @@ __device__ __forceinline__ void stream_item(const AttnArgs& a, int shift, int h,
       if (rid[m][e] < 0) continue;
       const int64_t at = (int64_t)rid[m][e] * parts_all + part;
       if ((lane & 3) == 0) a.pml[at] = make_float2(mx[m][e], sum[m][e]);
-      if (sum[m][e] > 0.f) {
+      if (sum[m][e] != 0.f) {  // (NaN where a score was)
 #pragma unroll
         for (int i = 0; i < D / 8; i++)
           *reinterpret_cast<float2*>(a.po + at * D + 8 * i + 2 * (lane & 3)) = make_float2(o[m][i][2 * e], o[m][i][2 * e + 1]);

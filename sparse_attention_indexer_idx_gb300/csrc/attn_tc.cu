@@ -619,12 +619,12 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       }
       const int64_t at = (int64_t)rid * parts_all + r.part;
       if (live) {
-        a.pml[at] = make_float2(l > 0.f ? m : -INFINITY, l);
+        a.pml[at] = make_float2(l != 0.f ? m : -INFINITY, l);
         // a cell that one block did alone has no second part
         if (!line.whole && (r.part & 1) == 0 && r.j1 == line.cell_start(r.part / 2 + 1))
           a.pml[at + 1] = make_float2(-INFINITY, 0.f);
       }
-      s_row[i][row] = live && l > 0.f ? (int)at : -1;
+      s_row[i][row] = live && l != 0.f ? (int)at : -1;  // (l is NaN where a score was)
       // the sums leave through the memory of the queries, half of a row at a
       // time, so that CH lanes write one row's half next to one another
 #pragma unroll
