@@ -236,8 +236,9 @@ def _stream(stream: Optional[torch.cuda.Stream]):
 
 
 # torch.cuda.current_stream() builds a Stream object; a decode step of a few
-# microseconds asks for the handle alone
+# microseconds asks for the handle alone (its tensors have initialised CUDA)
 _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _raw_stream(stream: Optional[torch.cuda.Stream]):
@@ -245,7 +246,7 @@ def _raw_stream(stream: Optional[torch.cuda.Stream]):
         return stream.cuda_stream
     if _current_raw_stream is None:
         return torch.cuda.current_stream().cuda_stream
-    return _current_raw_stream(torch.cuda.current_device())
+    return _current_raw_stream(_current_device())
 
 
 _DT = {torch.float32: IDX_F32, torch.bfloat16: IDX_BF16, torch.uint8: IDX_FP8_E4M3,
@@ -519,31 +520,38 @@ def _dense(t: torch.Tensor, name: str, shapes, dtype):
 class _Described:
     """A problem whose C struct is built, with all its checks, when it is first
     used and again after a field was assigned or one of its tensors got other
-    memory; a decode loop that only changes the tensors' contents builds it
-    once."""
+    memory, another shape, strides or type; a decode loop that only changes the
+    tensors' contents builds it once.  Lists of tensors are kept as tuples, so
+    that none of theirs is replaced unnoticed."""
 
     def __setattr__(self, name, value):
-        self.__dict__[name] = value
+        self.__dict__[name] = tuple(value) if isinstance(value, list) else value
         self.__dict__.pop("_desc", None)
 
     def _tensors(self):
         for v in list(self.__dict__.values()):
             if isinstance(v, torch.Tensor):
                 yield v
-            elif isinstance(v, (tuple, list)):
+            elif isinstance(v, tuple):
                 yield from (t for t in v if isinstance(t, torch.Tensor))
 
     def desc(self):
         d = self.__dict__.get("_desc")
         if d is not None:
-            for t, at in d[1]:
-                if t.data_ptr() != at:
+            for t, at, shape, dtype, strides in d[1]:
+                if t.data_ptr() != at or t.shape != shape or t.dtype is not dtype:
+                    break
+                if not t.is_contiguous() if strides is None else t.stride() != strides:
                     break
             else:
                 return d
         self.__dict__.pop("_desc", None)
         c = self.c()
-        d = (ctypes.byref(c), [(t, t.data_ptr()) for t in self._tensors()], c, self._shapes(c))
+        # strides are None for a contiguous tensor: with its shape that says all, and
+        # is asked for more quickly (a call of 9 us is as long on the host)
+        seen = [(t, t.data_ptr(), t.shape, t.dtype, None if t.is_contiguous() else t.stride())
+                for t in self._tensors()]
+        d = (ctypes.byref(c), seen, c, self._shapes(c))
         self.__dict__["_desc"] = d
         return d
 
@@ -564,9 +572,11 @@ class AttnProblem(_Described):
     ids: Optional[torch.Tensor] = None           # [B, T, W] or [B, T, n_kv, W] int32; W == 0 selects no slot
 
     def _shapes(self, c):
-        """Shapes of out, lse, and mass with one and with n_kv mass heads."""
+        """Shape and type of out, shape of lse, and of mass with one and with n_kv
+        mass heads."""
         q = self.q.shape
-        return q, q[:3], torch.Size((c.B, 1, c.S)), torch.Size((c.B, c.n_kv, c.S))
+        one, each = (torch.Size((c.B, h, c.S)) for h in (1, c.n_kv))
+        return q, self.q.dtype, q[:3], one if c.S else None, each if c.S else None
 
     def c(self) -> attn_problem:
         q = self.q
@@ -622,16 +632,17 @@ def attn_shared(p: AttnProblem, out: torch.Tensor, lse: Optional[torch.Tensor], 
                 ws: torch.Tensor, stream=None):
     """out [B, T, Hq, D]; lse [B, T, Hq] float32 or None; mass [B, n_kv or 1, S]
     float32 (added to) or None."""
-    ref, _, cp, (so, sl, s1, sh) = p.desc()
-    po = _out(out, "out", so, p.q.dtype)
+    ref, _, _, (so, dt, sl, s1, sh) = p.desc()
+    po = _out(out, "out", so, dt)
     pl = None if lse is None else _out(lse, "lse", sl, torch.float32)
     pm, heads = None, 1
     if mass is not None:
-        _need(cp.S > 0, "mass: there is no private cache")
-        one = mass.shape == s1
-        heads = 1 if one else cp.n_kv
-        pm = _out(mass, "mass", s1 if one else sh, torch.float32)
-    _need(ws.is_cuda and ws.is_contiguous(), "ws: expected a contiguous CUDA tensor")
+        _need(s1 is not None, "mass: there is no private cache")
+        s = mass.shape
+        heads = 1 if s == s1 else sh[1]
+        pm = _out(mass, "mass", s1 if heads == 1 else sh, torch.float32)
+    if not (ws.is_cuda and ws.is_contiguous()):
+        raise ValueError("ws: expected a contiguous CUDA tensor")
     st = (_lib or lib()).attn_shared(ref, po, pl, pm, heads, ws.data_ptr(), ws.nbytes, _raw_stream(stream))
     if st:
         _check(st)
