@@ -10,7 +10,7 @@ alike).  Everything is allocated once and enqueued on the current stream.
 """
 from __future__ import annotations
 
-from typing import Optional
+from typing import Optional, Sequence
 
 import torch
 
@@ -28,6 +28,7 @@ class DecodeCache:
         self.pos = torch.full((requests, 1, slots), -1, dtype=torch.int32, device=device)
         self.mass = z(requests, 1, slots, dt=torch.float32)
         self.cur = z(requests, dt=torch.int32)            # positions seen so far
+        self.filled = 0                                   # slots of the longest request, known to the host
         self.prefix_k, self.prefix_v = prefix_k, prefix_v
         self.top_k = top_k
         self.ids = z(requests, top_k, dt=torch.int32)
@@ -36,13 +37,37 @@ class DecodeCache:
         self.rows = torch.arange(requests, device=device)
         self.ws: Optional[torch.Tensor] = None
 
+    def fill(self, k: torch.Tensor, v: torch.Tensor, index_k: torch.Tensor,
+             lens: Optional[Sequence[int]] = None) -> None:
+        """The prompts, into empty caches: k, v [B, n, kv_heads, dim], index_k
+        [B, n, index_dim]; request b has lens[b] <= n tokens (n without lens)."""
+        requests, slots = self.index_k.shape[:2]
+        n = k.shape[1]
+        lens = [n] * requests if lens is None else [int(x) for x in lens]
+        if n > slots or len(lens) != requests or any(x < 0 or x > n for x in lens):
+            raise ValueError(f"prompts of {n} tokens, lens {lens}: {requests} requests of {slots} slots")
+        self.k[:, :n], self.v[:, :n], self.index_k[:, :n] = k, v, index_k
+        self.lens[:, 0] = torch.tensor(lens, dtype=torch.int32).to(self.lens.device)
+        self.cur.copy_(self.lens[:, 0])
+        at = torch.arange(self.pos.shape[2], dtype=torch.int32, device=self.pos.device)
+        self.pos[:, 0] = torch.where(at < self.lens, at, -1)
+        self.mass.zero_()
+        self.filled = max(lens, default=0)
+
     def append(self, k: torch.Tensor, v: torch.Tensor, index_k: torch.Tensor) -> None:
-        """One token of every request: k, v [B, kv_heads, dim], index_k [B, index_dim]."""
-        at = self.lens[:, 0].long()
+        """One token of every request: k, v [B, kv_heads, dim], index_k [B, index_dim].
+        Full caches are refused: trim them first."""
+        slots = self.index_k.shape[1]
+        if self.filled >= slots:
+            raise ValueError(f"append: a request's {slots} slots are full")
+        # The count is the host's.  Lengths that were changed past it must not index
+        # out of the caches: the kernels then report the length itself.
+        at = self.lens[:, 0].long().clamp(0, slots - 1)
         self.k[self.rows, at], self.v[self.rows, at], self.index_k[self.rows, at] = k, v, index_k
         self.pos[self.rows, 0, at] = self.cur
         self.lens += 1
         self.cur += 1
+        self.filled += 1
 
     def step(self, q: torch.Tensor, index_q: torch.Tensor, index_w: torch.Tensor, segments: int = 16) -> torch.Tensor:
         """q [B, 1, q_heads, dim]; index_q [B, H, index_dim], index_w [B, H] of the
@@ -66,6 +91,7 @@ class DecodeCache:
                            (self.k, self.v, self.index_k))
         src = torch.empty((self.lens.shape[0], 1, n_keep), dtype=torch.int32, device=self.mass.device)
         B.cache_evict(p, src, self.lens, self.pos, self.mass)
+        self.filled = min(self.filled, n_keep)
 
 
 def decode_step_example(seed: int = 0, requests: int = 8, prefix: int = 1000, slots: int = 2100, K: int = 256,
@@ -76,12 +102,8 @@ def decode_step_example(seed: int = 0, requests: int = 8, prefix: int = 1000, sl
     rn = lambda *s: torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
     c = DecodeCache(requests, slots, q_heads, kv_heads, dim, 128, K, rn(prefix, kv_heads, dim),
                     rn(prefix, kv_heads, dim))
-    fill = slots - 4
-    c.k[:, :fill], c.v[:, :fill] = rn(requests, fill, kv_heads, dim), rn(requests, fill, kv_heads, dim)
-    c.index_k[:, :fill] = rn(requests, fill, 128)
-    c.lens += fill
-    c.cur += fill
-    c.pos[:, 0, :fill] = torch.arange(fill, device="cuda", dtype=torch.int32)
+    n = slots - 4
+    c.fill(rn(requests, n, kv_heads, dim), rn(requests, n, kv_heads, dim), rn(requests, n, 128))
     finite = True
     for _ in range(4):
         c.append(rn(requests, kv_heads, dim), rn(requests, kv_heads, dim), rn(requests, 128))
