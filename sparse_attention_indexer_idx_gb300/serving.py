@@ -20,10 +20,12 @@ from . import binding as B
 class DecodeCache:
     def __init__(self, requests: int, slots: int, q_heads: int, kv_heads: int, dim: int, index_dim: int, top_k: int,
                  prefix_k: Optional[torch.Tensor] = None, prefix_v: Optional[torch.Tensor] = None,
-                 dtype=torch.bfloat16, device="cuda"):
+                 dtype=torch.bfloat16, device="cuda", index_dtype=torch.bfloat16):
+        """dtype (bfloat16 or float16): of keys, values and queries; index_dtype
+        (bfloat16 or float32): of the indexer's keys and queries."""
         z = lambda *s, dt=dtype: torch.zeros(s, dtype=dt, device=device)  # noqa: E731
         self.k, self.v = z(requests, slots, kv_heads, dim), z(requests, slots, kv_heads, dim)
-        self.index_k = z(requests, slots, index_dim)
+        self.index_k = z(requests, slots, index_dim, dt=index_dtype)
         self.lens = z(requests, 1, dt=torch.int32)
         self.pos = torch.full((requests, 1, slots), -1, dtype=torch.int32, device=device)
         self.mass = z(requests, 1, slots, dt=torch.float32)
