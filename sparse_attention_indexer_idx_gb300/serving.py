@@ -3,10 +3,16 @@
 `DecodeCache` holds the private caches of a batch of requests that share a
 prefix: keys, values and index keys by slot, each slot's position and running
 attention mass.  A step appends the new tokens, lets the indexer choose slots
-(idx_topk, covered by segment witnesses), attends to the prefix and the chosen
-slots (attn_shared, which adds the weights to the masses), and trims the caches
-to their budget by mass (cache_evict, which moves keys, values and index keys
-alike).  Everything is allocated once and enqueued on the current stream.
+(idx_topk), covers every segment of the slots with a witness (witness_merge),
+attends to the prefix and the chosen slots (attn_shared, which adds the weights
+to the masses), and trims the caches to their budget by mass (cache_evict, which
+moves keys, values and index keys alike).  Everything is allocated once and
+enqueued on the current stream.
+
+The segments are equal shares of a request's filled slots.  Until the first trim
+slots are positions, and a segment is a stretch of the context.  A trim moves
+rows into freed slots, out of the order of their positions: from then on a
+segment is a share of what is kept, and its witness still one of its slots.
 """
 from __future__ import annotations
 
