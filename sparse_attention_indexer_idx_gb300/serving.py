@@ -6,13 +6,17 @@ attention mass.  A step appends the new tokens, lets the indexer choose slots
 (idx_topk), covers every segment of the slots with a witness (witness_merge),
 attends to the prefix and the chosen slots (attn_shared, which adds the weights
 to the masses), and trims the caches to their budget by mass (cache_evict, which
-moves keys, values and index keys alike).  Everything is allocated once and
-enqueued on the current stream.
+moves keys, values and index keys alike).  The work is enqueued on the current
+stream.
 
 The segments are equal shares of a request's filled slots.  Until the first trim
 slots are positions, and a segment is a stretch of the context.  A trim moves
 rows into freed slots, out of the order of their positions: from then on a
 segment is a share of what is kept, and its witness still one of its slots.
+
+The caches, the chosen ids, the output and what a trim returns are allocated
+once, the workspace with the first step.  The problems of a step are described
+anew each time, because its queries are other tensors.
 """
 from __future__ import annotations
 
@@ -43,6 +47,7 @@ class DecodeCache:
         self.out = z(requests, 1, q_heads, dim)
         self.key_off = torch.arange(requests, dtype=torch.int64, device=device) * slots
         self.rows = torch.arange(requests, device=device)
+        self.src = z(requests * slots, dt=torch.int32)    # where a trim takes each slot from
         self.ws: Optional[torch.Tensor] = None
 
     def fill(self, k: torch.Tensor, v: torch.Tensor, index_k: torch.Tensor,
@@ -93,13 +98,19 @@ class DecodeCache:
         B.attn_shared(a, self.out, None, self.mass, self.ws)
         return self.out
 
-    def trim(self, n_keep: int, n_first: int, n_last: int) -> None:
-        """Evicts every request down to n_keep slots."""
+    def trim(self, n_keep: int, n_first: int, n_last: int) -> torch.Tensor:
+        """Evicts every request down to n_keep slots.  Returns the slot that each
+        new slot came from, [B, 1, n_keep] int32, -1 behind the new length; its
+        buffer is reused."""
+        requests, _, slots = self.mass.shape
+        if not 0 < n_keep <= slots:
+            raise ValueError(f"trim: n_keep={n_keep} of {slots} slots")
         p = B.EvictProblem(self.mass, self.lens, n_keep, n_first, n_last, self.pos, self.cur,
                            (self.k, self.v, self.index_k))
-        src = torch.empty((self.lens.shape[0], 1, n_keep), dtype=torch.int32, device=self.mass.device)
+        src = self.src[: requests * n_keep].view(requests, 1, n_keep)
         B.cache_evict(p, src, self.lens, self.pos, self.mass)
         self.filled = min(self.filled, n_keep)
+        return src
 
 
 def decode_step_example(seed: int = 0, requests: int = 8, prefix: int = 1000, slots: int = 2100, K: int = 256,

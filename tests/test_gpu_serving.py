@@ -31,7 +31,7 @@ def check_step(B, c, q, iq, iw, segments, dtype):  # noqa: F811
     B.idx_topk(p, c.top_k, learned, None, ws)
     out = c.step(q, iq, iw, segments)
     torch.cuda.synchronize()
-    K, ln = c.top_k, num(lens)
+    K, ln = c.top_k, num(lens).copy()
     for b in range(requests):
         s, a = od.indexer_score(num(iq[b]), num(iw[b]), num(c.index_k[b, :ln[b]]))
         check_topk_row(num(learned[b]), None, s, a, K, EPS["bf16"])
@@ -53,10 +53,13 @@ def check_step(B, c, q, iq, iw, segments, dtype):  # noqa: F811
 
 def check_trim(c, n_keep, n_first, n_last):
     before = {n: num(getattr(c, n)).copy() for n in ("k", "v", "index_k", "mass", "pos", "lens", "cur")}
-    c.trim(n_keep, n_first, n_last)
+    held = torch.cuda.memory_allocated()
+    moved = c.trim(n_keep, n_first, n_last)
+    assert torch.cuda.memory_allocated() == held         # a trim takes no memory
     torch.cuda.synchronize()
     src, ln, pos, mass = oa.cache_evict(before["mass"], before["lens"], n_keep, n_first, n_last, before["pos"],
                                         before["cur"])
+    assert np.array_equal(num(moved), src)
     assert np.array_equal(num(c.lens), ln) and np.array_equal(num(c.cur), before["cur"])
     assert np.array_equal(num(c.pos)[..., :n_keep], pos) and np.array_equal(num(c.mass)[..., :n_keep], mass)
     for n in ("k", "v", "index_k"):

@@ -62,3 +62,9 @@ def test_lengths_changed_past_the_count_index_nothing_out_of_range():
 def test_prompts_that_do_not_fit_are_refused(n, lens):
     with pytest.raises(ValueError):
         cache().fill(*prompt(n), lens=lens)
+
+
+@pytest.mark.parametrize("n_keep", [0, -1, 7])
+def test_trims_to_no_slot_or_to_more_than_there_are_are_refused(n_keep):
+    with pytest.raises(ValueError):
+        cache().trim(n_keep, 0, 0)
