@@ -75,9 +75,9 @@ def cache_evict(mass, lens, n_keep, n_first=0, n_last=0, pos=None, cur=None):
             nk = min(n, n_keep)
             stay = np.zeros(n, dtype=bool)
             stay[np.lexsort((np.arange(n), -rank))[:nk]] = True
-            late = [s for s in range(nk, n) if stay[s]]
-            row = [s if stay[s] else late.pop(0) for s in range(nk)]
-            assert not late
+            late, holes = nk + np.flatnonzero(stay[nk:]), np.flatnonzero(~stay[:nk])
+            row = np.arange(nk)
+            row[holes] = late   # both ascending, and equally many
             src[b, m, :nk] = row
             new_len[b, m] = nk
             new_pos[b, m, :nk] = at[row]
