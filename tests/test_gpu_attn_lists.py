@@ -1,9 +1,11 @@
-"""attn_shared over selections that hold nothing: a list without entries (W = 0)
-selects no slot, which is not the same as no list (every slot)."""
+"""attn_shared over selections: a list without entries (W = 0) selects no slot,
+which is not the same as no list (every slot); the positions of selected blocks
+are lists too."""
 import numpy as np
 import pytest
 import torch
 
+from oracle import block_select as ob
 from test_gpu_attn import B, check, make, run  # noqa: F401  (B is a fixture)
 
 pytestmark = pytest.mark.gpu
@@ -60,3 +62,32 @@ def test_an_empty_selection_of_an_empty_cache(B, per_head):  # noqa: F811
     ws = torch.empty(B.attn_shared_workspace_size(p, False), dtype=torch.uint8, device="cuda")
     B.attn_shared(p, out, lse, None, ws)
     check(t, out, lse, None)
+
+
+@pytest.mark.parametrize("T,L,P,dtype", [(1, 1000, 0, "bf16"), (3, 1500, 200, "f16"), (4, 517, 0, "bf16")])
+def test_positions_of_selected_blocks(B, T, L, P, dtype):  # noqa: F811
+    """From block scores to attention: each token's and KV head's blocks, the
+    positions that they cover, and attention over these."""
+    n_kv, bs, top = 4, 64, 3
+    t = make(420 + T, B=1, T=T, Hq=16, n_kv=n_kv, S=L, P=P, D=128, lens=[L], mass=n_kv, dtype=dtype)
+    g = torch.Generator().manual_seed(421)
+    index_q, index_k = torch.randn(T, n_kv, 128, generator=g), torch.randn(L, 128, generator=g)
+    pos = torch.arange(L - T, L, dtype=torch.int32)
+    cfg = B.block_sparse_config(bs, top, 1, 1)
+    dev = {"device": "cuda", "dtype": torch.int32}
+    blocks, counts = torch.empty((T, n_kv, top), **dev), torch.empty((T, n_kv), **dev)
+    ws = torch.empty(B.block_select_workspace_size(T, n_kv, L, cfg), dtype=torch.uint8, device="cuda")
+    B.block_select(index_q.cuda(), index_k.cuda(), pos.cuda(), cfg, blocks, counts, ws)
+    ids = torch.empty((T, n_kv, top * bs), **dev)
+    B.block_positions(blocks, counts, pos.cuda(), L, bs, ids, None)
+    t["ids"] = ids.cpu().view(1, T, n_kv, top * bs)
+    chosen, cover = blocks.cpu().numpy(), t["ids"].numpy()[0]
+    for i in range(T):
+        for h in range(n_kv):
+            want = ob.positions_of_blocks([b for b in chosen[i, h] if b >= 0], int(pos[i]), L, bs)
+            assert [x for x in cover[i, h] if x >= 0] == want
+    assert (t["ids"] == -1).any()          # the last block ends inside the cache
+    out, lse, mass, _, _ = run(B, t)
+    torch.cuda.synchronize()
+    check(t, out, lse, mass)
+    assert B.device_error() == 0
