@@ -654,7 +654,7 @@ class EvictProblem(_Described):
     """Device tensors of one cache_evict call (see evict_problem in include/idx.h).
     planes are indexed [B, S, heads, row] or [B, S, row]; they are compacted in
     place."""
-    mass: torch.Tensor                           # [B, mass_heads, S] float32, rows may be strided
+    mass: torch.Tensor                           # [B, mass_heads, S] float32
     lens: torch.Tensor                           # [B, mass_heads] int32
     n_keep: int
     n_first: int = 0
