@@ -91,3 +91,16 @@ def test_positions_of_selected_blocks(B, T, L, P, dtype):  # noqa: F811
     torch.cuda.synchronize()
     check(t, out, lse, mass)
     assert B.device_error() == 0
+
+
+@pytest.mark.parametrize("kw", [
+    dict(T=1, mass=1), dict(T=3, mass=2, D=64), dict(T=2, mass=1, ids_per_head=True, dtype="f16"),
+    dict(T=1, Hq=64, mass=1, P=30),
+])
+def test_lists_under_lengths_of_each_kv_head(B, kw):  # noqa: F811
+    a = dict(dict(B=3, Hq=8, n_kv=2, S=120, W=90, lens=[[120, 3], [0, 77], [1, 119]], per_head_lens=True), **kw)
+    t = make(430, **a)
+    out, lse, mass, _, _ = run(B, t)
+    torch.cuda.synchronize()
+    assert B.device_error() == 0
+    check(t, out, lse, mass)

@@ -80,6 +80,16 @@ def test_a_query(B):  # noqa: F811
 
 
 @pytest.mark.parametrize("kw", [
+    dict(T=3, mass=2), dict(T=3, mass=1), dict(T=3, mass=1, ids_per_head=True, D=64),
+    dict(T=1, mass=1, per_head_lens=True, lens=[[100, 50], [31, 90]]),
+])
+def test_a_query_whose_list_names_slots_that_it_does_not_see(B, kw):  # noqa: F811
+    # other rows see them: their masses get those rows' weights and nothing else
+    t = make(506, **dict(dict(B=2, Hq=8, n_kv=2, S=100, W=100, lens=[100, 60]), **kw))
+    _compare(B, t, _planted(t, "q", (0, 0, 5, 3)), lambda b, i, h: (b, i, h) == (0, 0, 5))
+
+
+@pytest.mark.parametrize("kw", [
     dict(B=2, T=1, Hq=8, n_kv=2, S=30, P=200, prefix_len=[90, 200], lens=[30, 30], mass=1),
     dict(B=20, T=1, Hq=8, n_kv=2, S=5, P=300, prefix_len=[15 * i for i in range(1, 21)], mass=2),   # a line of its own
     dict(B=40, T=1, Hq=16, n_kv=2, S=9, P=9000, prefix_len=[225 * i for i in range(1, 41)], mass=2),  # tensor cores
