@@ -56,7 +56,9 @@ PrefixWay prefix_way(const attn_problem& p) {
 // listed slots each behind 3,309 tokens: 31 us, with eight key tiles a block 34).
 // One after the other took 337 us for 128 requests with caches of 2,048 slots
 // behind 65,536 tokens, side by side 289; 53 and 41 for 32 requests with 1,024
-// slots behind 8,192.
+// slots behind 8,192.  Caches that are full are also best taken as 0.6 full: 330
+// us for those 128 requests, 390 with a share for full ones (lengths from half to
+// all: 287 and 385); the others measured do not depend on it.
 AttnTcArgs plan_tc(const AttnArgs& a) {
   const attn_problem& p = a.p;
   AttnTcArgs t{};

@@ -311,7 +311,10 @@ __device__ __forceinline__ void stream_item(const AttnArgs& a, int shift, int h,
           sum[m][e >> 1] += s[m][i][e];
         }
     }
-    // weights (rounded to the element type) times values
+    // Weights times values.  The weights are rounded to the element type, as the
+    // 16-bit operand of the product has to be, one rounding of at most 2^-8 (2^-11
+    // for fp16) of each weight, as large as the output's own; the sum that divides
+    // them is of the unrounded ones, in 32 bits.
 #pragma unroll
     for (int kk = 0; kk < KT / 16; kk++) {
       uint32_t pf[MT][4];

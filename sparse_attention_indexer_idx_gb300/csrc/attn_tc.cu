@@ -575,6 +575,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
           }
           fence_proxy_async_smem();
         }
+        // The weights are rounded to the element type, which the 16-bit operand has
+        // to be (in error as much as the output's own rounding); their sum, which
+        // divides the output, is of the unrounded ones.
         const float base = m == -INFINITY ? 0.f : m;
         const uint64_t c2 = f2_pack(c, c), b2 = f2_pack(-base, -base), one = f2_pack(1.f, 1.f);
 #pragma unroll
