@@ -236,17 +236,9 @@ def _stream(stream: Optional[torch.cuda.Stream]):
 
 
 # torch.cuda.current_stream() builds a Stream object; a decode step of a few
-# microseconds asks for the handle alone (its tensors have initialised CUDA)
-_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-
-
-def _raw_stream(stream: Optional[torch.cuda.Stream]):
-    if stream is not None:
-        return stream.cuda_stream
-    if _current_raw_stream is None:
-        return torch.cuda.current_stream().cuda_stream
-    return _current_raw_stream(_current_device())
+# microseconds asks for the handle alone
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 _DT = {torch.float32: IDX_F32, torch.bfloat16: IDX_BF16, torch.uint8: IDX_FP8_E4M3,
@@ -536,24 +528,32 @@ class _Described:
                 yield from (t for t in v if isinstance(t, torch.Tensor))
 
     def desc(self):
+        """(reference to the struct, index of the tensors' device, what the call
+        compares its outputs with)"""
         d = self.__dict__.get("_desc")
         if d is not None:
-            for t, at, shape, dtype, strides in d[1]:
-                if t.data_ptr() != at or t.shape != shape or t.dtype is not dtype:
-                    break
-                if not t.is_contiguous() if strides is None else t.stride() != strides:
+            for t, at, shape, dtype in d[1]:
+                if t.data_ptr() != at or t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
                     break
             else:
-                return d
+                for t, at, shape, dtype, strides in d[2]:
+                    if t.data_ptr() != at or t.shape != shape or t.dtype is not dtype or t.stride() != strides:
+                        break
+                else:
+                    return d[0]
         self.__dict__.pop("_desc", None)
         c = self.c()
-        # strides are None for a contiguous tensor: with its shape that says all, and
-        # is asked for more quickly (a call of 9 us is as long on the host)
-        seen = [(t, t.data_ptr(), t.shape, t.dtype, None if t.is_contiguous() else t.stride())
-                for t in self._tensors()]
-        d = (ctypes.byref(c), seen, c, self._shapes(c))
-        self.__dict__["_desc"] = d
-        return d
+        # The contiguous ones, whose shape says all, are asked for less (a call of
+        # 9 us is as long on the host).
+        dense, strided = [], []
+        for t in self._tensors():
+            if t.is_contiguous():
+                dense.append((t, t.data_ptr(), t.shape, t.dtype))
+            else:
+                strided.append((t, t.data_ptr(), t.shape, t.dtype, t.stride()))
+        use = (ctypes.byref(c), self._device(), self._shapes(c))
+        self.__dict__["_desc"] = (use, dense, strided)
+        return use
 
 
 @dataclass
@@ -570,6 +570,9 @@ class AttnProblem(_Described):
     pv: Optional[torch.Tensor] = None
     prefix_len: Optional[torch.Tensor] = None    # [B] int32
     ids: Optional[torch.Tensor] = None           # [B, T, W] or [B, T, n_kv, W] int32; W == 0 selects no slot
+
+    def _device(self):
+        return self.q.device.index
 
     def _shapes(self, c):
         """Shape and type of out, shape of lse, and of mass with one and with n_kv
@@ -632,18 +635,24 @@ def attn_shared(p: AttnProblem, out: torch.Tensor, lse: Optional[torch.Tensor], 
                 ws: torch.Tensor, stream=None):
     """out [B, T, Hq, D]; lse [B, T, Hq] float32 or None; mass [B, n_kv or 1, S]
     float32 (added to) or None."""
-    ref, _, _, (so, dt, sl, s1, sh) = p.desc()
+    ref, device, (so, dt, sl, s1, sh) = p.desc()
     po = _out(out, "out", so, dt)
     pl = None if lse is None else _out(lse, "lse", sl, torch.float32)
     pm, heads = None, 1
     if mass is not None:
-        _need(s1 is not None, "mass: there is no private cache")
+        if s1 is None:
+            raise ValueError("mass: there is no private cache")
         s = mass.shape
-        heads = 1 if s == s1 else sh[1]
-        pm = _out(mass, "mass", s1 if heads == 1 else sh, torch.float32)
+        if s != s1:
+            heads = sh[1]
+        if (s == s1 or s == sh) and mass.dtype is torch.float32 and mass.is_contiguous() and mass.is_cuda:
+            pm = mass.data_ptr()
+        else:
+            _dense(mass, "mass", (tuple(s1), tuple(sh)), torch.float32)  # raises
     if not (ws.is_cuda and ws.is_contiguous()):
         raise ValueError("ws: expected a contiguous CUDA tensor")
-    st = (_lib or lib()).attn_shared(ref, po, pl, pm, heads, ws.data_ptr(), ws.nbytes, _raw_stream(stream))
+    st = (_lib or lib()).attn_shared(ref, po, pl, pm, heads, ws.data_ptr(), ws.nbytes,
+                                     _current_raw_stream(device) if stream is None else stream.cuda_stream)
     if st:
         _check(st)
     return out, lse, mass
@@ -662,6 +671,9 @@ class EvictProblem(_Described):
     pos: Optional[torch.Tensor] = None           # [B, mass_heads, S] int32
     cur: Optional[torch.Tensor] = None           # [B] int32
     planes: tuple = ()
+
+    def _device(self):
+        return self.mass.device.index
 
     def _shapes(self, c):
         """Shapes of out_src (and of outputs beside it), and of out_len."""
@@ -699,7 +711,7 @@ def cache_evict(p: EvictProblem, out_src: torch.Tensor, out_len: Optional[torch.
     """out_src [B, mass_heads, n_keep] int32; out_len [B, mass_heads] int32;
     out_pos / out_mass [B, mass_heads, n_keep], or the problem's pos / mass
     themselves."""
-    ref, _, ce, (ss, sl) = p.desc()
+    ref, device, (ss, sl) = p.desc()
     ps = _out(out_src, "out_src", ss, torch.int32)
     pl = None if out_len is None else _out(out_len, "out_len", sl, torch.int32)
     ld, pp, pm = ss[2], None, None
@@ -712,7 +724,8 @@ def cache_evict(p: EvictProblem, out_src: torch.Tensor, out_len: Optional[torch.
             pp = _out(out_pos, "out_pos", so, torch.int32)
         if out_mass is not None:
             pm = _out(out_mass, "out_mass", so, torch.float32)
-    st = (_lib or lib()).cache_evict(ref, ps, pl, pp, pm, ld, _raw_stream(stream))
+    st = (_lib or lib()).cache_evict(ref, ps, pl, pp, pm, ld,
+                                     _current_raw_stream(device) if stream is None else stream.cuda_stream)
     if st:
         _check(st)
     return out_src, out_len, out_pos, out_mass
