@@ -6,7 +6,7 @@
 // warp or more each; the others add masses.  A mass block takes its rows'
 // normalisers from the pieces' (m, l) itself, so it need not wait for the join.
 // Large calls are bound by those reads and an exponential a score (16 caches of
-// 24,576 slots on average under 64 rows: 100 MB in 32 us), small ones by the
+// 24,576 slots on average under 64 rows: 100 MB in 34 us), small ones by the
 // chain of loads from the pieces to a block's sums, 6 to 10 us.
 //
 // A piece is empty where its sum is 0, and only there: a sum that is NaN (a
