@@ -251,16 +251,22 @@ def _ptr(t: Optional[torch.Tensor]):
     return ctypes.c_void_p(t.data_ptr())
 
 
+def _holds(t: Optional[torch.Tensor], dtype: torch.dtype, numel: int, name: str) -> None:
+    if t is None:
+        raise ValueError(f"{name}: expected a tensor, got None")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.numel() < numel:
+        raise ValueError(f"{name}: {t.numel()} elements, the call needs {numel}")
+
+
 def _buf(t: Optional[torch.Tensor], dtype: torch.dtype, numel: int, name: str):
     """A caller's device buffer that the library writes or reads as `numel`
     elements of `dtype` (the C ABI takes plain pointers, so this is the last
     place where a short or mistyped buffer can be caught)."""
     if t is None:
         return None
-    if t.dtype != dtype:
-        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.numel() < numel:
-        raise ValueError(f"{name}: {t.numel()} elements, the call needs {numel}")
+    _holds(t, dtype, numel, name)
     return _ptr(t)
 
 
@@ -291,10 +297,21 @@ class Problem:
     key_scale: Optional[torch.Tensor] = None  # [n_keys] float32 for FP8 keys
 
     def c(self) -> idx_problem:
-        M, H, D = self.q.shape
-        return idx_problem(_ptr(self.q), _DT[self.q.dtype], _ptr(self.w), M, H, D, _ptr(self.keys),
-                           _DT[self.keys.dtype], _ptr(self.key_scale), self.keys.shape[0], _ptr(self.key_off),
-                           _ptr(self.key_len), int(self.max_key_len))
+        q, keys = self.q, self.keys
+        if q.dim() != 3 or q.dtype not in _DT:
+            raise ValueError(f"q: expected [M, H, D] float32 or bfloat16, got {tuple(q.shape)} {q.dtype}")
+        M, H, D = q.shape
+        if keys.dim() != 2 or keys.shape[1] != D or keys.dtype not in _DT:
+            raise ValueError(f"keys: expected [n_keys, {D}] float32, bfloat16 or e4m3, got {tuple(keys.shape)} {keys.dtype}")
+        n_keys = keys.shape[0]
+        _holds(self.w, torch.float32, M * H, "w")
+        _holds(self.key_len, torch.int32, M, "key_len")
+        if self.key_off is not None:
+            _holds(self.key_off, torch.int64, M, "key_off")
+        if self.key_scale is not None:
+            _holds(self.key_scale, torch.float32, n_keys, "key_scale")
+        return idx_problem(_ptr(q), _DT[q.dtype], _ptr(self.w), M, H, D, _ptr(keys), _DT[keys.dtype],
+                           _ptr(self.key_scale), n_keys, _ptr(self.key_off), _ptr(self.key_len), int(self.max_key_len))
 
 
 def device_error() -> int:
