@@ -156,8 +156,9 @@ class PagedCache:
             self.ids = z(requests, 1, top_k, dt=torch.int32)
         self.ws: Optional[torch.Tensor] = None
 
-    def _take(self, grow: dict) -> None:
-        """Pages for the requests (index -> length), all of them or none."""
+    def _take(self, grow: dict) -> dict:
+        """Pages for the requests (index -> length), all of them or none.  Returns how
+        many each got."""
         want = {}
         for b, n in grow.items():
             if n > self.max_len:
@@ -170,6 +171,22 @@ class PagedCache:
                 at = len(self.pages[b])
                 self.pages[b] += [self.free.pop() for _ in range(n)]
                 self.table[b, at: at + n] = torch.tensor(self.pages[b][at:], dtype=torch.int32).to(self.table.device)
+        return want
+
+    def _append(self, p: B.AppendProblem, grow: dict) -> None:
+        """The rows of a described call into the caches of requests that become that
+        long, on pages taken for it.  Where the library refuses it they go back."""
+        took = self._take(grow)
+        try:
+            B.paged_append(p)
+        except Exception:
+            for b, n in reversed(took.items()):
+                for _ in range(n):
+                    self.free.append(self.pages[b].pop())
+                self.table[b, len(self.pages[b]): len(self.pages[b]) + n] = -1
+            raise
+        for b, n in grow.items():
+            self.known[b] = n
 
     def _check(self, b: int) -> None:
         if not 0 <= b < len(self.known):
@@ -191,6 +208,8 @@ class PagedCache:
 
         p = [plane("k", k, self.k, self.freq, self.table), B.HeadPlane(v, self.v, table=self.table)]
         if self.top_k is not None:
+            if index_k is None or (q is not None and index_q is None):
+                raise ValueError("the indexer's rows are missing")
             pool = self.index_k.view(-1, self.page_size, 1, self.index_k.shape[2])
             p.append(plane("index_k", index_k.unsqueeze(1), pool, self.index_freq, self.index_table))
         if q is not None:
@@ -206,31 +225,37 @@ class PagedCache:
         first, n = self.known[b], k.shape[0]
         if n == 0:
             raise ValueError("a prompt without tokens")
-        self._take({b: first + n})
         slot = torch.arange(first, first + n, dtype=torch.int32, device=k.device)
-        B.paged_append(B.AppendProblem(self._planes(k, v, index_k), slot, torch.full_like(slot, b)))
-        self.lens[b], self.live[b], self.known[b] = first + n, 1, first + n
+        append = B.AppendProblem(self._planes(k, v, index_k), slot, torch.full_like(slot, b))
+        append.desc()                                     # (refuses wrong tensors before pages are taken)
+        self._append(append, {b: first + n})
+        self.lens[b], self.live[b] = first + n, 1
 
     def step(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, index_q: Optional[torch.Tensor] = None,
              index_k: Optional[torch.Tensor] = None, index_w: Optional[torch.Tensor] = None,
              segments: int = 16) -> torch.Tensor:
         """One token of every request that has begun: q [B, q_heads, dim], k and v
         [B, kv_heads, dim], index_q [B, index_heads, index_dim], index_k [B, index_dim],
-        as the projections leave them; index_w [B, index_heads].  Rows of requests that
-        have ended are passed by, their output is 0.  Returns [B, 1, q_heads, dim]; its
-        buffer is reused."""
+        as the projections leave them; index_w [B, index_heads] float32, contiguous.  Rows
+        of requests that have ended are passed by, their output is 0.  A step that is
+        refused leaves the cache as it was.  Returns [B, 1, q_heads, dim]; its buffer is
+        reused."""
         requests = self.lens.shape[0]
         grow = {b: n + 1 for b, n in enumerate(self.known) if n}
-        self._take(grow)
+        longest = max(grow.values(), default=0)
+        # Whatever can be refused is, before anything is changed.
         append = B.AppendProblem(self._planes(k, v, index_k, q, index_q), self.slot)
-        append.desc()                                     # (refuses wrong tensors before anything is changed)
-        self.lens += self.live
-        torch.sub(self.lens, 1, out=self.slot)            # -1 for those that have ended
-        B.paged_append(append)
-        for b, n in grow.items():
-            self.known[b] = n
-        ids, longest, need = None, max(self.known, default=0), 0
+        append.desc()
+        ids, need = None, 0
         if self.top_k is not None:
+            heads = self.index_q.shape[1]
+            if not 0 <= segments <= B.IDX_MAX_SEGMENTS:
+                raise ValueError(f"segments={segments} outside [0, {B.IDX_MAX_SEGMENTS}]")
+            if index_w is None or index_w.numel() != requests * heads or index_w.shape[-1] != heads:
+                raise ValueError(f"index_w: expected [{requests}, {heads}], got "
+                                 f"{None if index_w is None else tuple(index_w.shape)}")
+            if index_w.device != self.lens.device:
+                raise ValueError(f"index_w: on {index_w.device}, the cache is on {self.lens.device}")
             ids, slots = self.ids, self.index_k.shape[1]
             p = B.Problem(self.index_q, index_w, self.index_k.view(requests * slots, -1), self.lens, max(longest, 1),
                           self.key_off)
@@ -239,6 +264,13 @@ class PagedCache:
         need = max(need, B.attn_paged_workspace_size(a))
         if self.ws is None or self.ws.numel() < need:
             self.ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+        self.lens += self.live
+        torch.sub(self.lens, 1, out=self.slot)            # -1 for those that have ended
+        try:
+            self._append(append, grow)
+        except Exception:
+            self.lens -= self.live
+            raise
         if ids is not None:
             flat = ids.view(requests, -1)
             B.idx_topk(p, self.top_k, flat, None, self.ws)
