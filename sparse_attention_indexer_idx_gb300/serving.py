@@ -126,12 +126,20 @@ class PagedCache:
                  index_rot: int = 64, base: float = 10000.0, eps: float = 1e-6, norms: Optional[dict] = None,
                  interleaved: bool = False, dtype=torch.bfloat16, device="cuda", index_dtype=torch.bfloat16):
         """max_len: slots that a request can grow to; n_pages pages of page_size slots
-        for all of them.  norms: float32 weights by name ("q", "k", "index_q",
+        for all of them.  dtype (bfloat16 or float16): of keys, values and queries;
+        index_dtype (bfloat16 or float32): of the indexer's rows.  norms: float32 weights by name ("q", "k", "index_q",
         "index_k") of the rows that are normalised.  index_heads 0: no indexer, every
         step attends to all slots; else to the top_k best and their witnesses.  The
         indexer's keys are read in one piece and stay by request and slot."""
         if not 0 < page_size or not 0 < max_len or n_pages < 0 or (index_heads > 0) != (top_k is not None):
             raise ValueError(f"max_len={max_len}, {n_pages} pages of {page_size}, {index_heads} index heads, top_k={top_k}")
+        self._check_kinds(q_heads, kv_heads, dim, dim if rot is None else rot, dtype, eps)
+        if index_heads:
+            self._check_indexer(index_heads, index_dim, index_rot, index_dtype, top_k)
+        for name, w in (norms or {}).items():
+            n = {"q": dim, "k": dim, "index_q": index_dim, "index_k": index_dim}.get(name)
+            if n is None or tuple(w.shape) != (n,) or w.dtype != torch.float32:
+                raise ValueError(f"norms: {name!r}, {tuple(w.shape)} {w.dtype}")
         z = lambda *s, dt=dtype: torch.zeros(s, dtype=dt, device=device)  # noqa: E731
         self.page_size, self.max_len, self.cols = page_size, max_len, -(-max_len // page_size)
         self.k, self.v = z(n_pages, page_size, kv_heads, dim), z(n_pages, page_size, kv_heads, dim)
@@ -155,6 +163,30 @@ class PagedCache:
             self.key_off = torch.arange(requests, dtype=torch.int64, device=device) * slots
             self.ids = z(requests, 1, top_k, dt=torch.int32)
         self.ws: Optional[torch.Tensor] = None
+
+    # What every step would be refused for: head rows, attention and the indexer each
+    # take less than all sizes and types.
+    @staticmethod
+    def _check_kinds(q_heads, kv_heads, dim, rot, dtype, eps):
+        if kv_heads < 1 or q_heads < 1 or q_heads % kv_heads or dim not in (64, 128):
+            raise ValueError(f"{q_heads} query heads over {kv_heads} KV heads of {dim} (64 or 128)")
+        if not 0 <= rot <= dim or rot % 16:
+            raise ValueError(f"rot={rot}: a multiple of 16, at most {dim}")
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError(f"dtype {dtype} (bfloat16 or float16)")
+        if not 0 <= eps < float("inf"):
+            raise ValueError(f"eps={eps}")
+
+    @staticmethod
+    def _check_indexer(heads, dim, rot, dtype, top_k):
+        if not 0 < heads <= 128 or dim not in (32, 64, 128, 256) or heads * dim > 16384:
+            raise ValueError(f"{heads} index heads of {dim}: at most 128, and 16384 elements, of 32, 64, 128 or 256")
+        if not 0 <= rot <= dim or rot % 16:
+            raise ValueError(f"index_rot={rot}: a multiple of 16, at most {dim}")
+        if dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError(f"index_dtype {dtype} (bfloat16 or float32)")
+        if not 0 < top_k <= B.IDX_MAX_K:
+            raise ValueError(f"top_k={top_k} outside [1, {B.IDX_MAX_K}]")
 
     def _take(self, grow: dict) -> dict:
         """Pages for the requests (index -> length), all of them or none.  Returns how

@@ -168,3 +168,28 @@ def test_a_refused_prompt_takes_no_pages(calls, bad):
         with pytest.raises(ValueError):
             c.prompt(b, t["k"], t["v"], t["index_k"])
         assert state(c) == before and calls == []
+
+
+@pytest.mark.parametrize("kw", [
+    dict(index_dtype=torch.float16), dict(index_dtype=torch.float8_e4m3fn), dict(index_dim=96), dict(index_dim=512),
+    dict(index_heads=129), dict(index_heads=128, index_dim=256), dict(index_rot=24), dict(index_dim=32, index_rot=64),
+    dict(top_k=0), dict(top_k=B.IDX_MAX_K + 1), dict(dtype=torch.float32), dict(rot=72), dict(rot=-16), dict(rot=24),
+    dict(eps=-1.0), dict(eps=float("nan")), dict(norms={"q": torch.ones(DIM + 1)}), dict(norms={"key": torch.ones(DIM)}),
+    dict(norms={"index_q": torch.ones(DIM)})])
+def test_a_cache_that_no_step_could_use_is_refused(kw):
+    kw = dict(dict(index_heads=IH, index_dim=ID, top_k=TOP), **kw)
+    with pytest.raises(ValueError):
+        serving.PagedCache(REQUESTS, 20, 8, 4, QH, KH, DIM, device="cpu", **kw)
+
+
+@pytest.mark.parametrize("q_heads,kv_heads,dim", [(5, 2, 64), (4, 0, 64), (0, 2, 64), (4, 2, 96), (4, 2, 256)])
+def test_heads_that_attention_does_not_have_are_refused(q_heads, kv_heads, dim):
+    with pytest.raises(ValueError):
+        serving.PagedCache(REQUESTS, 20, 8, 4, q_heads, kv_heads, dim, device="cpu")
+
+
+def test_caches_of_every_kind_that_steps_can_use():
+    for kw in (dict(dtype=torch.float16, rot=0), dict(rot=32, index_heads=3, top_k=1, index_dim=32, index_rot=32),
+               dict(index_heads=64, top_k=B.IDX_MAX_K, index_dim=256, index_rot=0, index_dtype=torch.float32),
+               dict(norms={n: torch.ones(DIM) for n in ("q", "k")}, eps=0.0)):
+        serving.PagedCache(REQUESTS, 20, 8, 4, QH, KH, DIM, device="cpu", **kw)
