@@ -611,6 +611,8 @@ class _Described:
                 strided.append((t, t.data_ptr(), t.shape, t.dtype, t.stride()))
         use = (ctypes.byref(c), self._device(), self._shapes(c))
         views = tuple(self._views())
+        devices = {t.device for t in (*views, *self._tensors())}
+        _need(len(devices) <= 1, f"tensors on more than one device: {sorted(map(str, devices))}")
         self.__dict__["_desc"] = (use, dense, strided, views, list(map(_data_ptr, views)))
         return use
 
@@ -1009,6 +1011,9 @@ def attn_paged(p: PagedAttnProblem, out: torch.Tensor, lse: Optional[torch.Tenso
     """out [B, T, Hq, D]; lse [B, T, Hq] float32 or None; ws of
     attn_paged_workspace_size bytes (None where that is 0)."""
     ref, device, (so, dt, sl) = p.desc()
+    for t in (out, lse, ws):
+        if t is not None and t.device.index != device:
+            raise ValueError(f"out, lse or ws: on {t.device}, another device than the queries")
     po = _out(out, "out", so, dt)
     pl = None if lse is None else _out(lse, "lse", sl, torch.float32)
     pw, nw = None, 0
