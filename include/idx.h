@@ -611,7 +611,8 @@ idx_status rope_heads(const heads_problem* p, void* stream);
 idx_status paged_append(const heads_problem* p, void* stream);
 
 /* Angles per position (radians; both arrays on the host) as 64-bit fractions of a
- * turn: out[i] = inv_freq[i] / 2 pi modulo 1, times 2^64. */
+ * turn: out[i] = inv_freq[i] / 2 pi modulo 1, times 2^64, to the nearest for up to
+ * 2^32 radians. */
 idx_status rope_frequencies(const double* inv_freq, int32_t n, uint64_t* out);
 
 /* --------------------------------------------------------------- attn_paged

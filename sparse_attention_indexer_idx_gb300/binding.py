@@ -799,7 +799,7 @@ def rope_frequencies(rot: int, base: float = 10000.0, inv_freq: Optional[Sequenc
                      device="cuda") -> torch.Tensor:
     """The frequencies of a rotation of `rot` dims, int64 [rot / 2] on the device, as
     HeadPlane takes them: base ** (-2 i / rot) radians per position, or inv_freq
-    (rot / 2 values, scaled as the model has it)."""
+    (rot / 2 values, scaled as the model has it), as the doubles that they are."""
     f = [base ** (-2.0 * i / rot) for i in range(rot // 2)] if inv_freq is None else [float(x) for x in inv_freq]
     _need(len(f) * 2 == rot, f"inv_freq: {len(f)} frequencies for {rot} dims")
     out = (ctypes.c_uint64 * len(f))()

@@ -20,6 +20,8 @@ BUILD = os.path.join(ROOT, "_build", "libidx")
 LIB = os.path.join(PKG, "libidx.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
+         # the host's sums are the same on machines that would contract them
+         "-Xcompiler", "-ffp-contract=off",
          "--expt-relaxed-constexpr", "-rdc=false", "-I", os.path.join(ROOT, "include")]
 
 

@@ -593,10 +593,20 @@ idx_status rope_frequencies(const double* inv_freq, int32_t n, uint64_t* out) {
   if (n < 0 || (n > 0 && (!inv_freq || !out))) return fail(IDX_ERR_INVALID_ARG, "n=%d, or a NULL pointer", n);
   for (int i = 0; i < n; i++)
     if (!std::isfinite(inv_freq[i])) return fail(IDX_ERR_INVALID_ARG, "inv_freq[%d] is not finite", i);
+  // 1 / 2 pi in two doubles, and the product's lower half by fma: some 106 bits, as a
+  // word of 53 would be off by 2^-25 turns at the farthest positions.
+  constexpr double hi = 0.15915494309189535, lo = -9.839338337591243e-18;
   for (int i = 0; i < n; i++) {
-    double f = inv_freq[i] / 6.283185307179586476925;
-    f -= std::floor(f);
-    out[i] = f < 1.0 ? (uint64_t)std::ldexp(f, 64) : 0;  // (a negative one next to 0 rounds to a whole turn)
+    const double p = inv_freq[i] * hi, e = std::fma(inv_freq[i], hi, -p) + inv_freq[i] * lo;
+    // whole turns go, then whole steps of 2^-64 are taken from both halves; all of it exact
+    uint64_t word = 0;
+    double rest = 0;
+    for (const double part : {p, e}) {
+      const double steps = std::ldexp(part - std::trunc(part), 64), whole = std::trunc(steps);
+      word += whole < 0 ? -(uint64_t)-whole : (uint64_t)whole;
+      rest += steps - whole;
+    }
+    out[i] = word + (uint64_t)std::llround(rest);
   }
   return IDX_OK;
 }
