@@ -327,7 +327,8 @@ __device__ __forceinline__ bool stream_keys(const PagedArgs& a, const CUtensorMa
       decide();
       issue_boxes(j + 2, 0);
     }
-    // Scores in units of log2, masked, and the running maximum.  A tile that every row
+    // Scores in units of log2, masked, and the running reference of the weights, kLift
+    // below the maximum.  A tile that every row
     // sees whole needs no masks, and its scale goes into the exponent's sum.
     const int c0 = 2 * (lane & 3);
     const unsigned seen = live >> c0;
@@ -342,8 +343,9 @@ __device__ __forceinline__ bool stream_keys(const PagedArgs& a, const CUtensorMa
 #pragma unroll
           for (int e = 0; e < 4; e++) raw[e >> 1] = fmaxf(raw[e >> 1], s[m][i][e]);
 #pragma unroll
-        for (int e = 0; e < 2; e++) top[e] = fmaxf(top[e], raw[e] * a.scale_log2);
+        for (int e = 0; e < 2; e++) top[e] = fmaxf(top[e], fmaf(raw[e], a.scale_log2, -kLift<BF16>));
       } else {
+        float high[2] = {-INFINITY, -INFINITY};
 #pragma unroll
         for (int i = 0; i < NT; i++)
 #pragma unroll
@@ -351,8 +353,10 @@ __device__ __forceinline__ bool stream_keys(const PagedArgs& a, const CUtensorMa
             bool see = seen >> (8 * i + (e & 1)) & 1;
             if (!LIST) see = see && base + 8 * i + c0 + (e & 1) < lim[m][e >> 1];
             s[m][i][e] = see ? s[m][i][e] * a.scale_log2 : -INFINITY;
-            top[e >> 1] = fmaxf(top[e >> 1], s[m][i][e]);
+            high[e >> 1] = fmaxf(high[e >> 1], s[m][i][e]);
           }
+#pragma unroll
+        for (int e = 0; e < 2; e++) top[e] = fmaxf(top[e], high[e] - kLift<BF16>);
       }
       bool grew = false;
       float scl[2];
@@ -398,8 +402,8 @@ __device__ __forceinline__ bool stream_keys(const PagedArgs& a, const CUtensorMa
     }
     // Weights times values.  The weights are rounded to the element type, as the
     // 16-bit operand of the product has to be, one rounding of at most 2^-8 (2^-11
-    // for fp16) of each weight, as large as the output's own; the sum that divides
-    // them is of the unrounded ones, in 32 bits.
+    // for fp16, down to 2^-29 of the largest, below that 2^-40 of it) of each weight, as
+    // large as the output's own; the sum that divides them is of the unrounded ones, in 32 bits.
 #pragma unroll
     for (int kk = 0; kk < KT / 16; kk++) {
       uint32_t pf[MT][4];
@@ -665,7 +669,7 @@ __global__ void __launch_bounds__(32 * kWarps, MT == 1 ? 3 : 2)
     const int64_t id = s_id[r];
     *reinterpret_cast<uint2*>((char*)sh.out + 2 * (id * D + col)) =
         make_uint2(pack2<BF16>(v.x * inv, v.y * inv), pack2<BF16>(v.z * inv, v.w * inv));
-    if (col == 0 && sh.lse) sh.lse[id] = sum != 0.f ? (top + log2f(sum)) * 0.693147180559945309f : -INFINITY;
+    if (col == 0 && sh.lse) sh.lse[id] = sum != 0.f ? log2_sum<BF16>(top, sum) * 0.693147180559945309f : -INFINITY;
   };
   // from the blocks of the cluster, by their ranks: sums, and (maximum, sum) of the
   // weights, of this block's units

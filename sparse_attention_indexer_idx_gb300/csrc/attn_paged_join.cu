@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kThreads) attn_paged_join_kernel(const __grid_
   uint32_t* to = reinterpret_cast<uint32_t*>(out) + (r * D + lane * E) / 2;
 #pragma unroll
   for (int e = 0; e < E / 2; e++) to[e] = pack2<BF16>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-  if (lane == 0 && lse) lse[r] = l != 0.f ? (top + log2f(l)) * 0.693147180559945309f : -INFINITY;
+  if (lane == 0 && lse) lse[r] = l != 0.f ? log2_sum<BF16>(top, l) * 0.693147180559945309f : -INFINITY;
 }
 
 template <int D, bool BF16>

@@ -472,11 +472,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;  // both warps of the pair
         const float top = fmaxf(tops_at[row], tops_at[128 + row]) * c;
         // The reference moves only when a score passes it by more than 2^8 (weights
-        // up to 2^8 lose nothing): the accumulator is almost never rescaled.
-        const bool move = top > m + 8.f;  // also from -inf to the first score
+        // up to 2^8 lose nothing): the accumulator is almost never rescaled.  With fp16
+        // it is set 11 below the maximum and moves at kLift.
+        constexpr float below = BF16 ? 0.f : 11.f, late = BF16 ? 8.f : kLift<BF16>;
+        const bool move = top > m + late;  // also from -inf to the first score
         if (__any_sync(0xffffffffu, move)) {
-          const float to_m = move ? top : m;
-          const float f = move ? attn_ex2(m - top) : 1.f;
+          const float to_m = move ? top - below : m;
+          const float f = move ? attn_ex2(m - to_m) : 1.f;
           m = to_m;
           const uint64_t f2 = f2_pack(f, f), zero = f2_pack(0.f, 0.f);
 #pragma unroll
@@ -504,8 +506,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         // The weights are rounded to the element type, which the 16-bit operand has
-        // to be (in error as much as the output's own rounding); their sum, which
-        // divides the output, is of the unrounded ones.
+        // to be (in error as much as the output's own rounding; fp16 ones below 2^-25 of
+        // the largest by 2^-36 of it); their sum, which divides the output, is of the
+        // unrounded ones.
         const float base = m == -INFINITY ? 0.f : m;
         const uint64_t c2 = f2_pack(c, c), b2 = f2_pack(-base, -base), one = f2_pack(1.f, 1.f);
         uint32_t w[32];
