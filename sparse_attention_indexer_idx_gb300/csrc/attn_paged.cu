@@ -247,6 +247,8 @@ __device__ __forceinline__ bool stream_keys(const PagedArgs& a, const CUtensorMa
 
   // the queries, as operand fragments: row lane / 4 (and 8 on) of a 16-row tile,
   // pairs of dims 2 (lane % 4) (and 8 on)
+  const float c = scale_of(a);
+  const uint32_t flip = flip_of(a);
   uint32_t qf[MT][KS][4];
   int lim[MT][2];
   // what the row that sees least sees (of the ones that there are)
@@ -262,8 +264,8 @@ __device__ __forceinline__ bool stream_keys(const PagedArgs& a, const CUtensorMa
       const uint32_t* q = reinterpret_cast<const uint32_t*>((const char*)p.q + 2 * q_at) + (lane & 3);
 #pragma unroll
       for (int ks = 0; ks < KS; ks++) {
-        qf[m][ks][e] = r.id[m][e] >= 0 ? __ldg(q + 8 * ks) : 0u;
-        qf[m][ks][e + 2] = r.id[m][e] >= 0 ? __ldg(q + 8 * ks + 4) : 0u;
+        qf[m][ks][e] = r.id[m][e] >= 0 ? __ldg(q + 8 * ks) ^ flip : 0u;
+        qf[m][ks][e + 2] = r.id[m][e] >= 0 ? __ldg(q + 8 * ks + 4) ^ flip : 0u;
       }
     }
 #pragma unroll
@@ -327,37 +329,28 @@ __device__ __forceinline__ bool stream_keys(const PagedArgs& a, const CUtensorMa
       decide();
       issue_boxes(j + 2, 0);
     }
-    // Scores in units of log2, masked, and the running reference of the weights, kLift
-    // below the maximum.  A tile that every row
-    // sees whole needs no masks, and its scale goes into the exponent's sum.
+    // Scores, masked, and the running maximum.  A tile that every row sees whole needs
+    // no masks.
     const int c0 = 2 * (lane & 3);
     const unsigned seen = live >> c0;
-    const bool whole = live == C::FULL && a.scale_log2 > 0.f && (LIST || base + KT <= least);
+    const bool whole = live == C::FULL && (LIST || base + KT <= least);
 #pragma unroll
     for (int m = 0; m < MT; m++) {
       float top[2] = {r.mx[m][0], r.mx[m][1]};
-      if (whole) {
-        float raw[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-        for (int i = 0; i < NT; i++)
-#pragma unroll
-          for (int e = 0; e < 4; e++) raw[e >> 1] = fmaxf(raw[e >> 1], s[m][i][e]);
-#pragma unroll
-        for (int e = 0; e < 2; e++) top[e] = fmaxf(top[e], fmaf(raw[e], a.scale_log2, -kLift<BF16>));
-      } else {
-        float high[2] = {-INFINITY, -INFINITY};
+      if (!whole) {
 #pragma unroll
         for (int i = 0; i < NT; i++)
 #pragma unroll
           for (int e = 0; e < 4; e++) {
             bool see = seen >> (8 * i + (e & 1)) & 1;
             if (!LIST) see = see && base + 8 * i + c0 + (e & 1) < lim[m][e >> 1];
-            s[m][i][e] = see ? s[m][i][e] * a.scale_log2 : -INFINITY;
-            high[e >> 1] = fmaxf(high[e >> 1], s[m][i][e]);
+            if (!see) s[m][i][e] = -INFINITY;
           }
-#pragma unroll
-        for (int e = 0; e < 2; e++) top[e] = fmaxf(top[e], high[e] - kLift<BF16>);
       }
+#pragma unroll
+      for (int i = 0; i < NT; i++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) top[e >> 1] = fmaxf(top[e >> 1], s[m][i][e]);
       bool grew = false;
       float scl[2];
 #pragma unroll
@@ -365,7 +358,7 @@ __device__ __forceinline__ bool stream_keys(const PagedArgs& a, const CUtensorMa
         top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
         top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
         const float x = top[e] == -INFINITY ? 0.f : top[e];
-        scl[e] = attn_ex2(r.mx[m][e] - x);  // 0 for a first maximum, 1 where it stays
+        scl[e] = attn_ex2((r.mx[m][e] - x) * c);  // 0 for a first maximum, 1 where it stays
         grew |= top[e] != r.mx[m][e];
         r.mx[m][e] = top[e];
         top[e] = x;
@@ -378,11 +371,13 @@ __device__ __forceinline__ bool stream_keys(const PagedArgs& a, const CUtensorMa
 #pragma unroll
           for (int e = 0; e < 4; e++) r.o[m][i][e] *= scl[e >> 1];
       }
+      // (the maximum is subtracted before the scale: c s - c m in one fma is not 0 for
+      // the largest score but half a step of c m, and infinite from 2^31 on)
 #pragma unroll
       for (int i = 0; i < NT; i++)
 #pragma unroll
         for (int e = 0; e < 4; e++) {
-          s[m][i][e] = attn_ex2(fmaf(s[m][i][e], whole ? a.scale_log2 : 1.f, -top[e >> 1]));
+          s[m][i][e] = attn_ex2(fmaf(s[m][i][e] - top[e >> 1], c, kLift<BF16>));
           r.sum[m][e >> 1] += s[m][i][e];
         }
     }
@@ -440,6 +435,7 @@ __device__ __forceinline__ bool stream_keys(const PagedArgs& a, const CUtensorMa
   for (int m = 0; m < MT; m++)
 #pragma unroll
     for (int e = 0; e < 2; e++) {
+      r.mx[m][e] *= c;  // in log2 units
       r.sum[m][e] += __shfl_xor_sync(0xffffffffu, r.sum[m][e], 1);
       r.sum[m][e] += __shfl_xor_sync(0xffffffffu, r.sum[m][e], 2);
     }

@@ -45,18 +45,23 @@ __device__ __forceinline__ int units_of(const paged_problem& p, int b, int shift
   return n <= p.max_len ? max(1, (n + (1 << shift) - 1) >> shift) : 1;
 }
 
-// Weights are 2^(y - m) for a reference m that lies below the running maximum, by
-// kLift or less: as 16-bit floats they reach down to 2^-14 before they lose bits, up
-// to 2^16 at most, and sums, outputs and the join's factors scale alike.  bf16 has
-// fp32's range and needs none of it.  (Without it, fp16 weights below 2^-25 of a
-// warp's largest were 0 in the product and yet in the sum that divides it: 4 % of a
+// The scale of the exponents, above zero: a negative one's sign goes into the queries
+// (flip), and a scale of zero becomes one that takes every score to zero but leaves
+// -inf alone.
+__device__ __forceinline__ float scale_of(const PagedArgs& a) { return fmaxf(fabsf(a.scale_log2), 0x1p-149f); }
+__device__ __forceinline__ uint32_t flip_of(const PagedArgs& a) { return a.scale_log2 < 0.f ? 0x80008000u : 0u; }
+
+// Weights are lifted, 2^(y - m + kLift): as fp16 they reach down to 2^-14 before they
+// lose bits, up to 2^16 at most, and sums, outputs and the join's factors scale alike.
+// bf16 has fp32's range and needs none of it.  (Without it, fp16 weights below 2^-25 of
+// a warp's largest were 0 in the product and yet in the sum that divides it: 4 % of a
 // row of 30,000 weights of 2^-27 got lost.)
 template <bool BF16>
 constexpr float kLift = BF16 ? 0.f : 15.f;
-// log2 of the sum, which is 2^kLift times as large as it was, so that no bits go to that.
+// lse in log2 units, from a maximum and a sum of lifted weights.
 template <bool BF16>
 __device__ __forceinline__ float log2_sum(float m, float sum) {
-  return m + kLift<BF16> + log2f(sum * (BF16 ? 1.f : 0x1p-15f));
+  return m + log2f(sum * (BF16 ? 1.f : 0x1p-15f));
 }
 
 // Rows beyond 16 over long caches, on the 5th-generation tensor cores.

@@ -335,10 +335,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool idle = pair * 32 >= nrow;  // no row of the warp is there: its lanes of P hold anything
     const uint32_t lane_off = (uint32_t)(pair * 32) << 16;
     const uint32_t to = tmem + lane_off + 256 + wg * (D / 2);  // this half of the columns' sums
-    // 2^(c s - m): a negative scale goes into the queries' sign, and a scale of
-    // zero becomes one that takes every score to zero but leaves -inf alone
-    const float c = fmaxf(fabsf(a.scale_log2), 1e-37f);
-    const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
+    const float c = scale_of(a);
+    const uint32_t flip = flip_of(a);
     uint32_t ns0 = 0, ns1 = 0, no = 0, npv = 0, cnt = 0;  // uses of the barriers; tiles
     bool ok = true;
     const bool live = row < nrow;
@@ -474,10 +472,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The reference moves only when a score passes it by more than 2^8 (weights
         // up to 2^8 lose nothing): the accumulator is almost never rescaled.  With fp16
         // it is set 11 below the maximum and moves at kLift.
-        constexpr float below = BF16 ? 0.f : 11.f, late = BF16 ? 8.f : kLift<BF16>;
-        const bool move = top > m + late;  // also from -inf to the first score
+        //   Steep scores, from 2^20 in log2 units on, leave this no room: 2^(c s - m) with c
+        // s unrounded, in one fma, is 2^(half the last bit of m) for the largest score,
+        // and infinite from 2^31 on.  They are multiplied first, so that the largest is
+        // met exactly, and their reference is the maximum itself.
+        constexpr float kSteep = 0x1p20f, below = BF16 ? 0.f : 11.f, late = BF16 ? 8.f : kLift<BF16>;
+        const bool move = top > m + (fabsf(top) >= kSteep ? 0.f : late);  // also from -inf to the first score
         if (__any_sync(0xffffffffu, move)) {
-          const float to_m = move ? top - below : m;
+          const float to_m = !move ? m : fabsf(top) >= kSteep ? top : top - below;
           const float f = move ? attn_ex2(m - to_m) : 1.f;
           m = to_m;
           const uint64_t f2 = f2_pack(f, f), zero = f2_pack(0.f, 0.f);
@@ -510,7 +512,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the largest by 2^-36 of it); their sum, which divides the output, is of the
         // unrounded ones.
         const float base = m == -INFINITY ? 0.f : m;
-        const uint64_t c2 = f2_pack(c, c), b2 = f2_pack(-base, -base), one = f2_pack(1.f, 1.f);
+        const bool steep = __any_sync(0xffffffffu, fabsf(base) >= kSteep);
+        const float cs = steep ? 1.f : c;
+        if (steep)
+#pragma unroll
+          for (int e = 0; e < 64; e++) s[e / 32][e % 32] = __float_as_uint(__uint_as_float(s[e / 32][e % 32]) * c);
+        const uint64_t c2 = f2_pack(cs, cs), b2 = f2_pack(-base, -base), one = f2_pack(1.f, 1.f);
         uint32_t w[32];
 #pragma unroll
         for (int e = 0; e < 32; e++) {
@@ -551,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         sums_at[128 * wg + row] = l;
         pair_sync(pair);
         l = sums_at[row] + sums_at[128 + row];
-        if (live && wg == 0) a.pml[at] = make_float2(l != 0.f ? m : -INFINITY, l);
+        if (live && wg == 0) a.pml[at] = make_float2(l != 0.f ? m + kLift<BF16> : -INFINITY, l);
         // the sums leave through 2 KB of the warp's own, 16 columns at a time, so that
         // four lanes write 64 bytes of a row next to one another
         uint8_t* stage = smem + (1 + C::NS) * C::TILE + (warp - 4) * 2048;

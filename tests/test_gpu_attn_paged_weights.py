@@ -30,13 +30,13 @@ KINDS = {
 }
 
 
-def exact_rows(kind, dtype, score, values):
-    """A call whose slot s has the score `score(s)` (in units of log2) and values of
+def exact_rows(kind, dtype, score, values, scale=math.log(2)):
+    """A call whose slot s has the score `score(s)` (in units of the scale) and values of
     `values(s)` in every row; and what each row has to be."""
     kw = KINDS[kind]
     n, W = kw["S"], kw.get("W", 0)
     t = make(7, dtype=dtype, lens=[n] * kw["B"], **kw)
-    t["scale"] = math.log(2)
+    t["scale"] = scale
     t["q"] = torch.zeros_like(t["q"])
     t["q"][..., 0] = 1
     s = torch.arange(n, device="cuda")
@@ -51,9 +51,9 @@ def exact_rows(kind, dtype, score, values):
         t["ids"] = torch.arange(W, dtype=torch.int32, device="cuda").expand(kw["B"], kw["T"], W).contiguous()
         see[..., W:] = False
     see &= s < torch.arange(n - kw["T"] + 1, n + 1, device="cuda").view(1, -1, 1)
-    y = torch.where(see, x.double() * math.log(2), -math.inf)
+    y = torch.where(see, x.double() * scale, -math.inf)
     lse = torch.logsumexp(y, -1)
-    w = torch.exp(y - lse.unsqueeze(-1))
+    w = torch.softmax(y, -1)             # (of differences: a steep row's lse has no bits left for its count)
     return t, (w @ v.double()).unsqueeze(-1), (w @ v.abs().double()).unsqueeze(-1), lse.unsqueeze(-1), int(see.sum(-1).max())
 
 
@@ -73,4 +73,29 @@ def test_many_small_weights(B, kind, dtype, low):  # noqa: F811
     err = (out.double() - want).abs()
     assert (err <= tol).all(), (err / tol).max().item()
     assert ((l.double() - lse).abs() <= 2.0 ** -20 * (1 + lse.abs())).all()
+    assert B.device_error() == 0
+
+
+@pytest.mark.parametrize("dtype,steep", [("bf16", 2), ("bf16", 19), ("bf16", 24), ("bf16", 31), ("bf16", 40), ("bf16", 90),
+                                         ("f16", 19), ("f16", 20), ("f16", 24), ("f16", 28), ("f16", 40)])
+@pytest.mark.parametrize("kind", KINDS)
+def test_steep_scores_keep_to_the_largest(B, kind, dtype, steep):  # noqa: F811
+    """Scores of 2^steep and more, as far apart, of either sign and rising along the
+    cache: a row is the average of the slots that share its largest one."""
+    u = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -11
+    scores = {
+        "above zero": lambda s: 3 - (s * 7 % 9) / 4,
+        "below zero": lambda s: -2 - (s * 5 % 7) / 8,
+        "rising": lambda s: 1 + s.float().mul(60 / len(s)).floor() / 4 - 8,
+    }
+    for name, score in scores.items():
+        t, want, absv, lse, n = exact_rows(kind, dtype, lambda s: score(s).float(), lambda s: 1.0 + (s % 8) / 8,
+                                           scale=2.0 ** steep)
+        out, l, _, _ = run(B, t)
+        # (scores are off by 2^-23 of themselves at most, equal ones alike)
+        near = 2.0 ** steep * 16 * 2.0 ** -23 if steep < 10 else 0
+        want, tol = (x.unsqueeze(-1).expand(out.shape) for x in (want, absv * (2.2 * u + 2.0 ** -17 + near)))
+        err = (out.double() - want).abs()
+        assert (err <= tol).all(), (name, (err / tol).max().item())
+        assert ((l.double() - lse).abs() <= 2.0 ** -20 * (1 + lse.abs())).all(), name
     assert B.device_error() == 0
