@@ -611,8 +611,9 @@ class _Described:
                 strided.append((t, t.data_ptr(), t.shape, t.dtype, t.stride()))
         use = (ctypes.byref(c), self._device(), self._shapes(c))
         views = tuple(self._views())
-        devices = {t.device for t in (*views, *self._tensors())}
-        _need(len(devices) <= 1, f"tensors on more than one device: {sorted(map(str, devices))}")
+        devices = {t.get_device() for t in (*views, *self._tensors())}
+        if len(devices) > 1:
+            raise ValueError(f"tensors on more than one device: {sorted(map(str, devices))}")
         self.__dict__["_desc"] = (use, dense, strided, views, list(map(_data_ptr, views)))
         return use
 
@@ -1006,20 +1007,25 @@ def attn_paged_workspace_size(p: PagedAttnProblem) -> int:
     return int(lib().attn_paged_workspace_size(p.desc()[0]))
 
 
+def _out_on(t: torch.Tensor, name: str, shape, dtype, device):
+    """_out on that device."""
+    if t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.get_device() == device:
+        return t.data_ptr()
+    _need(not t.is_cuda or t.get_device() == device, f"{name}: not on the queries' device")
+    return _dense(t, name, (tuple(shape),), dtype)
+
+
 def attn_paged(p: PagedAttnProblem, out: torch.Tensor, lse: Optional[torch.Tensor] = None,
                ws: Optional[torch.Tensor] = None, stream=None):
     """out [B, T, Hq, D]; lse [B, T, Hq] float32 or None; ws of
     attn_paged_workspace_size bytes (None where that is 0)."""
     ref, device, (so, dt, sl) = p.desc()
-    for t in (out, lse, ws):
-        if t is not None and t.device.index != device:
-            raise ValueError(f"out, lse or ws: on {t.device}, another device than the queries")
-    po = _out(out, "out", so, dt)
-    pl = None if lse is None else _out(lse, "lse", sl, torch.float32)
+    po = _out_on(out, "out", so, dt, device)
+    pl = None if lse is None else _out_on(lse, "lse", sl, torch.float32, device)
     pw, nw = None, 0
     if ws is not None:
-        if not (ws.is_cuda and ws.is_contiguous()):
-            raise ValueError("ws: expected a contiguous CUDA tensor")
+        if not (ws.get_device() == device and ws.is_contiguous()):
+            raise ValueError("ws: expected a contiguous tensor on the queries' device")
         pw, nw = ws.data_ptr(), ws.nbytes
     st = (_lib or lib()).attn_paged(ref, po, pl, pw, nw, _raw_stream(device, stream))
     if st:

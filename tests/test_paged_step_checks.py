@@ -13,6 +13,9 @@ REQUESTS, QH, KH, DIM, IH, ID, TOP = 3, 4, 2, 64, 16, 128, 8
 class OnGpu(torch.Tensor):
     is_cuda = True
 
+    def get_device(self):
+        return self.device.index
+
 
 def gpu(*shape, dtype=torch.bfloat16):
     return torch.zeros(shape, dtype=dtype).as_subclass(OnGpu)
