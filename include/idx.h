@@ -559,9 +559,9 @@ idx_status cache_evict(const evict_problem* p, int32_t* out_src, int32_t* out_le
  *   for i < rot / 2 the pair (a, b) = (y[i], y[i + rot/2]), or (y[2i], y[2i + 1])
  *   with interleaved, becomes (a cos t - b sin t, b cos t + a sin t),
  *   t = position * (frequency i); dims from rot on stay y.
- * All of it is fp32 (a row whose sum of squares is above fp32's range gives 0),
- * rounded once to the plane's type; the angle is exact to 2^-31 turns at any
- * position.  A plane without norm and with rot 0 is copied bit for bit.
+ * All of it is fp32 (a row whose sum of squares is above fp32's range gives 0,
+ * squares below it count as 0), rounded once to the plane's type; the angle is exact
+ * to 2^-31 turns at any position.  A plane without norm and with rot 0 is copied bit for bit.
  *
  *   src     device rows, element strides for token and head; the last dimension
  *           is contiguous.  dst may be src itself (same strides, no table).
@@ -622,9 +622,10 @@ idx_status rope_frequencies(const double* inv_freq, int32_t n, uint64_t* out);
  * slot s is slot s % page_size of page table[b, s / page_size] of the pools.  x =
  * scale q.k, lse = log sum exp(x), out = sum exp(x - lse) v, as in attn_shared: a
  * row with no visible key gets out 0 and lse -inf; sums, maxima and scores are
- * fp32, the weights are rounded to the element type for the product with v.  Each
- * row's sums are taken in an order that the sizes and lengths alone decide, so a
- * repeated call gives the same bits.
+ * fp32, the weights are rounded to the element type for the product with v (fp16 ones
+ * lifted by 2^11 or more, so that small ones keep their bits: below 2^-25 of a row's
+ * largest they are off by 2^-36 of it at most).  Each row's sums are taken in an order
+ * that the sizes and lengths alone decide, so a repeated call gives the same bits.
  *
  *   q           device [B, T, Hq, D], IDX_BF16 or IDX_F16, D 64 or 128 contiguous;
  *               strides (in elements) for b, t and head.

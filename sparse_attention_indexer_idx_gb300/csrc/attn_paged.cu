@@ -33,10 +33,10 @@
 // lie next to one another, are read together.
 //
 // Measured, with keys and values of 128 in bf16, 8 KV heads: 16 caches of 25,100 slots
-// on average (1.6 GB) 252 us, 6.5 TB/s; one of 524,288 325 us, 6.6 TB/s; 32 of 2,900 68
+// on average (1.6 GB) 256 us, 6.4 TB/s; one of 524,288 331 us, 6.5 TB/s; 32 of 2,900 68
 // us, 5.7 TB/s; 64 x 4 lists of 2,048 slots 55 us, 4.9 TB/s: rows of 256 bytes in no
-// order.  Row by row instead of in boxes the first took 265 us, and 16 requests of 4
-// tokens with heads of 64 34 us instead of 22.
+// order.  Row by row (pages of 4 slots) instead of in boxes the first takes as long, and
+// 16 requests of 4 tokens with heads of 64 15.5 us instead of 14.6.
 #include <algorithm>
 
 #include "attn_mma.cuh"
@@ -810,16 +810,15 @@ constexpr int kOneBlock = 116 << 10, kTwoBlocks = 78 << 10;
 
 // Row tiles of all KV heads and sequences.
 int64_t short_items(const paged_problem& p) {
-  const int64_t rows = (p.ids ? 1 : p.T) * (int64_t)(p.Hq / p.n_kv);
-  return (int64_t)p.B * (p.ids ? p.T : 1) * p.n_kv * ceil_div(rows, row_tile(p));
+  return (int64_t)p.B * (p.ids ? p.T : 1) * p.n_kv * ceil_div(rows_of(p), row_tile(p));
 }
 
 // Blocks of a cluster for a short call, 0: a long one.  An SM holds three blocks,
 // two where more than 16 rows ask for registers, or more than 8 of 128 for room in shared
 // memory (12 warps of 16 rows are no faster than 8, but for long calls).  A
 // cluster stays within a part of the GPU, whose SMs it need not use up, so of the blocks
-// that there is room for 0.95 or more run at once in clusters of up to 5, 0.89 in 6 to
-// 12 (even numbers) and 0.73 in 16 (4 requests of 4 KV heads of 32 rows of 64 over 6,000
+// that there is room for 0.95 or more run at once in clusters of up to 5, 0.89 or more in
+// 6, 8, 10 and 12 and 0.73 in 16, as the runtime says for two and for three blocks an SM (4 requests of 4 KV heads of 32 rows of 64 over 6,000
 // slots took 17 us in 16 clusters of 16, 13 in 16 of 8).  Powers of two alone left up to
 // half of the room empty: 16 requests of 4 heads over 4,000 slots 29 us instead of 23.
 int short_blocks(const paged_problem& p) {
@@ -998,7 +997,7 @@ idx_status launch_attn_paged(const paged_problem& p, void* out, float* lse, void
   if (!fits(p)) return IDX_ERR_UNSUPPORTED;
   PagedArgs a = make_args(p);
   if (const int blocks = short_blocks(p)) {
-    const int64_t rows = std::min<int64_t>(row_tile(p), (p.ids ? 1 : p.T) * (int64_t)a.G);
+    const int64_t rows = std::min<int64_t>(row_tile(p), rows_of(p));
     const Short sh{blocks, (int)ceil_div(rows * p.D / 4, blocks), out, lse};
     *err = launch(a, nullptr, &sh, st);
     return *err == cudaSuccess ? IDX_OK : IDX_ERR_CUDA;

@@ -16,9 +16,9 @@
 // streaming kernel do, and leave partial results for the join.
 //
 // Measured, with heads of 128 in bf16 and 8 KV heads: 16 requests of 8 tokens and 8 heads
-// a KV head over 25,100 slots 246 us (243 at the copy rate; the streaming kernel 543); 8
-// of 8 tokens and 16 heads over 12,800 81 us (62; 289); 4 of one KV head over 81,250 43
-// us (24; 150).  What is left is a block's start and the end of its runs, about 9 us,
+// a KV head over 25,100 slots 247 us (243 at the copy rate; the streaming kernel 543); 8
+// of 8 tokens and 16 heads over 12,800 81 us (62; 289); 4 of one KV head over 81,250 45
+// us (26; 150).  What is left is a block's start and the end of its runs, about 9 us,
 // and where the rows fill the 128 the exponentials: two threads a row take 1 us for 128
 // keys, one thread took 1.3.
 //
