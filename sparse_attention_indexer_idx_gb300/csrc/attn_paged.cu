@@ -818,9 +818,10 @@ int64_t short_items(const paged_problem& p) {
 // memory (12 warps of 16 rows are no faster than 8, but for long calls).  A
 // cluster stays within a part of the GPU, whose SMs it need not use up, so of the blocks
 // that there is room for 0.95 or more run at once in clusters of up to 5, 0.89 or more in
-// 6, 8, 10 and 12 and 0.73 in 16, as the runtime says for two and for three blocks an SM (4 requests of 4 KV heads of 32 rows of 64 over 6,000
-// slots took 17 us in 16 clusters of 16, 13 in 16 of 8).  Powers of two alone left up to
-// half of the room empty: 16 requests of 4 heads over 4,000 slots 29 us instead of 23.
+// 6, 8, 10 and 12 and 0.73 in 16, as the runtime says for two and for three blocks an SM
+// (4 requests of 4 KV heads of 32 rows of 64 over 6,000 slots took 17 us in 16 clusters
+// of 16, 13 in 16 of 8).  Powers of two alone left up to half of the room empty: 16
+// requests of 4 heads over 4,000 slots 29 us instead of 23.
 int short_blocks(const paged_problem& p) {
   const int64_t items = short_items(p), room = (rows_of(p) <= (p.D == 64 ? 16 : 8) ? 3 : 2) * (int64_t)sm_count();
   const int64_t tiles = std::max<int64_t>(1, ceil_div(keys_of(p), stream_tile(p.D)));

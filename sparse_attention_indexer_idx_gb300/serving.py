@@ -127,10 +127,11 @@ class PagedCache:
                  interleaved: bool = False, dtype=torch.bfloat16, device="cuda", index_dtype=torch.bfloat16):
         """max_len: slots that a request can grow to; n_pages pages of page_size slots
         for all of them.  dtype (bfloat16 or float16): of keys, values and queries;
-        index_dtype (bfloat16 or float32): of the indexer's rows.  norms: float32 weights by name ("q", "k", "index_q",
-        "index_k") of the rows that are normalised.  index_heads 0: no indexer, every
-        step attends to all slots; else to the top_k best and their witnesses.  The
-        indexer's keys are read in one piece and stay by request and slot."""
+        index_dtype (bfloat16 or float32): of the indexer's rows.  norms: float32 weights
+        by name ("q", "k", "index_q", "index_k") of the rows that are normalised.
+        index_heads 0: no indexer, every step attends to all slots; else to the top_k best
+        and their witnesses.  The indexer's keys are read in one piece and stay by request
+        and slot."""
         if not 0 < page_size or not 0 < max_len or n_pages < 0 or (index_heads > 0) != (top_k is not None):
             raise ValueError(f"max_len={max_len}, {n_pages} pages of {page_size}, {index_heads} index heads, top_k={top_k}")
         self._check_kinds(q_heads, kv_heads, dim, dim if rot is None else rot, dtype, eps)
